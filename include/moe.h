@@ -305,6 +305,51 @@ moe_status_t moe_expert_fc2_mxfp8(const moe_config_t* cfg, const uint8_t* a_q,
                                   const uint8_t* w2_q, const uint8_t* w2_sf, void* y_perm,
                                   moe_stream_t stream);
 
+/* ---- MXFP4 expert GEMMs (review §5.3, the low-precision recipes) -------------
+ * The 4-bit microscaled format: 1 x 32 blocks along the GEMM's K dimension, each
+ * block one E8M0 scale, elements FP4 E2M1 (OCP Microscaling v1.0: X =
+ * floor(log2 max|x|) - 2, element = x / 2^X rounded to nearest even among
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and saturated to +-6; an all-zero block takes
+ * X = -127).  A block that holds an infinity or a NaN gets the NaN scale
+ * (255) and stands for NaNs.  The GEMMs run as block-scaled tensor-core MMAs
+ * with fp32 accumulation.  Forward only, SwiGLU experts without biases.
+ *
+ * MXFP4 tensor format: codes [rows, K/2] uint8, two columns a byte (the even
+ * column in bits 0-3; a code is sign << 3 | exponent << 1 | mantissa), and the
+ * scale buffer of the MXFP8 format (moe_mxfp8_scale_bytes(rows, K, groups)
+ * bytes, the same atoms).  K must be a multiple of 128.
+ *
+ * Errors: as for MXFP8. */
+
+/* Quantise x [rows, K] bf16 (device) to MXFP4: codes q [rows, K/2] and scales
+ * sf.  offsets and groups as in moe_mxfp8_quantize (rows outside every group
+ * get codes but no scales).  Deterministic and exact: the decisions depend
+ * only on the bf16 values. */
+moe_status_t moe_mxfp4_quantize(int64_t rows, int32_t K, int32_t groups, const int32_t* offsets,
+                                const void* x, uint8_t* q, uint8_t* sf, moe_stream_t stream);
+
+/* The values of an MXFP4 tensor: x [rows, K] bf16 out, exact (every value of
+ * the format is a bf16 number, except those above bf16's largest finite number
+ * with scale codes above 252, which become infinities).  Rows outside every
+ * group are left as they were. */
+moe_status_t moe_mxfp4_dequantize(int64_t rows, int32_t K, int32_t groups, const int32_t* offsets,
+                                  const uint8_t* q, const uint8_t* sf, void* x,
+                                  moe_stream_t stream);
+
+/* moe_expert_fc1_mxfp8 and moe_expert_fc2_mxfp8 on MXFP4 operands: the same
+ * arguments with codes of half the bytes (x_q [P, h/2], w1_q [E*2F, h/2],
+ * a_q [P, F/2], w2_q [E*h, F/2]).  FC1 writes a (bf16), its MXFP4 form
+ * (quantised from fp32), or both. */
+moe_status_t moe_expert_fc1_mxfp4(const moe_config_t* cfg, const uint8_t* x_q,
+                                  const uint8_t* x_sf, const int32_t* offsets,
+                                  const float* perm_prob, const uint8_t* w1_q,
+                                  const uint8_t* w1_sf, void* a, uint8_t* a_q, uint8_t* a_sf,
+                                  moe_stream_t stream);
+moe_status_t moe_expert_fc2_mxfp4(const moe_config_t* cfg, const uint8_t* a_q,
+                                  const uint8_t* a_sf, const int32_t* offsets,
+                                  const uint8_t* w2_q, const uint8_t* w2_sf, void* y_perm,
+                                  moe_stream_t stream);
+
 /* Combine (review §2.1 "Combine"; the skill page's index_add_):
  *   y[t] = sum_{k=0}^{K-1} w[t,k] * y_perm[dst_row[t,k]]  (+ shared_y[t])
  * with w = topk_prob, or 1 when topk_prob is NULL (probabilities already
@@ -327,6 +372,38 @@ moe_status_t moe_layer_fwd(const moe_config_t* cfg, const void* x, const float* 
                            const void* w1_shared, const void* w2_shared, void* y,
                            int32_t* topk_idx_out, float* topk_prob_out, void* ws,
                            size_t ws_bytes, moe_stream_t stream);
+
+/* ---- The layer for a few tokens (a serving step) ------------------------------
+ * moe_layer_fwd's formulas, options and rules (routing with ties and selection
+ * bias, force-balanced routing, capacity, shared expert) for T <= 64 tokens,
+ * where the layer's time is the bytes of the busy experts' weights: those
+ * weights are read once and the rows of all tokens multiplied as they pass.
+ * bf16 configurations without SAVE_FOR_BWD and without loss weights (else
+ * MOE_ERR_UNSUPPORTED, as for T > 64).  p is applied to the expert's output.
+ * Results may differ from moe_layer_fwd's in the last bits (other orders of
+ * the fp32 sums).  Bitwise reproducible.  ws: moe_workspace_size(cfg) bytes, no
+ * state of an earlier call is read, and what a moe_layer_fwd left there for a
+ * backward is overwritten. */
+moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const void* x, const float* w_r,
+                               const float* gate_bias, const float* sel_bias, const void* w1,
+                               const void* b1, const void* w2, const void* b2,
+                               const void* w1_shared, const void* w2_shared, void* y,
+                               int32_t* topk_idx_out, float* topk_prob_out, void* ws,
+                               size_t ws_bytes, moe_stream_t stream);
+
+/* The same with the expert weights in MXFP4 (as moe_mxfp4_quantize writes them:
+ * W1 [E*2F, h] in uniform groups of 2F rows, W2 [E*h, F] in uniform groups of
+ * h rows, the shared expert's as one group); activations stay 16-bit, the
+ * products are of the weights' exact values.  SwiGLU, h and F multiples of 128
+ * (else MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_layer_fwd_few_mxfp4(const moe_config_t* cfg, const void* x, const float* w_r,
+                                     const float* gate_bias, const float* sel_bias,
+                                     const uint8_t* w1_q, const uint8_t* w1_sf,
+                                     const uint8_t* w2_q, const uint8_t* w2_sf,
+                                     const uint8_t* w1_shared_q, const uint8_t* w1_shared_sf,
+                                     const uint8_t* w2_shared_q, const uint8_t* w2_shared_sf,
+                                     void* y, int32_t* topk_idx_out, float* topk_prob_out,
+                                     void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ---- Backward (the training configuration: bf16, SwiGLU experts, a
  * renormalised softmax or sigmoid router; others return MOE_ERR_UNSUPPORTED).

@@ -27,7 +27,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr
 LIBS = {
     "libmoe_gb300.so": ["api.cu", "router.cu", "router_tc.cu", "permute.cu", "combine.cu", "gemm_simt.cu",
                         "gemm_tc.cu", "gemm_tc2.cu", "gemm_tc_bwd.cu", "bwd.cu", "permute_noalloc.cu",
-                        "aux_loss.cu", "gemm_mxfp8.cu"],
+                        "aux_loss.cu", "gemm_mxfp8.cu", "gemm_mxfp4.cu", "few.cu"],
     "libmoe_synth.so": ["synth.cu"],
 }
 

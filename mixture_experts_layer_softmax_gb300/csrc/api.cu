@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "few.cuh"
 
 namespace moe {
 cudaError_t launch_router(const moe_config_t&, const void*, const float*, const float*,
@@ -56,6 +57,14 @@ cudaError_t launch_scatter_quantize(const moe_config_t&, const void*, const int3
                                     const int32_t*, const int32_t*, uint8_t*, uint8_t*, int, int*,
                                     cudaStream_t);
 cudaError_t launch_grouped_gemm_mxfp8(bool, int, const uint8_t*, const uint8_t*, int,
+                                      const uint8_t*, const uint8_t*, int, int, int,
+                                      const int32_t*, const float*, void*, uint8_t*, uint8_t*,
+                                      int, int*, cudaStream_t);
+cudaError_t launch_mxfp4_quantize(int, int, int, const int32_t*, const void*, uint8_t*, uint8_t*,
+                                  int, cudaStream_t);
+cudaError_t launch_mxfp4_dequantize(int, int, int, const int32_t*, const uint8_t*, const uint8_t*,
+                                    void*, int, cudaStream_t);
+cudaError_t launch_grouped_gemm_mxfp4(bool, int, const uint8_t*, const uint8_t*, int,
                                       const uint8_t*, const uint8_t*, int, int, int,
                                       const int32_t*, const float*, void*, uint8_t*, uint8_t*,
                                       int, int*, cudaStream_t);
@@ -292,7 +301,8 @@ int32_t moe_expert_capacity(int32_t T, int32_t K, int32_t E, float capacity_fact
 
 size_t moe_workspace_size(const moe_config_t* cfg) {
   if (check_config(cfg) != MOE_OK) return 0;
-  return workspace_layout(*cfg).total;
+  const size_t layer = workspace_layout(*cfg).total, few = few_layout(*cfg).total;
+  return few > layer ? few : layer;
 }
 
 moe_status_t moe_router_topk(const moe_config_t* cfg, const void* x, const float* w_r,
@@ -533,6 +543,76 @@ moe_status_t moe_expert_fc2_mxfp8(const moe_config_t* cfg, const uint8_t* a_q,
                                                static_cast<cudaStream_t>(stream)));
 }
 
+moe_status_t moe_mxfp4_quantize(int64_t rows, int32_t K, int32_t groups, const int32_t* offsets,
+                                const void* x, uint8_t* q, uint8_t* sf, moe_stream_t stream) {
+  if (rows < 0 || rows > INT32_MAX || K <= 0 || groups < 1 || groups > 256)
+    return MOE_ERR_INVALID_ARG;
+  if (K % 128) return MOE_ERR_UNSUPPORTED;
+  if (!offsets && rows % groups) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !sf || !al16(x) || !al16(q) || !al16(sf)) return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  return cuda_status(launch_mxfp4_quantize((int)rows, K, groups, offsets, x, q, sf, d->sms,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_mxfp4_dequantize(int64_t rows, int32_t K, int32_t groups, const int32_t* offsets,
+                                const uint8_t* q, const uint8_t* sf, void* x, moe_stream_t stream) {
+  if (rows < 0 || rows > INT32_MAX || K <= 0 || groups < 1 || groups > 256)
+    return MOE_ERR_INVALID_ARG;
+  if (K % 128) return MOE_ERR_UNSUPPORTED;
+  if (!offsets && rows % groups) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !sf || !al16(x) || !al16(q) || !al16(sf)) return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  return cuda_status(launch_mxfp4_dequantize((int)rows, K, groups, offsets, q, sf, x, d->sms,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_expert_fc1_mxfp4(const moe_config_t* cfg, const uint8_t* x_q,
+                                  const uint8_t* x_sf, const int32_t* offsets,
+                                  const float* perm_prob, const uint8_t* w1_q,
+                                  const uint8_t* w1_sf, void* a, uint8_t* a_q, uint8_t* a_sf,
+                                  moe_stream_t stream) {
+  moe_status_t st = check_mxfp8(cfg);
+  if (st != MOE_OK) return st;
+  if (!x_q || !x_sf || !offsets || !w1_q || !w1_sf) return MOE_ERR_INVALID_ARG;
+  if (!a && !a_q) return MOE_ERR_INVALID_ARG;
+  if (!a_q != !a_sf) return MOE_ERR_INVALID_ARG;
+  if (!al16(x_q) || !al16(x_sf) || !al16(w1_q) || !al16(w1_sf) || !al16(a) || !al16(a_q) ||
+      !al16(a_sf))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  const moe_config_t& c = *cfg;
+  return cuda_status(launch_grouped_gemm_mxfp4(true, c.T * c.K, x_q, x_sf, c.h, w1_q, w1_sf,
+                                               2 * c.F, c.E, c.F, offsets, perm_prob, a, a_q, a_sf,
+                                               d->sms, d->status,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_expert_fc2_mxfp4(const moe_config_t* cfg, const uint8_t* a_q,
+                                  const uint8_t* a_sf, const int32_t* offsets,
+                                  const uint8_t* w2_q, const uint8_t* w2_sf, void* y_perm,
+                                  moe_stream_t stream) {
+  moe_status_t st = check_mxfp8(cfg);
+  if (st != MOE_OK) return st;
+  if (!a_q || !a_sf || !offsets || !w2_q || !w2_sf || !y_perm) return MOE_ERR_INVALID_ARG;
+  if (!al16(a_q) || !al16(a_sf) || !al16(w2_q) || !al16(w2_sf) || !al16(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  const moe_config_t& c = *cfg;
+  return cuda_status(launch_grouped_gemm_mxfp4(false, c.T * c.K, a_q, a_sf, c.F, w2_q, w2_sf, c.h,
+                                               c.E, c.h, offsets, nullptr, y_perm, nullptr,
+                                               nullptr, d->sms, d->status,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
 moe_status_t moe_unpermute_combine(const moe_config_t* cfg, const void* y_perm,
                                    const int32_t* dst_row, const float* topk_prob,
                                    const void* shared_y, void* y, moe_stream_t stream) {
@@ -637,6 +717,89 @@ moe_status_t moe_layer_fwd(const moe_config_t* cfg, const void* x, const float* 
   if (e == cudaSuccess && topk_prob_out)
     e = cudaMemcpyAsync(topk_prob_out, prob, sizeof(float) * c.T * c.K, cudaMemcpyDeviceToDevice, s);
   return cuda_status(e);
+}
+
+namespace {
+// The checks that both calls for a few tokens share.
+moe_status_t check_few(const moe_config_t* cfg, const void* x, const float* w_r, const void* y,
+                       const void* ws, size_t ws_bytes) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.dtype != MOE_BF16 || c.T > kFewMaxT || (c.flags & MOE_FLAG_SAVE_FOR_BWD) ||
+      c.aux_loss_coeff != 0.f || c.z_loss_coeff != 0.f)
+    return MOE_ERR_UNSUPPORTED;
+  if (c.T > 0 && (!x || !w_r || !y)) return MOE_ERR_INVALID_ARG;
+  if (!al16(x) || !al16(w_r) || !al16(y)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_workspace_size(cfg);
+  if (need == 0) return MOE_OK;
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status_t run_few(FewArgs& a, const moe_config_t* cfg, const void* x, const float* w_r,
+                     const float* gate_bias, const float* sel_bias, void* y, int32_t* idx_out,
+                     float* prob_out, void* ws, bool mxfp4, moe_stream_t stream) {
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  if (cfg->T == 0) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  a.c = *cfg;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.w_r = w_r; a.gate_bias = gate_bias; a.sel_bias = sel_bias;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  a.idx_out = idx_out; a.prob_out = prob_out;
+  a.ws = static_cast<char*>(ws);
+  a.status = d->status; a.sms = d->sms;
+  return cuda_status(launch_few(a, mxfp4, static_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const void* x, const float* w_r,
+                               const float* gate_bias, const float* sel_bias, const void* w1,
+                               const void* b1, const void* w2, const void* b2,
+                               const void* w1_shared, const void* w2_shared, void* y,
+                               int32_t* topk_idx_out, float* topk_prob_out, void* ws,
+                               size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = check_few(cfg, x, w_r, y, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (cfg->T > 0 && (!w1 || !w2)) return MOE_ERR_INVALID_ARG;
+  if (cfg->has_bias && (!b1 || !b2)) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared && (!w1_shared || !w2_shared)) return MOE_ERR_INVALID_ARG;
+  if (!al16(w1) || !al16(w2) || !al16(w1_shared) || !al16(w2_shared) || !al16(b1) || !al16(b2))
+    return MOE_ERR_INVALID_ARG;
+  FewArgs a{};
+  a.w1 = {w1, nullptr, w1_shared, nullptr};
+  a.w2 = {w2, nullptr, w2_shared, nullptr};
+  a.b1 = cfg->has_bias ? static_cast<const __nv_bfloat16*>(b1) : nullptr;
+  a.b2 = cfg->has_bias ? static_cast<const __nv_bfloat16*>(b2) : nullptr;
+  return run_few(a, cfg, x, w_r, gate_bias, sel_bias, y, topk_idx_out, topk_prob_out, ws, false,
+                 stream);
+}
+
+moe_status_t moe_layer_fwd_few_mxfp4(const moe_config_t* cfg, const void* x, const float* w_r,
+                                     const float* gate_bias, const float* sel_bias,
+                                     const uint8_t* w1_q, const uint8_t* w1_sf,
+                                     const uint8_t* w2_q, const uint8_t* w2_sf,
+                                     const uint8_t* w1_shared_q, const uint8_t* w1_shared_sf,
+                                     const uint8_t* w2_shared_q, const uint8_t* w2_shared_sf,
+                                     void* y, int32_t* topk_idx_out, float* topk_prob_out,
+                                     void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = check_mxfp8(cfg);
+  if (st != MOE_OK) return st;
+  if ((st = check_few(cfg, x, w_r, y, ws, ws_bytes)) != MOE_OK) return st;
+  if (cfg->T > 0 && (!w1_q || !w1_sf || !w2_q || !w2_sf)) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_shared && (!w1_shared_q || !w1_shared_sf || !w2_shared_q || !w2_shared_sf))
+    return MOE_ERR_INVALID_ARG;
+  for (const uint8_t* p : {w1_q, w1_sf, w2_q, w2_sf, w1_shared_q, w1_shared_sf, w2_shared_q,
+                           w2_shared_sf})
+    if (!al16(p)) return MOE_ERR_INVALID_ARG;
+  FewArgs a{};
+  a.w1 = {w1_q, w1_sf, w1_shared_q, w1_shared_sf};
+  a.w2 = {w2_q, w2_sf, w2_shared_q, w2_shared_sf};
+  return run_few(a, cfg, x, w_r, gate_bias, sel_bias, y, topk_idx_out, topk_prob_out, ws, true,
+                 stream);
 }
 
 moe_status_t moe_grouped_mlp_bwd(const moe_config_t* cfg, const void* dy_perm, const void* x_perm,

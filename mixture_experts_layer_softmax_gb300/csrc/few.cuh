@@ -1,0 +1,71 @@
+// Workspace of the layer for a few tokens (few.cu), laid over the bytes of the
+// whole-layer workspace: a call of one never needs what the other left.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kFewMaxT = 64;  // tokens of one moe_layer_fwd_few call
+
+// Slices of the router's h reduction: enough (expert, slice) pairs to give
+// every SM eight warps, slices of at least 256 columns, at most 32 of them.
+inline int few_kparts(const moe_config_t& c) {
+  const int64_t most = ceil_div(c.h, 256);
+  int64_t p = ceil_div(8 * 152, c.E);
+  if (p > most) p = most;
+  if (p > 32) p = 32;
+  return p < 1 ? 1 : (int)p;
+}
+
+struct FewLayout {
+  size_t parts, idx, prob, a, total;
+};
+
+inline FewLayout few_layout(const moe_config_t& c) {
+  FewLayout w{};
+  if (c.T < 1 || c.T > kFewMaxT || c.dtype != MOE_BF16) return w;
+  const size_t T = (size_t)c.T, P = T * c.K, S = P + (c.n_shared ? T : 0);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  w.parts = take((size_t)few_kparts(c) * T * c.E * 4);
+  w.idx = take(P * 4);
+  w.prob = take(P * 4);
+  w.a = take(S * c.F * 4);
+  w.total = off;
+  return w;
+}
+
+// The expert matrices of one projection: bf16 [E][rows][cols], or MXFP4 codes
+// with their scale atoms (uniform groups of `rows` rows, 128-row tiles).
+struct FewWeights {
+  const void* w;        // routed experts
+  const uint8_t* sf;    // their scales (MXFP4)
+  const void* ws;       // shared expert or null
+  const uint8_t* ws_sf;
+};
+
+struct FewArgs {
+  moe_config_t c;
+  const __nv_bfloat16* x;
+  const float* w_r;
+  const float* gate_bias;
+  const float* sel_bias;
+  FewWeights w1, w2;
+  const __nv_bfloat16* b1;
+  const __nv_bfloat16* b2;
+  __nv_bfloat16* y;
+  int32_t* idx_out;   // or null
+  float* prob_out;    // or null
+  char* ws;           // few_layout
+  int* status;
+  int sms;
+};
+
+cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s);
+
+}  // namespace moe

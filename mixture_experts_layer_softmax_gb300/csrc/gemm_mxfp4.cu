@@ -1,0 +1,560 @@
+// MXFP4: quantisation, its inverse, and the expert GEMMs on 4-bit operands:
+// E2M1 codes with one E8M0 scale per 1 x 32 block along K, block-scaled MMAs on
+// the 5th-generation tensor cores (tcgen05.mma kind::mxf4, scales in TMEM),
+// fp32 accumulate.
+//
+// "Scalable Training of Mixture-of-Experts Models with Megatron Core" (review),
+// §5.3 low-precision recipes: the microscaled formats native to Blackwell.
+// Element and scale rules are the OCP Microscaling v1.0 ones of MXFP4: shared
+// exponent X = floor(log2 max|x|) - 2 (E2M1's largest binade is 2^2), element =
+// x / 2^X rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the
+// even code), saturated to +-6.
+//
+// Operand format (written by mxfp4_quantize_kernel or by the FC1 epilogue):
+//   codes  [rows, K / 2] uint8, two columns a byte (the even column in bits
+//          0-3), code = sign << 3 | exponent << 1 | mantissa;
+//   scales in the atoms of mx.cuh, the same as MXFP8's.
+//
+// GEMM kernel (persistent, 1 CTA per SM, 320 threads), the roles of the MXFP8
+// kernel with twice the columns per stage:
+//   warp 0     TMA producer: 4 stages of {A 128 x 128 B, B 256 x 128 B} = 256
+//              columns (128-byte swizzle) plus two scale atoms per 128 rows.
+//   warp 1     TMEM owner and MMA issuer: per stage, tcgen05.cp of six atoms
+//              into the stage's 24 TMEM columns, then 4 MMAs M128 N256 K64
+//              (atom k / 2, scale bytes 2 (k % 2) and the next).
+//   warps 2-9  epilogue, as in the MXFP8 kernel; FC1 can re-quantise a.
+// K is a multiple of 128; an odd last 128 columns are half a stage (the box's
+// other half is zero fill and gets no MMA).
+// Every wait is bounded; a wait that gives up records MOE_ERR_TIMEOUT and
+// every role leaves its loop.
+#include <cuda_fp4.h>
+
+#include "mx.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+using mx::ATOM;
+constexpr int BM = 128, BN = 256;
+constexpr int BK = 256, BKB = 128;  // K elements and bytes per row and stage
+constexpr int A_BYTES = BM * BKB;   // 16 KB
+constexpr int B_BYTES = BN * BKB;   // 32 KB
+constexpr int SF_BYTES = 6 * ATOM;  // two atoms per 128 rows of A and B
+constexpr int STAGES = 4;
+constexpr int kThreads = 320;  // producer, MMA, 8 epilogue warps
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t SF_COL0 = 256, SF_STRIDE = 32;  // per stage: A scales +0..7, B +8..23
+
+enum Mx4Mode { kSwiGLU = 0, kPlain = 1 };
+
+struct Mx4Params {
+  const int32_t* offsets;  // [E+1]
+  const float* prob;       // FC1: [P] or null
+  const uint8_t* a_sf;     // A scale atoms
+  const uint8_t* b_sf;     // B scale atoms (uniform groups of Nb rows)
+  __nv_bfloat16* out;      // [P, N] bf16 or null
+  uint8_t* out_q;          // FC1: codes of a [P, N / 2] or null
+  uint8_t* out_sf;         // FC1: scale atoms of a
+  int E, Kd, N, Nb;
+  int* status;
+  uint64_t wait_limit_ns;
+};
+
+struct Mx4Ctl {
+  uint64_t full[STAGES], empty[STAGES], tmem_full, tmem_empty, drain;
+  uint32_t tmem_base;
+  int abort;
+  int tile_start[257];  // GEMM tiles before expert e
+  int rtile[257];       // 128-row tiles before expert e (scale atom numbering)
+  int off[257];
+};
+
+constexpr size_t kSmem = 1024 + (size_t)STAGES * (A_BYTES + B_BYTES + SF_BYTES) + sizeof(Mx4Ctl);
+
+// ---- E8M0 / E2M1 helpers ------------------------------------------------------
+// E8M0 code of a block whose largest magnitude has the fp32 bits `abits`: X + 127
+// with X = floor(log2 amax) - 2 clamped at -127.  A block that holds an infinity
+// or a NaN (exponent field 255) gets 255, the format's NaN.
+MOE_D uint32_t e8m0_code(uint32_t abits) {
+  const uint32_t e = abits >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+// 2^-X for scale code c; 0 for the NaN block (its codes are 0).
+MOE_D float e8m0_inverse(uint32_t c) { return c == 255u ? 0.f : __uint_as_float((254u - c) << 23); }
+
+// 8 values (already divided by the scale) -> 8 E2M1 codes, the first in the
+// low bits, round to nearest even with saturation.
+MOE_D uint32_t e2m1x8(const float* v) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_E2M1,
+                                            cudaRoundNearest)
+         << (8 * i);
+  return w;
+}
+
+MOE_D uint32_t pack_bf16x2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---- quantiser and its inverse ----------------------------------------------------
+// A 16-thread group per (row, 128-column chunk): each thread converts 8
+// consecutive values, 4 threads share a block (largest magnitude by shuffles),
+// and the group's first thread writes the chunk's 4 scale codes as one word.
+// Groups: offsets [G+1] on the device, or uniform groups of `urows` rows.
+__global__ void __launch_bounds__(256)
+    mxfp4_quantize_kernel(const __nv_bfloat16* __restrict__ x, int rows, int K, int G,
+                          const int32_t* __restrict__ offsets, int urows,
+                          uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
+  __shared__ int s_off[257], s_rt[257];
+  if (offsets) mx::load_groups(offsets, G, s_off, s_rt);
+  const int KB = K / 128;
+  const int lane = threadIdx.x & 31, sub = lane & 15;
+  const int64_t chunks = (int64_t)rows * KB;
+  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x / 32);
+  // every lane of a warp runs the same iterations (two chunks per warp), so
+  // the shuffles below always see the whole warp
+  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); 2 * w < chunks;
+       w += nwarps) {
+    const int64_t ch = 2 * w + (lane >> 4);
+    const bool valid = ch < chunks;
+    const int r = valid ? (int)(ch / KB) : 0;
+    const int kb = valid ? (int)(ch - (int64_t)r * KB) : 0;
+    const int64_t base = (int64_t)r * K + kb * 128 + sub * 8;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (valid) raw = __ldg(reinterpret_cast<const uint4*>(x + base));
+    const __nv_bfloat16* xv = reinterpret_cast<const __nv_bfloat16*>(&raw);
+    float v[8];
+    uint32_t abits = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = __bfloat162float(xv[i]);
+      abits = max(abits, __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    abits = max(abits, __shfl_xor_sync(0xffffffffu, abits, 1));
+    abits = max(abits, __shfl_xor_sync(0xffffffffu, abits, 2));
+    const uint32_t code = e8m0_code(abits);
+    const float inv = e8m0_inverse(code);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = code == 255u ? 0.f : v[i] * inv;  // exact: a power of two
+    const uint32_t c1 = __shfl_down_sync(0xffffffffu, code, 4);
+    const uint32_t c2 = __shfl_down_sync(0xffffffffu, code, 8);
+    const uint32_t c3 = __shfl_down_sync(0xffffffffu, code, 12);
+    if (!valid) continue;
+    *reinterpret_cast<uint32_t*>(q + base / 2) = e2m1x8(v);
+    if (sub == 0) {
+      int i;
+      int64_t tile;
+      if (offsets) {
+        if (!mx::find_row(s_off, s_rt, G, r, tile, i)) continue;  // a row of no group: no scales
+      } else {
+        const int g = r / urows, lr = r - g * urows;
+        tile = (int64_t)g * ((urows + 127) / 128) + lr / 128;
+        i = lr & 127;
+      }
+      *reinterpret_cast<uint32_t*>(sf + mx::atom_word(tile, KB, kb, i)) =
+          code | (c1 << 8) | (c2 << 16) | (c3 << 24);
+    }
+  }
+}
+
+// Codes and scales -> bf16 values, exact (one significant bit pair times a
+// power of two).  A thread per 8 columns; rows of no group are left as they are.
+__global__ void __launch_bounds__(256)
+    mxfp4_dequantize_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf, int rows,
+                            int K, int G, const int32_t* __restrict__ offsets, int urows,
+                            __nv_bfloat16* __restrict__ x) {
+  __shared__ int s_off[257], s_rt[257];
+  if (offsets) mx::load_groups(offsets, G, s_off, s_rt);
+  const int KB = K / 128, per_row = K / 8;
+  const int64_t n = (int64_t)rows * per_row, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < n; u += step) {
+    const int r = (int)(u / per_row), k = (int)(u - (int64_t)r * per_row) * 8;
+    int i;
+    int64_t tile;
+    if (offsets) {
+      if (!mx::find_row(s_off, s_rt, G, r, tile, i)) continue;
+    } else {
+      const int g = r / urows, lr = r - g * urows;
+      tile = (int64_t)g * ((urows + 127) / 128) + lr / 128;
+      i = lr & 127;
+    }
+    const float s = mx::e8m0_value(__ldg(sf + mx::atom_word(tile, KB, k / 128, i) + (k >> 5 & 3)));
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q + u * 4));
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t c = w >> (8 * j + 4 * b);
+        const uint32_t ex = c >> 1 & 3, m = c & 1;
+        const float mag = ex ? (float)((2 + m) << ex) * 0.25f : 0.5f * (float)m;
+        v[b] = ((c & 8) ? -mag : mag) * s;
+      }
+      o[j] = pack_bf16x2(v[0], v[1]);
+    }
+    *reinterpret_cast<uint4*>(x + u * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ---- GEMM -------------------------------------------------------------------------
+MOE_D void decode_tile(const Mx4Ctl& c, int E, int tile, int& e, int& mb, int& nb) {
+  int lo = 0, hi = E - 1;  // largest e with tile_start[e] <= tile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c.tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  e = lo;
+  const int local = tile - c.tile_start[e];
+  const int mblk = (c.off[e + 1] - c.off[e] + BM - 1) / BM;
+  nb = local / mblk;
+  mb = local - nb * mblk;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_gemm_mxfp4_kernel(const __grid_constant__ CUtensorMap tmA,
+                              const __grid_constant__ CUtensorMap tmB, const Mx4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * A_BYTES;
+  uint8_t* sSF = sB + STAGES * B_BYTES;
+  Mx4Ctl& ctl = *reinterpret_cast<Mx4Ctl*>(sSF + STAGES * SF_BYTES);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p.E;
+  const int nblk = MODE == kSwiGLU ? (p.N + 127) / 128 : (p.N + BN - 1) / BN;
+  const int KB = p.Kd / 128;     // scale atoms along K
+  const int KS = (p.Kd + BK - 1) / BK;  // stages along K; the last may hold one atom
+  const int nbt = p.Nb / 128;  // B row tiles per expert
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.full[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.empty[s]), 1);
+    }
+    tc::mbar_init(tc::smem_u32(&ctl.tmem_full), 1);
+    tc::mbar_init(tc::smem_u32(&ctl.tmem_empty), 8);
+    tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+    tc::prefetch_tensormap(&tmA);
+    tc::prefetch_tensormap(&tmB);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  for (int e = threadIdx.x; e <= E; e += kThreads) ctl.off[e] = __ldg(p.offsets + e);
+  __syncthreads();
+  if (warp == 2) {  // tile_start and rtile: exclusive scans over the experts
+    int run_t = 0, run_r = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int mblk = e < E ? (ctl.off[e + 1] - ctl.off[e] + BM - 1) / BM : 0;
+      int it = mblk * nblk, ir = mblk;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, it, o);
+        const int r = __shfl_up_sync(0xffffffffu, ir, o);
+        if (lane >= o) { it += t; ir += r; }
+      }
+      if (e < E) {
+        ctl.tile_start[e] = run_t + it - mblk * nblk;
+        ctl.rtile[e] = run_r + ir - mblk;
+      }
+      run_t += __shfl_sync(0xffffffffu, it, 31);
+      run_r += __shfl_sync(0xffffffffu, ir, 31);
+    }
+    if (lane == 0) ctl.tile_start[E] = run_t;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem_base = ctl.tmem_base;
+  const int total = ctl.tile_start[E];
+  tc::WaitCtl wc{p.status, &ctl.abort, p.wait_limit_ns, 0};
+  tc::WaitCtl wdrain{p.status, nullptr, 1000000000ull, 0};
+
+  if (warp == 0) {
+    // ================= TMA producer =================
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+        int e, mb, nb;
+        decode_tile(ctl, E, tile, e, mb, nb);
+        const int a_row = ctl.off[e] + mb * BM;
+        const int64_t a_atom = (int64_t)(ctl.rtile[e] + mb) * KB;
+        int b_row0, b_row1;
+        int64_t b_atom0, b_atom1;
+        bool two_b = true;
+        if (MODE == kSwiGLU) {  // gate rows nb*128.., up rows N + nb*128..
+          b_row0 = e * p.Nb + nb * 128;
+          b_row1 = e * p.Nb + p.N + nb * 128;
+          b_atom0 = ((int64_t)e * nbt + nb) * KB;
+          b_atom1 = ((int64_t)e * nbt + p.N / 128 + nb) * KB;
+        } else {
+          b_row0 = e * p.Nb + nb * BN;
+          b_row1 = b_row0 + 128;
+          b_atom0 = ((int64_t)e * nbt + 2 * nb) * KB;
+          b_atom1 = b_atom0 + KB;
+          two_b = nb * BN + 128 < p.N;  // a half past N has no scale atom to read
+        }
+                bool ok = true;
+        for (int ks = 0; ks < KS; ++ks) {
+          if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
+          const int kb = 2 * ks;
+          const uint32_t sfb = (kb + 1 < KB ? 2 : 1) * ATOM;  // scale bytes per 128 rows
+          const uint32_t fb = tc::smem_u32(&ctl.full[stage]);
+          tc::mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES + (two_b ? 3 : 2) * sfb);
+          const uint32_t a_dst = tc::smem_u32(sA + stage * A_BYTES);
+          const uint32_t b_dst = tc::smem_u32(sB + stage * B_BYTES);
+          const uint32_t sf_dst = tc::smem_u32(sSF + stage * SF_BYTES);
+          tc::tma_load_2d(a_dst, &tmA, ks * BKB, a_row, fb);
+          tc::tma_load_2d(b_dst, &tmB, ks * BKB, b_row0, fb);
+          tc::tma_load_2d(b_dst + B_BYTES / 2, &tmB, ks * BKB, b_row1, fb);
+          tc::bulk_load(sf_dst, p.a_sf + (a_atom + kb) * ATOM, sfb, fb);
+          tc::bulk_load(sf_dst + 2 * ATOM, p.b_sf + (b_atom0 + kb) * ATOM, sfb, fb);
+          if (two_b) tc::bulk_load(sf_dst + 4 * ATOM, p.b_sf + (b_atom1 + kb) * ATOM, sfb, fb);
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+      }
+      for (int s = 0; s < STAGES; ++s)
+        if ((issued >> s) & 1u)
+          tc::mbar_wait(tc::smem_u32(&ctl.full[s]), (issued_par >> s) & 1u, wdrain);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================= MMA issuer =================
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.tmem_empty), acc_phase ^ 1, wc)) break;
+        tc::fence_after_sync();
+        for (int ks = 0; ks < KS; ++ks) {
+          if (!tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), phase, wc)) { ok = false; break; }
+          tc::fence_after_sync();
+          const uint32_t a0 = tc::smem_u32(sA + stage * A_BYTES);
+          const uint32_t b0 = tc::smem_u32(sB + stage * B_BYTES);
+          const uint32_t sf0 = tc::smem_u32(sSF + stage * SF_BYTES);
+          const uint32_t sfa = tmem_base + SF_COL0 + stage * SF_STRIDE;
+          const int atoms = 2 * ks + 1 < KB ? 2 : 1;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (j >= atoms) break;
+            // atom j: A scales in columns 4j .. 4j+3, B scales in 8 + 8j .. 8 + 8j + 7
+            tc::tmem_cp_32x128b_warpx4(sfa + 4 * j, tc::desc_sf_atom(sf0 + j * ATOM));
+            tc::tmem_cp_32x128b_warpx4(sfa + 8 + 8 * j, tc::desc_sf_atom(sf0 + (2 + j) * ATOM));
+            tc::tmem_cp_32x128b_warpx4(sfa + 12 + 8 * j, tc::desc_sf_atom(sf0 + (4 + j) * ATOM));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 64 columns (32 bytes, two blocks) an MMA
+            if ((k >> 1) >= atoms) break;
+            tc::mma_mxf4(tmem_base, tc::desc_kmajor_sw128(a0 + k * 32),
+                         tc::desc_kmajor_sw128(b0 + k * 32),
+                         tc::idesc_mxf4_e2m1(BM, BN, 2 * (k & 1), 2 * (k & 1)), sfa + 4 * (k >> 1),
+                         sfa + 8 + 8 * (k >> 1), (ks | k) != 0);
+          }
+          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        tc::mma_commit(tc::smem_u32(&ctl.tmem_full));
+        acc_phase ^= 1;
+      }
+      if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
+        tc::mma_commit(tc::smem_u32(&ctl.drain));
+        tc::mbar_wait(tc::smem_u32(&ctl.drain), 0, wdrain);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================= epilogue (warps 2..9) =================
+    // two warps per TMEM lane quarter, each taking half of the tile's columns;
+    // each releases the accumulator as soon as its TMEM reads are done
+    const int q = warp & 3;          // TMEM lane quarter this warp may access
+    const int hf = (warp - 2) >> 2;  // which half of the columns
+    uint32_t acc_phase = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      int e, mb, nb;
+      decode_tile(ctl, E, tile, e, mb, nb);
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.tmem_full), acc_phase, wc)) break;
+      tc::fence_after_sync();
+      const int m_e = ctl.off[e + 1] - ctl.off[e];
+      const int i = q * 32 + lane;  // row within the tile
+      const bool valid = mb * BM + i < m_e;
+      const int64_t row = (int64_t)ctl.off[e] + mb * BM + i;
+      const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+      if (MODE == kSwiGLU) {
+        // columns: gate hf*64 .. +63 and the matching up columns (two 32-wide chunks)
+        const float pr = (p.prob && valid) ? __ldg(p.prob + row) : 1.f;
+        // all of this warp's TMEM reads first (gate and up, two 32-column
+        // chunks each), then the release, then the math: the next tile's MMAs
+        // need not wait for the SiLU evaluations
+        uint32_t g[2][32], u[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = hf * 64 + c * 32;
+          tc::tmem_ld_32x32b_x32(tbase + col, g[c]);
+          tc::tmem_ld_32x32b_x32(tbase + 128 + col, u[c]);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tmem_empty));
+        float a[2][32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            a[c][j] = pr * (silu_f(__uint_as_float(g[c][j])) * __uint_as_float(u[c][j]));
+        uint32_t codes = 0;  // this warp's 2 of the row's 4 block scales
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int n = nb * 128 + hf * 64 + c * 32;
+          if (valid && p.out) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 w;
+              w.x = pack_bf16x2(a[c][j], a[c][j + 1]);
+              w.y = pack_bf16x2(a[c][j + 2], a[c][j + 3]);
+              w.z = pack_bf16x2(a[c][j + 4], a[c][j + 5]);
+              w.w = pack_bf16x2(a[c][j + 6], a[c][j + 7]);
+              *reinterpret_cast<uint4*>(p.out + row * p.N + n + j) = w;
+            }
+          }
+          if (p.out_q) {
+            uint32_t abits = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) abits = max(abits, __float_as_uint(a[c][j]) & 0x7fffffffu);
+            const uint32_t code = e8m0_code(abits);
+            const float inv = e8m0_inverse(code);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) a[c][j] *= inv;
+            codes |= code << (8 * c);
+            if (valid)
+              *reinterpret_cast<uint4*>(p.out_q + (row * p.N + n) / 2) =
+                  make_uint4(e2m1x8(a[c]), e2m1x8(a[c] + 8), e2m1x8(a[c] + 16), e2m1x8(a[c] + 24));
+          }
+        }
+        if (p.out_q)  // FC2's A operand: atom (rtile[e] + mb, kb = nb), row i, blocks 2 hf, 2 hf + 1
+          *reinterpret_cast<uint16_t*>(
+              p.out_sf + mx::atom_word(ctl.rtile[e] + mb, p.N / 128, nb, i) + 2 * hf) =
+              (uint16_t)(valid ? codes : 0u);
+      } else {
+        // columns hf*128 .. +127: all four 32-column loads first, then release
+        uint32_t r[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld_32x32b_x32(tbase + hf * 128 + c * 32, r[c]);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tmem_empty));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int n = nb * BN + hf * 128 + c * 32;
+          if (valid && n < p.N) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
+              w.y = pack_bf16x2(__uint_as_float(r[c][j + 2]), __uint_as_float(r[c][j + 3]));
+              w.z = pack_bf16x2(__uint_as_float(r[c][j + 4]), __uint_as_float(r[c][j + 5]));
+              w.w = pack_bf16x2(__uint_as_float(r[c][j + 6]), __uint_as_float(r[c][j + 7]));
+              *reinterpret_cast<uint4*>(p.out + row * p.N + n + j) = w;
+            }
+          }
+        }
+      }
+      acc_phase ^= 1;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ---- host side ----------------------------------------------------------------------
+// 2-D uint8 [rows, bytes] map with a {128, 128} box, 128-byte swizzle, zero fill.
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t bytes) {
+  tc::EncodeTiledFn fn = tc::encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {bytes, rows};
+  const cuuint64_t strides[1] = {bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)BKB, 128};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_quantize(int rows, int K, int groups, const int32_t* offsets,
+                                  const void* x, uint8_t* q, uint8_t* sf, int sms,
+                                  cudaStream_t s) {
+  if (rows == 0) return cudaSuccess;
+  const int64_t blocks = ceil_div((int64_t)rows * (K / 128), 2 * (256 / 32));
+  const int grid = (int)(blocks < 8LL * sms ? blocks : 8LL * sms);
+  mxfp4_quantize_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), rows, K, groups,
+                                             offsets, offsets ? 0 : rows / groups, q, sf);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mxfp4_dequantize(int rows, int K, int groups, const int32_t* offsets,
+                                    const uint8_t* q, const uint8_t* sf, void* x, int sms,
+                                    cudaStream_t s) {
+  if (rows == 0) return cudaSuccess;
+  const int64_t blocks = ceil_div((int64_t)rows * (K / 8), 256);
+  const int grid = (int)(blocks < 8LL * sms ? blocks : 8LL * sms);
+  mxfp4_dequantize_kernel<<<grid, 256, 0, s>>>(q, sf, rows, K, groups, offsets,
+                                               offsets ? 0 : rows / groups,
+                                               static_cast<__nv_bfloat16*>(x));
+  return cudaGetLastError();
+}
+
+// One MXFP4 grouped GEMM.  swiglu (FC1): A = x_perm [P, Kd], B = W1 [E * 2N, Kd]
+// (gate rows then up rows per expert), out = a [P, N] bf16 (or null) and/or
+// out_q / out_sf = a re-quantised for FC2; prob scales a.  Plain (FC2): B = W2
+// [E * N, Kd], out [P, N] bf16.
+cudaError_t launch_grouped_gemm_mxfp4(bool swiglu, int P, const uint8_t* A, const uint8_t* A_sf,
+                                      int Kd, const uint8_t* B, const uint8_t* B_sf, int Nb,
+                                      int E, int N, const int32_t* offsets, const float* prob,
+                                      void* out, uint8_t* out_q, uint8_t* out_sf, int sms,
+                                      int* status, cudaStream_t s) {
+  if (P == 0) return cudaSuccess;
+  CUtensorMap ma, mb;
+  if (!encode_codes(&ma, A, (uint64_t)P, (uint64_t)Kd / 2)) return cudaErrorInvalidValue;
+  if (!encode_codes(&mb, B, (uint64_t)E * Nb, (uint64_t)Kd / 2)) return cudaErrorInvalidValue;
+  Mx4Params p{};
+  p.offsets = offsets; p.prob = prob; p.a_sf = A_sf; p.b_sf = B_sf;
+  p.out = static_cast<__nv_bfloat16*>(out); p.out_q = out_q; p.out_sf = out_sf;
+  p.E = E; p.Kd = Kd; p.N = N; p.Nb = Nb;
+  p.status = status;
+  p.wait_limit_ns = 2000000000ull;
+  const int nblk = swiglu ? (N + 127) / 128 : (N + BN - 1) / BN;
+  const int64_t tiles_max = (ceil_div(P, BM) + E) * (int64_t)nblk;
+  const int grid = (int)(tiles_max < sms ? tiles_max : sms);
+  auto kern = swiglu ? grouped_gemm_mxfp4_kernel<kSwiGLU> : grouped_gemm_mxfp4_kernel<kPlain>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, kSmem, s>>>(ma, mb, p);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -261,6 +261,27 @@ MOE_D void mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t id
       : "memory");
 }
 
+// ---- block-scaled MMA (kind::mxf4) ----------------------------------------------
+// Instruction descriptor for E2M1 x E2M1 -> fp32 with E8M0 scales, K = 64, two
+// 32-column blocks an MMA: the layout of kind::mxf8f6f4 with both formats E2M1
+// (1); the scale id (0 or 2) picks the lower or the upper two bytes of each
+// 32-bit TMEM scale word.
+MOE_HD constexpr uint32_t idesc_mxf4_e2m1(int M, int N, int sfa_id, int sfb_id) {
+  return ((uint32_t)sfb_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         (1u << 23) | ((uint32_t)(M >> 4) << 24) | ((uint32_t)sfa_id << 29);
+}
+
+MOE_D void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                    uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
 // Shared-memory descriptor of one 512-byte scale atom as the source of a
 // tcgen05.cp 32x128b: 32 rows of 16 bytes, no swizzle, 8-row core-matrix
 // groups 128 bytes apart.

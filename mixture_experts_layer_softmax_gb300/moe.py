@@ -67,6 +67,14 @@ _SIG = {
     "moe_permute_mxfp8": (ctypes.c_int, [_CFG] + [_P] * 11 + [ctypes.c_size_t, _P]),
     "moe_expert_fc1_mxfp8": (ctypes.c_int, [_CFG] + [_P] * 10),
     "moe_expert_fc2_mxfp8": (ctypes.c_int, [_CFG] + [_P] * 7),
+    "moe_mxfp4_quantize": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                          _P, _P, _P]),
+    "moe_mxfp4_dequantize": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
+                                            _P, _P, _P, _P]),
+    "moe_expert_fc1_mxfp4": (ctypes.c_int, [_CFG] + [_P] * 10),
+    "moe_expert_fc2_mxfp4": (ctypes.c_int, [_CFG] + [_P] * 7),
+    "moe_layer_fwd_few": (ctypes.c_int, [_CFG] + [_P] * 14 + [ctypes.c_size_t, _P]),
+    "moe_layer_fwd_few_mxfp4": (ctypes.c_int, [_CFG] + [_P] * 16 + [ctypes.c_size_t, _P]),
     "moe_unpermute_combine": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P]),
     "moe_layer_fwd": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                      ctypes.c_size_t, _P]),
@@ -253,6 +261,34 @@ def moe_expert_fc2_mxfp8(cfg, a_q, a_sf, offsets, w2_q, w2_sf, y_perm, stream=No
         _ptr(y_perm), _stream(stream)))
 
 
+def moe_mxfp4_quantize(rows, K, groups, offsets, x, q, sf, stream=None):
+    """x [rows, K] bf16 -> MXFP4 codes q [rows, K/2] and scales sf
+    (moe_mxfp8_scale_bytes(rows, K, groups) bytes)."""
+    _check("moe_mxfp4_quantize", _lib.moe_mxfp4_quantize(
+        int(rows), int(K), int(groups), _ptr(offsets), _ptr(x), _ptr(q), _ptr(sf),
+        _stream(stream)))
+
+
+def moe_mxfp4_dequantize(rows, K, groups, offsets, q, sf, x, stream=None):
+    """The bf16 values of an MXFP4 tensor, into x [rows, K]."""
+    _check("moe_mxfp4_dequantize", _lib.moe_mxfp4_dequantize(
+        int(rows), int(K), int(groups), _ptr(offsets), _ptr(q), _ptr(sf), _ptr(x),
+        _stream(stream)))
+
+
+def moe_expert_fc1_mxfp4(cfg, x_q, x_sf, offsets, perm_prob, w1_q, w1_sf, a, a_q, a_sf,
+                         stream=None):
+    _check("moe_expert_fc1_mxfp4", _lib.moe_expert_fc1_mxfp4(
+        ctypes.byref(cfg), _ptr(x_q), _ptr(x_sf), _ptr(offsets), _ptr(perm_prob), _ptr(w1_q),
+        _ptr(w1_sf), _ptr(a), _ptr(a_q), _ptr(a_sf), _stream(stream)))
+
+
+def moe_expert_fc2_mxfp4(cfg, a_q, a_sf, offsets, w2_q, w2_sf, y_perm, stream=None):
+    _check("moe_expert_fc2_mxfp4", _lib.moe_expert_fc2_mxfp4(
+        ctypes.byref(cfg), _ptr(a_q), _ptr(a_sf), _ptr(offsets), _ptr(w2_q), _ptr(w2_sf),
+        _ptr(y_perm), _stream(stream)))
+
+
 def moe_unpermute_combine(cfg, y_perm, dst_row, topk_prob, shared_y, y, stream=None):
     _check("moe_unpermute_combine", _lib.moe_unpermute_combine(
         ctypes.byref(cfg), _ptr(y_perm), _ptr(dst_row), _ptr(topk_prob), _ptr(shared_y), _ptr(y),
@@ -266,6 +302,28 @@ def moe_layer_fwd(cfg, x, w_r, gate_bias, sel_bias, w1, b1, w2, b2, w1_shared, w
         ctypes.byref(cfg), _ptr(x), _ptr(w_r), _ptr(gate_bias), _ptr(sel_bias), _ptr(w1),
         _ptr(b1), _ptr(w2), _ptr(b2), _ptr(w1_shared), _ptr(w2_shared), _ptr(y),
         _ptr(topk_idx_out), _ptr(topk_prob_out), wp, wb, _stream(stream)))
+
+
+def moe_layer_fwd_few(cfg, x, w_r, gate_bias, sel_bias, w1, b1, w2, b2, w1_shared, w2_shared, y,
+                      topk_idx_out=None, topk_prob_out=None, ws=None, stream=None):
+    """moe_layer_fwd for T <= 64 tokens (a serving step), bf16 weights."""
+    wp, wb = _ws(ws)
+    _check("moe_layer_fwd_few", _lib.moe_layer_fwd_few(
+        ctypes.byref(cfg), _ptr(x), _ptr(w_r), _ptr(gate_bias), _ptr(sel_bias), _ptr(w1),
+        _ptr(b1), _ptr(w2), _ptr(b2), _ptr(w1_shared), _ptr(w2_shared), _ptr(y),
+        _ptr(topk_idx_out), _ptr(topk_prob_out), wp, wb, _stream(stream)))
+
+
+def moe_layer_fwd_few_mxfp4(cfg, x, w_r, gate_bias, sel_bias, w1_q, w1_sf, w2_q, w2_sf,
+                            w1_shared_q, w1_shared_sf, w2_shared_q, w2_shared_sf, y,
+                            topk_idx_out=None, topk_prob_out=None, ws=None, stream=None):
+    """moe_layer_fwd_few with the expert weights in MXFP4."""
+    wp, wb = _ws(ws)
+    _check("moe_layer_fwd_few_mxfp4", _lib.moe_layer_fwd_few_mxfp4(
+        ctypes.byref(cfg), _ptr(x), _ptr(w_r), _ptr(gate_bias), _ptr(sel_bias), _ptr(w1_q),
+        _ptr(w1_sf), _ptr(w2_q), _ptr(w2_sf), _ptr(w1_shared_q), _ptr(w1_shared_sf),
+        _ptr(w2_shared_q), _ptr(w2_shared_sf), _ptr(y), _ptr(topk_idx_out), _ptr(topk_prob_out),
+        wp, wb, _stream(stream)))
 
 
 def moe_grouped_mlp_bwd(cfg, dy_perm, x_perm, act_save, a, offsets, perm_prob, w1, w2, dx_perm,
