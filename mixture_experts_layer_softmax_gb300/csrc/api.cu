@@ -177,8 +177,15 @@ moe_status_t check_config(const moe_config_t* c) {
   return MOE_OK;
 }
 
+// Workspace bytes of a valid config, the same for every entry point: the
+// layer's layout, or the few-token call's (laid over it) where that is larger.
+size_t workspace_bytes(const moe_config_t& c) {
+  const size_t layer = workspace_layout(c).total, few = few_layout(c).total;
+  return few > layer ? few : layer;
+}
+
 moe_status_t check_ws(const moe_config_t* c, const void* ws, size_t ws_bytes) {
-  const size_t need = workspace_layout(*c).total;
+  const size_t need = workspace_bytes(*c);
   if (need == 0) return MOE_OK;
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return MOE_ERR_INVALID_ARG;
@@ -301,8 +308,7 @@ int32_t moe_expert_capacity(int32_t T, int32_t K, int32_t E, float capacity_fact
 
 size_t moe_workspace_size(const moe_config_t* cfg) {
   if (check_config(cfg) != MOE_OK) return 0;
-  const size_t layer = workspace_layout(*cfg).total, few = few_layout(*cfg).total;
-  return few > layer ? few : layer;
+  return workspace_bytes(*cfg);
 }
 
 moe_status_t moe_router_topk(const moe_config_t* cfg, const void* x, const float* w_r,
@@ -731,11 +737,7 @@ moe_status_t check_few(const moe_config_t* cfg, const void* x, const float* w_r,
     return MOE_ERR_UNSUPPORTED;
   if (c.T > 0 && (!x || !w_r || !y)) return MOE_ERR_INVALID_ARG;
   if (!al16(x) || !al16(w_r) || !al16(y)) return MOE_ERR_INVALID_ARG;
-  const size_t need = moe_workspace_size(cfg);
-  if (need == 0) return MOE_OK;
-  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
-  if (reinterpret_cast<uintptr_t>(ws) & 255u) return MOE_ERR_INVALID_ARG;
-  return MOE_OK;
+  return check_ws(cfg, ws, ws_bytes);
 }
 
 moe_status_t run_few(FewArgs& a, const moe_config_t* cfg, const void* x, const float* w_r,

@@ -18,24 +18,37 @@ inline int few_kparts(const moe_config_t& c) {
   return p < 1 ? 1 : (int)p;
 }
 
+// FC2's reduction (F) is cut into slices of at most 4096 columns whose partial
+// results are added in order: units stay small enough to spread evenly.
+constexpr int kFewKC = 512;  // columns per pipeline stage
+inline int few_ksplit(const moe_config_t& c) {
+  return (int)ceil_div(ceil_div(c.F, kFewKC), 4096 / kFewKC);
+}
+
 struct FewLayout {
-  size_t parts, idx, prob, a, total;
+  size_t sync, parts, xh, xs, a, as, ypart, total;
 };
+// int32 words at `sync`: the unit counter, the warps that finished FC2 results,
+// and those that finished FC1 results per busy expert (E + 1).
+inline size_t few_sync_words(const moe_config_t& c) { return 2 + c.E + 1; }
 
 inline FewLayout few_layout(const moe_config_t& c) {
   FewLayout w{};
   if (c.T < 1 || c.T > kFewMaxT || c.dtype != MOE_BF16) return w;
-  const size_t T = (size_t)c.T, P = T * c.K, S = P + (c.n_shared ? T : 0);
+  const size_t T = (size_t)c.T, S = T * c.K + (c.n_shared ? T : 0);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
     return o;
   };
+  w.sync = take(few_sync_words(c) * 4);
   w.parts = take((size_t)few_kparts(c) * T * c.E * 4);
-  w.idx = take(P * 4);
-  w.prob = take(P * 4);
-  w.a = take(S * c.F * 4);
+  w.xh = take(T * c.h * 2);              // tokens in fp16 (MXFP4 weights)
+  w.xs = take(T * 4);                    // and their power-of-two scales
+  w.a = take(S * c.F * 2);               // hidden values, 16 bits
+  w.as = take(S * ceil_div(c.F, 32) * 4);  // and their scales (MXFP4 weights)
+  w.ypart = take((size_t)few_ksplit(c) * S * c.h * 4);
   w.total = off;
   return w;
 }
