@@ -135,20 +135,34 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// One token's logits (the slices added in order) and its selection: a warp.
+// All experts' loads of four slices go out together: their latency, not their
+// number, is what a decoding step waits for here.
 template <int J>
 MOE_D void few_select_token(const float* parts, int kparts, const float* gate_bias, int t,
                             const RouterArgs& r, int lane) {
   float l[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = lane + 32 * j;
-    float s = 0.f;
-    if (e < r.E) {
-      for (int p = 0; p < kparts; ++p) s += parts[((int64_t)p * r.T + t) * r.E + e];
-      if (gate_bias) s += __ldg(gate_bias + e);
-    }
-    l[j] = s;
+  for (int j = 0; j < J; ++j) l[j] = 0.f;
+  for (int p0 = 0; p0 < kparts; p0 += 4) {
+    float v[J][4];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = lane + 32 * j;
+        v[j][i] = e < r.E && p0 + i < kparts
+                      ? __ldcg(parts + ((int64_t)(p0 + i) * r.T + t) * r.E + e) : 0.f;
+      }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[j] += v[j][i];
   }
+  if (gate_bias)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane + 32 * j < r.E) l[j] += __ldg(gate_bias + lane + 32 * j);
   select_and_write<J>(l, t, r, lane);
 }
 
@@ -177,12 +191,14 @@ struct FewCtl {
   uint64_t empty[kMaxStages], meet;
   alignas(16) FewStage st[kMaxStages];
   int abort;
-  int entries, pairs, units1, units2, fc2_writers;
+  int pairs, units1, units2, fc2_writers;
   int ent_e[kMaxEntries];        // expert (E: the shared one)
   int ent_start[kMaxEntries];    // first sorted pair
   int ent_n[kMaxEntries];        // pairs
   int cum1[kMaxEntries + 1], cum2[kMaxEntries + 1];  // units before entry j
-  int cnt[kMaxEntries];
+  int start[kMaxEntries];                // first sorted pair of an expert
+  unsigned long long mask[kMaxEntries];  // tokens of an expert
+  int4 part[9];                          // a 32-expert chunk's entries, pairs, sub-units, writers
   int idx[kMaxPairs];
   float prob[kMaxPairs];
   int16_t pos_of[kMaxPairs];     // sorted position of pair p, -1: dropped
@@ -207,13 +223,15 @@ struct FewParams {
   uint64_t wait_limit_ns;
 };
 
-template <bool W4_, int MT_, int NT_, int NW_>
+// RT = 16 MT weight rows of a unit, NB = 8 NT tokens, NW consumer warps: MT of
+// them share a slice of a stage's KC columns, one m-tile each.
+template <bool W4_, int MT_, int NT_, int NW_, int KC_>
 struct FewTile {
   static constexpr bool W4 = W4_;
-  static constexpr int MT = MT_, NT = NT_, NW = NW_;
+  static constexpr int MT = MT_, NT = NT_, NW = NW_, KC = KC_;
   static constexpr int RT = 16 * MT;  // weight rows of a unit
   static constexpr int NB = 8 * NT;   // tokens of a unit
-  static constexpr int KC = kFewKC, KW = KC / NW;
+  static constexpr int KG = NW / MT, KW = KC / KG;  // slices and their columns
   // A stage holds KC / 256 boxes of 256 columns, rows one after the other.
   // bf16 rows are 512 bytes, unswizzled: two of a quarter-warp's eight 16-byte
   // loads meet in a bank, which the shared-memory bandwidth has room for.
@@ -225,9 +243,9 @@ struct FewTile {
   static constexpr int BS_ROW = W4 ? KC / 32 * 4 : 0;
   static constexpr int STAGE = (A_BYTES + B_BYTES + SF + NB * BS_ROW + 1023) / 1024 * 1024;
   static constexpr int RED_TOK = RT + 4;  // padded token stride of the meeting buffer
-  static constexpr int RED = 2 * NW * NB * RED_TOK * 4;  // two units in turn
+  static constexpr int RED = 2 * KG * NB * RED_TOK * 4;  // two units in turn
   static constexpr int THREADS = 32 * (NW + 2);
-  static_assert(KW % 32 == 0, "whole scale blocks per warp");
+  static_assert(NW % MT == 0 && NW >= 8 && KW % (W4 ? 128 : 32) == 0, "whole scale words per warp");
 };
 
 // Warps that write the results of a unit of n tokens by `width` values, and of
@@ -240,79 +258,100 @@ MOE_HD int few_writers_of(int n, int nb, int width, int warps) {
   return n / nb * few_writers(nb, width, warps) + few_writers(n % nb, width, warps);
 }
 
-// Sorts the pairs by expert (tokens ascending) and lays out the units: warp 0.
-__device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nb, int rows1, int rows2,
-                               int rt, int ksplit, int warps, int* status) {
-  const int lane = threadIdx.x & 31, P = cf.T * cf.K;
-  for (int e = lane; e <= cf.E; e += 32) c.cnt[e] = 0;
-  __syncwarp();
-  for (int p0 = 0; p0 < P; p0 += 32) {
-    const int p = p0 + lane;
-    int e = p < P ? c.idx[p] : -1;
-    if (p < P && (e < 0 || e >= cf.E)) {
-      report(status, MOE_ERR_DEVICE_BOUNDS);
-      e = -1;
-    }
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    const int before = __popc(same & ((1u << lane) - 1));
-    const int rank = e >= 0 ? c.cnt[e] + before : -1;
-    __syncwarp();
-    if (e >= 0 && before == 0) c.cnt[e] += __popc(same);
-    __syncwarp();
-    if (p < P) c.pos_of[p] = (int16_t)((cf.capacity > 0 && rank >= cf.capacity) ? -1 : rank);
+// Sorts the pairs by expert (tokens ascending) and lays out the units; every
+// thread of the block calls it.  A token picks an expert at most once, so the
+// tokens of an expert are a 64-bit mask: a pair's place is the number of set
+// bits below its token, whatever the order the bits were set in.
+template <class L>
+__device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int nrb2, int ksplit,
+                               int* status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = cf.T * cf.K;
+  for (int p = threadIdx.x; p < P; p += L::THREADS) {
+    const int e = c.idx[p];
+    if (e < 0 || e >= cf.E) report(status, MOE_ERR_DEVICE_BOUNDS);
+    else atomicOr(&c.mask[e], 1ull << (p / cf.K));
   }
-  // busy experts in order, their first pairs and units
-  const int nrb1 = (rows1 + rt - 1) / rt, nrb2 = (rows2 + rt - 1) / rt;
-  int ents = 0, pairs = 0, u1 = 0, u2 = 0, writers = 0;
-  const int last = cf.E + (cf.n_shared ? 1 : 0);
-  for (int e0 = 0; e0 < last; e0 += 32) {
-    const int e = e0 + lane;
-    int n = 0;
-    if (e < cf.E) n = cf.capacity > 0 ? min(c.cnt[e], cf.capacity) : c.cnt[e];
-    else if (e < last) n = cf.T;
-    const int sub = (n + nb - 1) / nb;
-    int ie = n > 0 ? 1 : 0, ip = n, is = sub;
-    writers += __reduce_add_sync(0xffffffffu, few_writers_of(n, nb, rt, warps));
+  if (threadIdx.x == 0 && cf.n_shared) c.mask[cf.E] = ~0ull >> (64 - cf.T);
+  __syncthreads();
+  // a 32-expert chunk a warp; the shared expert is one more expert
+  const int last = cf.E + (cf.n_shared ? 1 : 0), chunks = (last + 31) / 32;
+  for (int ch = warp; ch < chunks; ch += L::NW + 2) {
+    const int e = ch * 32 + lane;
+    int n = e < last ? __popcll(c.mask[e]) : 0;
+    if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
+    int ie = n > 0 ? 1 : 0, ip = n, is = (n + L::NB - 1) / L::NB;
+    int iw = few_writers_of(n, L::NB, L::RT, L::NW);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, ie, o), b = __shfl_up_sync(0xffffffffu, ip, o),
-                d = __shfl_up_sync(0xffffffffu, is, o);
-      if (lane >= o) { ie += a; ip += b; is += d; }
+                d = __shfl_up_sync(0xffffffffu, is, o), f = __shfl_up_sync(0xffffffffu, iw, o);
+      if (lane >= o) { ie += a; ip += b; is += d; iw += f; }
     }
-    if (n > 0) {
-      const int j = ents + ie - 1;
-      c.ent_e[j] = e;
-      c.ent_start[j] = pairs + ip - n;
-      c.ent_n[j] = n;
-      c.cum1[j] = u1 + (is - sub) * nrb1;
-      c.cum2[j] = u2 + (is - sub) * nrb2 * ksplit;
+    if (lane == 31) c.part[ch] = make_int4(ie, ip, is, iw);
+    if (e < last) {  // within the chunk, for now
+      c.start[e] = ip - n;
+      c.cum1[e] = is - (n + L::NB - 1) / L::NB;
+      c.cum2[e] = n > 0 ? ie - 1 : -1;
     }
-    if (e < last) c.cnt[e] = pairs + ip - n;  // first pair of expert e
-    ents += __shfl_sync(0xffffffffu, ie, 31);
-    pairs += __shfl_sync(0xffffffffu, ip, 31);
-    const int subs = __shfl_sync(0xffffffffu, is, 31);
-    u1 += subs * nrb1;
-    u2 += subs * nrb2 * ksplit;
   }
-  if (lane == 0) {
-    c.entries = ents;
-    c.pairs = pairs;
-    c.cum1[ents] = c.units1 = u1;
-    c.cum2[ents] = c.units2 = u2;
-    c.fc2_writers = writers * nrb2 * ksplit;
+  __syncthreads();
+  int4 all = make_int4(0, 0, 0, 0);
+  for (int ch = 0; ch < chunks; ++ch) {
+    const int4 v = c.part[ch];
+    all.x += v.x; all.y += v.y; all.z += v.z; all.w += v.w;
   }
-  __syncwarp();
-  for (int p = lane; p < P; p += 32) {
-    const int e = c.idx[p];
-    if (c.pos_of[p] >= 0 && e >= 0 && e < cf.E) {
-      c.pos_of[p] = (int16_t)(c.cnt[e] + c.pos_of[p]);
-      c.tok_of[c.pos_of[p]] = (uint8_t)(p / cf.K);
-    } else {
-      c.pos_of[p] = -1;
+  // experts and their entries: read everything, then write
+  constexpr int kPer = (kMaxEntries + L::THREADS - 1) / L::THREADS;
+  int4 mine[kPer];  // entry, first pair, sub-units before, pairs
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x + i * L::THREADS;
+    mine[i].x = -1;
+    if (e >= last) continue;
+    int4 b = make_int4(0, 0, 0, 0);
+    for (int ch = 0; ch < e / 32; ++ch) {
+      const int4 v = c.part[ch];
+      b.x += v.x; b.y += v.y; b.z += v.z;
     }
+    int n = __popcll(c.mask[e]);
+    if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
+    mine[i] = make_int4(c.cum2[e] < 0 ? -1 : b.x + c.cum2[e], b.y + c.start[e], b.z + c.cum1[e], n);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x + i * L::THREADS, j = mine[i].x;
+    if (e >= last) continue;
+    c.start[e] = mine[i].y;
+    if (j < 0) continue;
+    c.ent_e[j] = e;
+    c.ent_start[j] = mine[i].y;
+    c.ent_n[j] = mine[i].w;
+    c.cum1[j] = mine[i].z * nrb1;
+    c.cum2[j] = mine[i].z * nrb2 * ksplit;
+  }
+  if (threadIdx.x == 0) {
+    c.pairs = all.y;
+    c.cum1[all.x] = c.units1 = all.z * nrb1;
+    c.cum2[all.x] = c.units2 = all.z * nrb2 * ksplit;
+    c.fc2_writers = all.w * nrb2 * ksplit;
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += L::THREADS) {
+    const int e = c.idx[p], t = p / cf.K;
+    int pos = -1;
+    if (e >= 0 && e < cf.E) {
+      const int rank = __popcll(c.mask[e] & ((1ull << t) - 1));
+      if (cf.capacity == 0 || rank < cf.capacity) {
+        pos = c.start[e] + rank;
+        c.tok_of[pos] = (uint8_t)t;
+      }
+    }
+    c.pos_of[p] = (int16_t)pos;
   }
   if (cf.n_shared)
-    for (int t = lane; t < cf.T; t += 32) c.tok_of[c.cnt[cf.E] + t] = (uint8_t)t;
+    for (int t = threadIdx.x; t < cf.T; t += L::THREADS) c.tok_of[c.start[cf.E] + t] = (uint8_t)t;
+  __syncthreads();
 }
 
 MOE_D int ld_acquire(const int32_t* p) {
@@ -423,8 +462,13 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     ctl.abort = 0;
     tc::fence_barrier_init();
     tc::fence_proxy_async_smem();
+    for (const CUtensorMap* m : {&p.w1, &p.w2, &p.x, &p.act}) tc::prefetch_tensormap(m);
   }
+  for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[e] = 0ull;
   pdl_wait();  // the partial logits, the cleared counters, the fp16 tokens
+  int32_t* claim = p.sync;
+  // the first unit's number comes while the experts are selected
+  const int first_claim = threadIdx.x == 32 * L::NW ? atomicAdd(claim, 1) : 0;
   {
     RouterArgs r = p.r;
     r.topk_idx = ctl.idx;
@@ -443,15 +487,12 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       if (p.a.prob_out) p.a.prob_out[i] = ctl.prob[i];
     }
   }
-  if (warp == 0)
-    few_build_list(ctl, cf, L::NB, glu ? 2 * cf.F : cf.F, cf.h, L::RT, p.ksplit, L::NW, p.a.status);
-  __syncthreads();
+  const int nrb1 = ((glu ? 2 * cf.F : cf.F) + L::RT - 1) / L::RT;
+  few_build_list<L>(ctl, cf, nrb1, (cf.h + L::RT - 1) / L::RT, p.ksplit, p.a.status);
 
-  int32_t* claim = p.sync;
   int32_t* done = p.sync + 2;   // warps that wrote FC1 results, per busy expert
   int32_t* done2 = p.sync + 1;  // warps that wrote FC2 results
   const int width1 = few_rows1<L>(glu);
-  const int nrb1 = ((glu ? 2 * cf.F : cf.F) + L::RT - 1) / L::RT;
   const int total = ctl.units1 + ctl.units2;
   tc::WaitCtl wc{p.a.status, &ctl.abort, p.wait_limit_ns, 0};
   tc::WaitCtl wdrain{p.a.status, nullptr, 1000000000ull, 0};
@@ -461,7 +502,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     if (lane == 0) {
       int stage = 0, j1 = 0, j2 = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
-      int next = atomicAdd(claim, 1);
+      int next = first_claim;
       bool ok = true;
       while (ok) {
         const int u = next;
@@ -608,13 +649,12 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     const int g = lane >> 2, q = lane & 3;
     int stage = 0;
     uint32_t phase = 0;
-    float acc[L::MT][L::NT][4];
+    const int mi = warp % L::MT, ki = warp / L::MT;  // its m-tile and slice of the columns
+    float acc[L::NT][4];
 #pragma unroll
-    for (int m = 0; m < L::MT; ++m)
+    for (int n = 0; n < L::NT; ++n)
 #pragma unroll
-      for (int n = 0; n < L::NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
     // A barrier of the consumer warps that gives up like every other wait (a
     // hardware barrier would hang if one warp had left after a timeout).
     uint32_t meet_par = 0;
@@ -638,77 +678,63 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const int ntiles = (st.n + 7) >> 3;
       // rows of an m-tile's two halves: gate and up rows lie in two blocks
       const bool two = glu && st.kind == kFC1;
-      const int m_step = two ? 8 : 16, hi_row = two ? 8 * L::MT : 8;
+      const int m_row = (two ? 8 : 16) * mi + g, hi_row = two ? 8 * L::MT : 8;
+      uint32_t sw0 = 0, sw1 = 0;  // the scales of 128 columns of the lane's two rows
 #pragma unroll
       for (int c = 0; c < L::KW / 32; ++c) {
-        const int kb = warp * L::KW + c * 32;  // the warp's 32 columns
+        const int kb = ki * L::KW + c * 32;  // 32 columns (zeros past the matrix)
         if (kb >= st.kc) break;
-        const bool in = L::W4 || kb + 8 * q < st.kc;  // ragged ends: multiples of 8
         uint32_t b[L::NT][4];
 #pragma unroll
         for (int n = 0; n < L::NT; ++n) {
           if (n < ntiles) {
             const int row = min(8 * n + g, st.n - 1);
-            uint4 v = lds128(b_s + (kb / L::KB * L::NB + row) * L::B_ROW + (kb % L::KB + 8 * q) * 2);
-            if (!in) v = make_uint4(0, 0, 0, 0);
+            const uint4 v = lds128(b_s + (kb / L::KB * L::NB + row) * L::B_ROW + (kb % L::KB + 8 * q) * 2);
             b[n][0] = v.x; b[n][1] = v.y; b[n][2] = v.z; b[n][3] = v.w;
           }
         }
         if constexpr (!L::W4) {
+          const uint32_t at = a_s + (kb / L::KB * L::RT + m_row) * L::A_ROW + (kb % L::KB + 8 * q) * 2;
+          const uint4 lo = lds128(at), hi = lds128(at + hi_row * L::A_ROW);
 #pragma unroll
-          for (int m = 0; m < L::MT; ++m) {
-            const uint32_t at = a_s + (kb / L::KB * L::RT + m_step * m + g) * L::A_ROW +
-                                (kb % L::KB + 8 * q) * 2;
-            uint4 lo = lds128(at);
-            uint4 hi = lds128(at + hi_row * L::A_ROW);
-            if (!in) lo = hi = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int n = 0; n < L::NT; ++n)
-              if (n < ntiles) {
-                mma16816<false>(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n][0], b[n][1]);
-                mma16816<false>(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n][2], b[n][3]);
-              }
-          }
+          for (int n = 0; n < L::NT; ++n)
+            if (n < ntiles) {
+              mma16816<false>(acc[n], lo.x, hi.x, lo.y, hi.y, b[n][0], b[n][1]);
+              mma16816<false>(acc[n], lo.z, hi.z, lo.w, hi.w, b[n][2], b[n][3]);
+            }
         } else {
           // the fp16 products of one 32-column block, then its scales in fp32
-          float bs[L::NT][2];
-#pragma unroll
-          for (int n = 0; n < L::NT; ++n) {
-            bs[n][0] = bs[n][1] = 1.f;
-            if (st.kind == kFC2 && n < ntiles) {
-              bs[n][0] = __uint_as_float(lds32(bs_s + min(8 * n + 2 * q, st.n - 1) * L::BS_ROW + kb / 32 * 4));
-              bs[n][1] = __uint_as_float(lds32(bs_s + min(8 * n + 2 * q + 1, st.n - 1) * L::BS_ROW + kb / 32 * 4));
-            }
+          if (c % 4 == 0) {
+            const int i0 = (st.r0 + m_row) & 127, i1 = two ? i0 : i0 + 8;
+            const uint32_t at = sf_s + kb / 128 * mx::ATOM;
+            sw0 = lds32(at + 16 * (i0 & 31) + 4 * (i0 >> 5));
+            sw1 = lds32(at + (two ? L::SF / 2 : 0) + 16 * (i1 & 31) + 4 * (i1 >> 5));
           }
+          uint32_t lo[4], hi[4];
+          // 16 bytes hold the block's codes of a row; the swizzle moves them by
+          // the row's place in its group of eight, which is g
+          const uint32_t at = a_s + (kb / L::KB * L::RT + m_row) * L::A_ROW +
+                              (((kb % L::KB) / 32) ^ g) * 16 + 4 * q;
+          e2m1x8_to_f16(lds32(at), lo);
+          e2m1x8_to_f16(lds32(at + hi_row * L::A_ROW), hi);
+          const float s0 = mx::e8m0_value(sw0 >> (8 * (c & 3)) & 255u);
+          const float s1 = mx::e8m0_value(sw1 >> (8 * (c & 3)) & 255u);
 #pragma unroll
-          for (int m = 0; m < L::MT; ++m) {
-            uint32_t lo[4], hi[4];
-            // 16 bytes hold the block's codes of a row; the swizzle moves them by
-            // the row's place in its group of eight, which is g
-            const uint32_t at_c = a_s + (kb / L::KB * L::RT + m_step * m + g) * L::A_ROW +
-                                  (((kb % L::KB) / 32) ^ g) * 16 + 4 * q;
-            e2m1x8_to_f16(lds32(at_c), lo);
-            e2m1x8_to_f16(lds32(at_c + hi_row * L::A_ROW), hi);
-            // rows of the two halves of the m-tile within their 128-row tiles
-            const int i0 = (st.r0 + (two ? 8 * m : 16 * m) + g) & 127;
-            const int i1 = two ? i0 : (i0 + 8);
-            const uint32_t at = kb / 128 * mx::ATOM + (kb / 32 & 3);
-            uint32_t c0, c1;
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c0) : "r"(sf_s + at + 16 * (i0 & 31) + 4 * (i0 >> 5)));
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c1) : "r"(sf_s + (two ? L::SF / 2 : 0) + at + 16 * (i1 & 31) + 4 * (i1 >> 5)));
-            const float s0 = mx::e8m0_value(c0), s1 = mx::e8m0_value(c1);
-#pragma unroll
-            for (int n = 0; n < L::NT; ++n)
-              if (n < ntiles) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816<true>(d, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-                mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-                acc[m][n][0] = fmaf(d[0], s0 * bs[n][0], acc[m][n][0]);
-                acc[m][n][1] = fmaf(d[1], s0 * bs[n][1], acc[m][n][1]);
-                acc[m][n][2] = fmaf(d[2], s1 * bs[n][0], acc[m][n][2]);
-                acc[m][n][3] = fmaf(d[3], s1 * bs[n][1], acc[m][n][3]);
+          for (int n = 0; n < L::NT; ++n)
+            if (n < ntiles) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<true>(d, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
+              mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
+              if (st.kind == kFC2) {  // the tokens' own scales of these columns
+                const float b0 = __uint_as_float(lds32(bs_s + min(8 * n + 2 * q, st.n - 1) * L::BS_ROW + kb / 32 * 4));
+                const float b1 = __uint_as_float(lds32(bs_s + min(8 * n + 2 * q + 1, st.n - 1) * L::BS_ROW + kb / 32 * 4));
+                d[0] *= b0; d[1] *= b1; d[2] *= b0; d[3] *= b1;
               }
-          }
+              acc[n][0] = fmaf(d[0], s0, acc[n][0]);
+              acc[n][1] = fmaf(d[1], s0, acc[n][1]);
+              acc[n][2] = fmaf(d[2], s1, acc[n][2]);
+              acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+            }
         }
       }
       __syncwarp();
@@ -724,24 +750,22 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       // the stores' way to the L2 falls on another warp each time.
       float* mine = red + (unit & 1) * (L::RED / 8);
 #pragma unroll
-      for (int m = 0; m < L::MT; ++m)
-#pragma unroll
-        for (int n = 0; n < L::NT; ++n) {
-          if (n < ntiles) {
-            float* d = mine + (warp * L::NB + 8 * n + 2 * q) * L::RED_TOK + 16 * m + g;
-            d[0] = acc[m][n][0];
-            d[L::RED_TOK] = acc[m][n][1];
-            d[8] = acc[m][n][2];
-            d[L::RED_TOK + 8] = acc[m][n][3];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
+      for (int n = 0; n < L::NT; ++n) {
+        if (n < ntiles) {
+          float* d = mine + (ki * L::NB + 8 * n + 2 * q) * L::RED_TOK + 16 * mi + g;
+          d[0] = acc[n][0];
+          d[L::RED_TOK] = acc[n][1];
+          d[8] = acc[n][2];
+          d[L::RED_TOK + 8] = acc[n][3];
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+      }
       if (!meet()) break;
       auto sum = [&](int tok, int row) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < L::NW; ++w) v += mine[(w * L::NB + tok) * L::RED_TOK + row];
+        for (int w = 0; w < L::KG; ++w) v += mine[(w * L::NB + tok) * L::RED_TOK + row];
         return v;
       };
       const int rw = (warp + L::NW - unit % L::NW) % L::NW;  // place among the writers
@@ -808,25 +832,39 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
            i += (int64_t)gridDim.x * L::NW * 32) {
         const int t = (int)(2 * i / cf.h), r = (int)(2 * i - (int64_t)t * cf.h);
         float2 y = make_float2(0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < slots; ++k) {
-          const bool shared = k == cf.K;
-          const int pr = t * cf.K + k;
-          const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
-          if (pos < 0) continue;  // dropped
-          const float w = shared ? 1.f : ctl.prob[pr];
-          float2 o = make_float2(0.f, 0.f);
-          if (cf.has_bias) {
-            const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
-            o = make_float2(to_f32(b[0]), to_f32(b[1]));
+        constexpr int kBatch = 4;  // slots whose loads go out together
+        for (int k0 = 0; k0 < slots; k0 += kBatch) {
+          float2 o[kBatch];
+          float w[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int k = k0 + j;
+            const bool shared = k == cf.K;
+            const int pr = t * cf.K + min(k, cf.K - 1);
+            const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
+            const bool there = k < slots && pos >= 0;  // else past the end, or dropped
+            w[j] = shared ? 1.f : ctl.prob[pr];
+            o[j] = make_float2(0.f, 0.f);
+            if (!there) w[j] = 0.f;
+            if (there && cf.has_bias && !shared) {
+              const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
+              o[j] = make_float2(to_f32(b[0]), to_f32(b[1]));
+            }
+            if (there) {
+              const float* src = p.ypart + (int64_t)pos * cf.h + r;
+              const int64_t step = (int64_t)p.S * cf.h;
+              for (int s = 0; s < p.ksplit; ++s) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(src + s * step));
+                o[j].x += v.x;
+                o[j].y += v.y;
+              }
+            }
           }
-          for (int s = 0; s < p.ksplit; ++s) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ypart + ((int64_t)s * p.S + pos) * cf.h + r));
-            o.x += v.x;
-            o.y += v.y;
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            y.x = fmaf(w[j], o[j].x, y.x);
+            y.y = fmaf(w[j], o[j].y, y.y);
           }
-          y.x = fmaf(w, o.x, y.x);
-          y.y = fmaf(w, o.y, y.y);
         }
         *reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r) = __floats2bfloat162_rn(y.x, y.y);
       }
@@ -925,10 +963,12 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
       xh, const_cast<float*>(p.xs), p.sync, (int)few_sync_words(c));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (mxfp4) return c.T <= 8 ? few_launch<FewTile<true, 4, 1, 8>>(p, xh, s) : few_launch<FewTile<true, 4, 2, 8>>(p, xh, s);
-  if (c.T <= 8) return few_launch<FewTile<false, 1, 1, 8>>(p, xh, s);
-  if (c.T <= 16) return few_launch<FewTile<false, 2, 2, 8>>(p, xh, s);
-  return few_launch<FewTile<false, 2, 4, 8>>(p, xh, s);
+  if (mxfp4)
+    return c.T <= 8 ? few_launch<FewTile<true, 4, 1, 16, 512>>(p, xh, s)
+                    : few_launch<FewTile<true, 4, 2, 16, 512>>(p, xh, s);
+  if (c.T <= 8) return few_launch<FewTile<false, 2, 1, 8, 512>>(p, xh, s);
+  if (c.T <= 16) return few_launch<FewTile<false, 2, 2, 8, 512>>(p, xh, s);
+  return few_launch<FewTile<false, 2, 4, 8, 256>>(p, xh, s);
 }
 
 }  // namespace moe

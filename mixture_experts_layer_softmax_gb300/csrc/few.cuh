@@ -20,9 +20,8 @@ inline int few_kparts(const moe_config_t& c) {
 
 // FC2's reduction (F) is cut into slices of at most 4096 columns whose partial
 // results are added in order: units stay small enough to spread evenly.
-constexpr int kFewKC = 512;  // columns per pipeline stage
 inline int few_ksplit(const moe_config_t& c) {
-  return (int)ceil_div(ceil_div(c.F, kFewKC), 4096 / kFewKC);
+  return (int)ceil_div(c.F, 4096);
 }
 
 struct FewLayout {

@@ -171,6 +171,7 @@ BF16 = [
     dict(T=5, h=1032, E=256, K=8, F=72, score=1, sel=True, shared=1),
     dict(T=7, h=264, E=5, K=2, F=1000, act=0, bias=True),
     dict(T=8, h=512, E=3, K=3, F=264, act=0),
+    dict(T=11, h=296, E=6, K=3, F=200, act=0, bias=True, shared=1),
     dict(T=9, h=256, E=1, K=1, F=520, gate=True),                    # one expert has every token
     dict(T=16, h=1024, E=8, K=2, F=512, shared=1),
     dict(T=17, h=776, E=100, K=16, F=88, renorm=False, score=1),
