@@ -5,19 +5,22 @@
 //
 // The expert weights are the traffic: each busy expert's matrices are read
 // from HBM for a handful of rows.  bf16 weights, or MXFP4 weights (E2M1 codes
-// with one E8M0 scale per 32 columns).
+// with one E8M0 scale per 32 columns; scale code 0, 2^-127, counts as zero: what
+// it scales is below fp32's normal numbers).
 //
-// Two launches.  few_router_kernel writes partial logits (and, for MXFP4
-// weights, the tokens in fp16).  few_kernel does the rest, one block per SM:
-//   every block selects the experts of all tokens and sorts the (token, slot)
-//   pairs by expert (the same list everywhere), then takes units of work from
-//   one counter: first all of FC1's units (an expert, a block of its rows),
-//   then FC2's (an expert, a block of rows of h, a slice of F).  An FC2 unit
-//   waits until its expert's FC1 units are done.  Units are taken in order, so
-//   every FC1 unit that an FC2 unit waits for belongs to a block that already
-//   runs and waits for nothing: no block needs any other to become resident.
+// Three launches, each started while the one before drains (programmatic
+// dependent launch).  few_router_kernel writes partial logits (and, for MXFP4
+// weights, the tokens in fp16); few_select_kernel adds them and selects, a warp
+// a token.  few_kernel does the rest, one block per SM:
+//   every block sorts the (token, slot) pairs by expert (the same list
+//   everywhere), then takes units of work from one counter: first all of FC1's
+//   units (an expert, a block of its rows), then FC2's (an expert, a block of
+//   rows of h, a slice of F).  An FC2 unit waits until its expert's FC1 units
+//   are done.  Units are taken in order, so every FC1 unit that an FC2 unit
+//   waits for belongs to a block that already runs and waits for nothing: no
+//   block needs any other to become resident.
 //   When all FC2 units are done every block adds its share of the slots'
-//   results, in slot order, and writes y.
+//   results, in a fixed order, and writes y.
 // Within a block: two producer warps stream the unit's weight rows and the
 // expert's token rows through a ring of shared-memory stages (512 columns a
 // stage, TMA boxes of many rows: a copy per row costs its issuing warp about
@@ -103,13 +106,14 @@ __global__ void __launch_bounds__(256)
     few_convert_token(x + (int64_t)t * h, h, xh + (int64_t)t * h, xs + t);
     return;
   }
+  // one warp per (expert, slice, eight tokens)
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (unit >= E * kparts) return;
-  const int e = unit % E, part = unit / E;
+  if (unit >= E * kparts * (int)ceil_div(T, kRouteTok)) return;
+  const int e = unit % E, part = unit / E % kparts, t0 = unit / (E * kparts) * kRouteTok;
   const int vecs = h / 8;  // 16-byte vectors of x
   const int v0 = (int)((int64_t)vecs * part / kparts), v1 = (int)((int64_t)vecs * (part + 1) / kparts);
   const float* w = w_r + (int64_t)e * h;
-  for (int t0 = 0; t0 < T; t0 += kRouteTok) {
+  {
     float acc[kRouteTok];
 #pragma unroll
     for (int j = 0; j < kRouteTok; ++j) acc[j] = 0.f;
@@ -135,35 +139,99 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One token's logits (the slices added in order) and its selection: a warp.
-// All experts' loads of four slices go out together: their latency, not their
-// number, is what a decoding step waits for here.
-template <int J>
-MOE_D void few_select_token(const float* parts, int kparts, const float* gate_bias, int t,
-                            const RouterArgs& r, int lane) {
-  float l[J];
+// The full selection on one token's logits (router_select.cuh), by a warp; out of
+// line, for the rare token whose fp32 sigmoid keys are too close to rank.
+__device__ __noinline__ void few_select_exact(const float* logit, int t, RouterArgs r, int lane) {
+  float l[8];
 #pragma unroll
-  for (int j = 0; j < J; ++j) l[j] = 0.f;
-  for (int p0 = 0; p0 < kparts; p0 += 4) {
-    float v[J][4];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = lane + 32 * j;
-        v[j][i] = e < r.E && p0 + i < kparts
-                      ? __ldcg(parts + ((int64_t)(p0 + i) * r.T + t) * r.E + e) : 0.f;
-      }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) l[j] += v[j][i];
+  for (int j = 0; j < 8; ++j) l[j] = lane + 32 * j < r.E ? logit[lane + 32 * j] : 0.f;
+  select_and_write<8>(l, t, r, lane);
+}
+
+// Adds the partial logits and selects: a block a token, a thread an expert, with
+// select_and_write's choices.  A decoding step runs this code once, from a cold
+// instruction cache, and the fetches are what it waits for (select_and_write in
+// a warp took 13 us for one token of 256 experts): so each thread ranks its
+// expert by counting the keys above its own, in a short loop.  The results are
+// written kFewCopies times: each block of few_kernel reads one of the copies.
+__global__ void __launch_bounds__(256)
+    few_select_kernel(const float* __restrict__ parts, int kparts, const float* gate_bias,
+                      RouterArgs r, int pairs_pad, int32_t* idx_out, float* prob_out) {
+  __shared__ float s_logit[256];
+  __shared__ __align__(16) uint32_t s_key[256];
+  __shared__ int s_sel[32];
+  __shared__ float s_prob[16];
+  const unsigned FULL = 0xffffffffu;
+  const int e = threadIdx.x, t = blockIdx.x, lane = threadIdx.x & 31;
+  const bool sig = r.score == MOE_SCORE_SIGMOID;
+  pdl_trigger();
+  pdl_wait();
+  float l = 0.f;
+  uint32_t key = 0u;  // order-preserving, 0 past E
+  if (e < r.E) {
+#pragma unroll 4
+    for (int p = 0; p < kparts; ++p) l += __ldcg(parts + ((int64_t)p * r.T + t) * r.E + e);
+    if (gate_bias) l += __ldg(gate_bias + e);
+    key = sortable_key(selection_key_fast(l, e, r));
   }
-  if (gate_bias)
+  s_logit[e] = l;
+  s_key[e] = key;
+  if (e < 32) s_sel[e] = 0;
+  __syncthreads();
+  if (r.force_balance) {
+    if (e < r.K) s_sel[e] = (int)(((int64_t)t * r.K + e) % r.E);
+  } else if (e < r.E) {
+    int rank = 0;  // equal keys: the lower expert first
+#pragma unroll 2
+    for (int j = 0; j < r.E; j += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
+      rank += (k.x > key || (k.x == key && j < e)) + (k.y > key || (k.y == key && j + 1 < e)) +
+              (k.z > key || (k.z == key && j + 2 < e)) + (k.w > key || (k.w == key && j + 3 < e));
+    }
+    if (rank <= r.K) s_sel[rank] = e;  // the (K+1)-th too: its gap is looked at
+  }
+  __syncthreads();
+  if (e >= 32) return;
+  const int my = s_sel[lane];
+  bool close = false;  // sigmoid: two of the best K + 1 keys within their error bound
+  if (sig && !r.force_balance && lane >= 1 && lane < min(r.K + 1, r.E)) {
+    const float prev = from_sortable_key(s_key[s_sel[lane - 1]]), cur = from_sortable_key(s_key[my]);
+    close = !(prev - cur > 4e-6f * (1.f + fabsf(prev) + fabsf(cur)));
+  }
+  if (__any_sync(FULL, close)) {
+    RouterArgs w = r;  // the results in shared memory, as below
+    w.topk_idx = s_sel - (int64_t)t * r.K;
+    w.topk_prob = s_prob - (int64_t)t * r.K;
+    few_select_exact(s_logit, t, w, lane);
+  } else {
+    const bool active = lane < r.K;
+    const float ml = s_logit[my];
+    float m = 0.f, num, den = 0.f;
+    if (!sig) {
+      m = active ? ml : -INFINITY;
+      if (!r.renorm)
+        for (int j = lane; j < r.E; j += 32) m = fmaxf(m, s_logit[j]);
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (lane + 32 * j < r.E) l[j] += __ldg(gate_bias + lane + 32 * j);
-  select_and_write<J>(l, t, r, lane);
+      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+    }
+    num = active ? (sig ? sigmoid_f(ml) : expf(ml - m)) : 0.f;
+    if (r.renorm) den = num;
+    else
+      for (int j = lane; j < r.E; j += 32) den += sig ? sigmoid_f(s_logit[j]) : expf(s_logit[j] - m);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) den += __shfl_xor_sync(FULL, den, o);
+    if (active) s_prob[lane] = num / den;
+  }
+  __syncwarp();
+  for (int i = lane; i < kFewCopies * r.K; i += 32) {
+    const int k = i % r.K, at = i / r.K * pairs_pad + t * r.K + k;
+    r.topk_idx[at] = s_sel[k];
+    r.topk_prob[at] = s_prob[k];
+  }
+  if (lane < r.K) {
+    if (idx_out) idx_out[t * r.K + lane] = s_sel[lane];
+    if (prob_out) prob_out[t * r.K + lane] = s_prob[lane];
+  }
 }
 
 // ---- units ------------------------------------------------------------------------
@@ -198,7 +266,6 @@ struct FewCtl {
   int cum1[kMaxEntries + 1], cum2[kMaxEntries + 1];  // units before entry j
   int start[kMaxEntries];                // first sorted pair of an expert
   unsigned long long mask[kMaxEntries];  // tokens of an expert
-  int4 part[9];                          // a 32-expert chunk's entries, pairs, sub-units, writers
   int idx[kMaxPairs];
   float prob[kMaxPairs];
   int16_t pos_of[kMaxPairs];     // sorted position of pair p, -1: dropped
@@ -210,9 +277,9 @@ struct FewParams {
   // hidden values and their scales as (columns, rows)
   CUtensorMap w1, w2, w1s, w2s, x, act, act_s;
   FewArgs a;
-  RouterArgs r;
-  const float* parts;
-  int kparts;
+  const int32_t* idx;  // kFewCopies copies of the selection, pairs_pad apart
+  const float* prob;
+  int pairs_pad;
   int32_t* sync;
   const float* xs;
   void* hidden;      // bf16, or fp16 with hidden_s (MXFP4 weights)
@@ -223,15 +290,15 @@ struct FewParams {
   uint64_t wait_limit_ns;
 };
 
-// RT = 16 MT weight rows of a unit, NB = 8 NT tokens, NW consumer warps: MT of
-// them share a slice of a stage's KC columns, one m-tile each.
-template <bool W4_, int MT_, int NT_, int NW_, int KC_>
+// RT = 16 MT weight rows of a unit, NB = 8 NT tokens, NW consumer warps of MPW
+// m-tiles each: MT / MPW of them share a slice of a stage's KC columns.
+template <bool W4_, int MT_, int MPW_, int NT_, int NW_, int KC_>
 struct FewTile {
   static constexpr bool W4 = W4_;
-  static constexpr int MT = MT_, NT = NT_, NW = NW_, KC = KC_;
+  static constexpr int MT = MT_, MPW = MPW_, NT = NT_, NW = NW_, KC = KC_;
   static constexpr int RT = 16 * MT;  // weight rows of a unit
   static constexpr int NB = 8 * NT;   // tokens of a unit
-  static constexpr int KG = NW / MT, KW = KC / KG;  // slices and their columns
+  static constexpr int MG = MT / MPW, KG = NW / MG, KW = KC / KG;  // slices and their columns
   // A stage holds KC / 256 boxes of 256 columns, rows one after the other.
   // bf16 rows are 512 bytes, unswizzled: two of a quarter-warp's eight 16-byte
   // loads meet in a bank, which the shared-memory bandwidth has room for.
@@ -243,9 +310,12 @@ struct FewTile {
   static constexpr int BS_ROW = W4 ? KC / 32 * 4 : 0;
   static constexpr int STAGE = (A_BYTES + B_BYTES + SF + NB * BS_ROW + 1023) / 1024 * 1024;
   static constexpr int RED_TOK = RT + 4;  // padded token stride of the meeting buffer
-  static constexpr int RED = 2 * KG * NB * RED_TOK * 4;  // two units in turn
+  static constexpr int REDS = NT >= 4 ? 1 : 2;  // meeting buffers
+  static constexpr int RED1 = KG * NB * RED_TOK * 4, RED = REDS * RED1;
   static constexpr int THREADS = 32 * (NW + 2);
-  static_assert(NW % MT == 0 && NW >= 8 && KW % (W4 ? 128 : 32) == 0, "whole scale words per warp");
+  static_assert(MT % MPW == 0 && NW % MG == 0 && NW >= 8 && KB % KW == 0 &&
+                    KW % (W4 ? 128 : 32) == 0,
+                "whole blocks per warp");
 };
 
 // Warps that write the results of a unit of n tokens by `width` values, and of
@@ -273,68 +343,45 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
   }
   if (threadIdx.x == 0 && cf.n_shared) c.mask[cf.E] = ~0ull >> (64 - cf.T);
   __syncthreads();
-  // a 32-expert chunk a warp; the shared expert is one more expert
-  const int last = cf.E + (cf.n_shared ? 1 : 0), chunks = (last + 31) / 32;
-  for (int ch = warp; ch < chunks; ch += L::NW + 2) {
-    const int e = ch * 32 + lane;
-    int n = e < last ? __popcll(c.mask[e]) : 0;
-    if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
-    int ie = n > 0 ? 1 : 0, ip = n, is = (n + L::NB - 1) / L::NB;
-    int iw = few_writers_of(n, L::NB, L::RT, L::NW);
+  // busy experts in order, 32 experts a step (the shared expert is one more);
+  // a loop of few instructions, as they are fetched once
+  if (warp == 0) {
+    const int last = cf.E + (cf.n_shared ? 1 : 0);
+    int ents = 0, pairs = 0, subs = 0, writers = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < last; e0 += 32) {
+      const int e = e0 + lane;
+      int n = e < last ? __popcll(c.mask[e]) : 0;
+      if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
+      const uint32_t busy = __ballot_sync(0xffffffffu, n > 0);
+      if (busy == 0) continue;
+      const int sub = (n + L::NB - 1) / L::NB;
+      int ip = n, is = sub;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, ie, o), b = __shfl_up_sync(0xffffffffu, ip, o),
-                d = __shfl_up_sync(0xffffffffu, is, o), f = __shfl_up_sync(0xffffffffu, iw, o);
-      if (lane >= o) { ie += a; ip += b; is += d; iw += f; }
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, ip, o), b = __shfl_up_sync(0xffffffffu, is, o);
+        if (lane >= o) { ip += a; is += b; }
+      }
+      if (n > 0) {
+        const int j = ents + __popc(busy & ((1u << lane) - 1));
+        c.start[e] = c.ent_start[j] = pairs + ip - n;
+        c.ent_e[j] = e;
+        c.ent_n[j] = n;
+        c.cum1[j] = (subs + is - sub) * nrb1;
+        c.cum2[j] = (subs + is - sub) * nrb2 * ksplit;
+        writers += few_writers_of(n, L::NB, L::RT, L::NW);
+      }
+      ents += __popc(busy);
+      pairs += __shfl_sync(0xffffffffu, ip, 31);
+      subs += __shfl_sync(0xffffffffu, is, 31);
     }
-    if (lane == 31) c.part[ch] = make_int4(ie, ip, is, iw);
-    if (e < last) {  // within the chunk, for now
-      c.start[e] = ip - n;
-      c.cum1[e] = is - (n + L::NB - 1) / L::NB;
-      c.cum2[e] = n > 0 ? ie - 1 : -1;
+    writers = __reduce_add_sync(0xffffffffu, writers);
+    if (lane == 0) {
+      c.pairs = pairs;
+      c.cum1[ents] = c.units1 = subs * nrb1;
+      c.cum2[ents] = c.units2 = subs * nrb2 * ksplit;
+      c.fc2_writers = writers * nrb2 * ksplit;
     }
-  }
-  __syncthreads();
-  int4 all = make_int4(0, 0, 0, 0);
-  for (int ch = 0; ch < chunks; ++ch) {
-    const int4 v = c.part[ch];
-    all.x += v.x; all.y += v.y; all.z += v.z; all.w += v.w;
-  }
-  // experts and their entries: read everything, then write
-  constexpr int kPer = (kMaxEntries + L::THREADS - 1) / L::THREADS;
-  int4 mine[kPer];  // entry, first pair, sub-units before, pairs
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = threadIdx.x + i * L::THREADS;
-    mine[i].x = -1;
-    if (e >= last) continue;
-    int4 b = make_int4(0, 0, 0, 0);
-    for (int ch = 0; ch < e / 32; ++ch) {
-      const int4 v = c.part[ch];
-      b.x += v.x; b.y += v.y; b.z += v.z;
-    }
-    int n = __popcll(c.mask[e]);
-    if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
-    mine[i] = make_int4(c.cum2[e] < 0 ? -1 : b.x + c.cum2[e], b.y + c.start[e], b.z + c.cum1[e], n);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = threadIdx.x + i * L::THREADS, j = mine[i].x;
-    if (e >= last) continue;
-    c.start[e] = mine[i].y;
-    if (j < 0) continue;
-    c.ent_e[j] = e;
-    c.ent_start[j] = mine[i].y;
-    c.ent_n[j] = mine[i].w;
-    c.cum1[j] = mine[i].z * nrb1;
-    c.cum2[j] = mine[i].z * nrb2 * ksplit;
-  }
-  if (threadIdx.x == 0) {
-    c.pairs = all.y;
-    c.cum1[all.x] = c.units1 = all.z * nrb1;
-    c.cum2[all.x] = c.units2 = all.z * nrb2 * ksplit;
-    c.fc2_writers = all.w * nrb2 * ksplit;
   }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += L::THREADS) {
@@ -398,6 +445,15 @@ MOE_D void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The fp16 product alone (a zero addend).
+MOE_D void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                         uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+               "{%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Eight E2M1 codes -> eight fp16 values (exact), in order.
 MOE_D void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
@@ -410,13 +466,20 @@ MOE_D void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
       : "r"(w));
 }
 
-// A box of a 3-D tensor map (as tc::tma_load_2d).
+// A box of a 3-D tensor map (as tc::tma_load_2d), first to leave the L2: weights
+// are read once, and what they would push out is the code, the router's weight
+// and the hidden values.
+MOE_D uint64_t evict_first_policy() {
+  uint64_t v;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(v));
+  return v;
+}
 MOE_D void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
-                       uint32_t bar) {
+                       uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -465,28 +528,18 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     for (const CUtensorMap* m : {&p.w1, &p.w2, &p.x, &p.act}) tc::prefetch_tensormap(m);
   }
   for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[e] = 0ull;
-  pdl_wait();  // the partial logits, the cleared counters, the fp16 tokens
+  pdl_wait();  // the selection, and with it the cleared counters and the fp16 tokens
   int32_t* claim = p.sync;
-  // the first unit's number comes while the experts are selected
+  // the first unit's number comes while the list is made
   const int first_claim = threadIdx.x == 32 * L::NW ? atomicAdd(claim, 1) : 0;
   {
-    RouterArgs r = p.r;
-    r.topk_idx = ctl.idx;
-    r.topk_prob = ctl.prob;
-    for (int t = warp; t < cf.T; t += L::NW + 2) {
-      if (cf.E <= 32) few_select_token<1>(p.parts, p.kparts, p.a.gate_bias, t, r, lane);
-      else if (cf.E <= 64) few_select_token<2>(p.parts, p.kparts, p.a.gate_bias, t, r, lane);
-      else if (cf.E <= 128) few_select_token<4>(p.parts, p.kparts, p.a.gate_bias, t, r, lane);
-      else few_select_token<8>(p.parts, p.kparts, p.a.gate_bias, t, r, lane);
+    const int64_t at = (int64_t)(blockIdx.x % kFewCopies) * p.pairs_pad;
+    for (int i = threadIdx.x; i < cf.T * cf.K; i += L::THREADS) {
+      ctl.idx[i] = __ldcg(p.idx + at + i);
+      ctl.prob[i] = __ldcg(p.prob + at + i);
     }
   }
   __syncthreads();
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < cf.T * cf.K; i += L::THREADS) {
-      if (p.a.idx_out) p.a.idx_out[i] = ctl.idx[i];
-      if (p.a.prob_out) p.a.prob_out[i] = ctl.prob[i];
-    }
-  }
   const int nrb1 = ((glu ? 2 * cf.F : cf.F) + L::RT - 1) / L::RT;
   few_build_list<L>(ctl, cf, nrb1, (cf.h + L::RT - 1) / L::RT, p.ksplit, p.a.status);
 
@@ -502,6 +555,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     if (lane == 0) {
       int stage = 0, j1 = 0, j2 = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
+      const uint64_t policy = evict_first_policy();
       int next = first_claim;
       bool ok = true;
       while (ok) {
@@ -574,7 +628,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           const uint32_t a_dst = ring0 + stage * L::STAGE;
           for (int b = 0; b < nkb; ++b)
             tma_load_3d(a_dst + b * L::RT * L::A_ROW, map, (k0 + b * L::KB) / (L::W4 ? 2 : 1),
-                        st.r0, half0, fb);
+                        st.r0, half0, fb, policy);
           if (L::W4) {  // the scales of the unit's rows: atoms of their 128-row tile
             const uint32_t sf_dst = a_dst + L::A_BYTES + L::B_BYTES;
             for (int i = 0; i < (pairs_of_rows ? 2 : 1); ++i) {
@@ -649,12 +703,15 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     const int g = lane >> 2, q = lane & 3;
     int stage = 0;
     uint32_t phase = 0;
-    const int mi = warp % L::MT, ki = warp / L::MT;  // its m-tile and slice of the columns
-    float acc[L::NT][4];
+    const int mi = warp % L::MG * L::MPW, ki = warp / L::MG;  // its first m-tile, its columns
+    const int k_w = ki * L::KW;
+    float acc[L::MPW][L::NT][4];
 #pragma unroll
-    for (int n = 0; n < L::NT; ++n)
+    for (int m = 0; m < L::MPW; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+      for (int n = 0; n < L::NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
     // A barrier of the consumer warps that gives up like every other wait (a
     // hardware barrier would hang if one warp had left after a timeout).
     uint32_t meet_par = 0;
@@ -678,63 +735,98 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const int ntiles = (st.n + 7) >> 3;
       // rows of an m-tile's two halves: gate and up rows lie in two blocks
       const bool two = glu && st.kind == kFC1;
-      const int m_row = (two ? 8 : 16) * mi + g, hi_row = two ? 8 * L::MT : 8;
-      uint32_t sw0 = 0, sw1 = 0;  // the scales of 128 columns of the lane's two rows
+      const int m_step = two ? 8 : 16, hi_row = two ? 8 * L::MT : 8;
+      const int m_row = m_step * mi + g;
+      uint32_t b_at[L::NT];  // the lane's token rows; past the last one, the last
 #pragma unroll
-      for (int c = 0; c < L::KW / 32; ++c) {
-        const int kb = ki * L::KW + c * 32;  // 32 columns (zeros past the matrix)
-        if (kb >= st.kc) break;
-        uint32_t b[L::NT][4];
+      for (int n = 0; n < L::NT; ++n)
+        b_at[n] = b_s + (k_w / L::KB * L::NB + min(8 * n + g, st.n - 1)) * L::B_ROW +
+                  (k_w % L::KB + 8 * q) * 2;
+      // the lane's weight rows
+      const uint32_t a_at = a_s + (k_w / L::KB * L::RT + m_row) * L::A_ROW +
+                            (L::W4 ? 4 * q : (k_w % L::KB + 8 * q) * 2);
+      if constexpr (!L::W4) {
 #pragma unroll
-        for (int n = 0; n < L::NT; ++n) {
-          if (n < ntiles) {
-            const int row = min(8 * n + g, st.n - 1);
-            const uint4 v = lds128(b_s + (kb / L::KB * L::NB + row) * L::B_ROW + (kb % L::KB + 8 * q) * 2);
-            b[n][0] = v.x; b[n][1] = v.y; b[n][2] = v.z; b[n][3] = v.w;
+        for (int c = 0; c < L::KW / 32; ++c) {
+          if (k_w + c * 32 >= st.kc) break;  // (the boxes are zero past the matrix)
+          uint4 b[L::NT];
+#pragma unroll
+          for (int n = 0; n < L::NT; ++n)
+            if (n < ntiles) b[n] = lds128(b_at[n] + c * 64);
+#pragma unroll
+          for (int m = 0; m < L::MPW; ++m) {
+            const uint4 lo = lds128(a_at + m * m_step * L::A_ROW + c * 64);
+            const uint4 hi = lds128(a_at + (m * m_step + hi_row) * L::A_ROW + c * 64);
+#pragma unroll
+            for (int n = 0; n < L::NT; ++n)
+              if (n < ntiles) {
+                mma16816<false>(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n].x, b[n].y);
+                mma16816<false>(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n].z, b[n].w);
+              }
           }
         }
-        if constexpr (!L::W4) {
-          const uint32_t at = a_s + (kb / L::KB * L::RT + m_row) * L::A_ROW + (kb % L::KB + 8 * q) * 2;
-          const uint4 lo = lds128(at), hi = lds128(at + hi_row * L::A_ROW);
+      } else {
 #pragma unroll
-          for (int n = 0; n < L::NT; ++n)
-            if (n < ntiles) {
-              mma16816<false>(acc[n], lo.x, hi.x, lo.y, hi.y, b[n][0], b[n][1]);
-              mma16816<false>(acc[n], lo.z, hi.z, lo.w, hi.w, b[n][2], b[n][3]);
-            }
-        } else {
-          // the fp16 products of one 32-column block, then its scales in fp32
-          if (c % 4 == 0) {
-            const int i0 = (st.r0 + m_row) & 127, i1 = two ? i0 : i0 + 8;
-            const uint32_t at = sf_s + kb / 128 * mx::ATOM;
-            sw0 = lds32(at + 16 * (i0 & 31) + 4 * (i0 >> 5));
-            sw1 = lds32(at + (two ? L::SF / 2 : 0) + 16 * (i1 & 31) + 4 * (i1 >> 5));
+        for (int c4 = 0; c4 < L::KW / 128; ++c4) {  // 128 columns: one word of scales a row
+          if (k_w + c4 * 128 >= st.kc) break;
+          const uint32_t sf_at = sf_s + (k_w / 128 + c4) * mx::ATOM;
+          uint32_t sw[L::MPW][2];
+#pragma unroll
+          for (int m = 0; m < L::MPW; ++m) {
+            const int i0 = (st.r0 + m_row + m * m_step) & 127, i1 = two ? i0 : i0 + 8;
+            sw[m][0] = lds32(sf_at + 16 * (i0 & 31) + 4 * (i0 >> 5));
+            sw[m][1] = lds32(sf_at + (two ? L::SF / 2 : 0) + 16 * (i1 & 31) + 4 * (i1 >> 5));
           }
-          uint32_t lo[4], hi[4];
-          // 16 bytes hold the block's codes of a row; the swizzle moves them by
-          // the row's place in its group of eight, which is g
-          const uint32_t at = a_s + (kb / L::KB * L::RT + m_row) * L::A_ROW +
-                              (((kb % L::KB) / 32) ^ g) * 16 + 4 * q;
-          e2m1x8_to_f16(lds32(at), lo);
-          e2m1x8_to_f16(lds32(at + hi_row * L::A_ROW), hi);
-          const float s0 = mx::e8m0_value(sw0 >> (8 * (c & 3)) & 255u);
-          const float s1 = mx::e8m0_value(sw1 >> (8 * (c & 3)) & 255u);
+          // the tokens' own scales of these columns (FC2)
+          float ts[L::NT][2][4];
+          if (st.kind == kFC2) {
 #pragma unroll
-          for (int n = 0; n < L::NT; ++n)
-            if (n < ntiles) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<true>(d, lo[0], hi[0], lo[1], hi[1], b[n][0], b[n][1]);
-              mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n][2], b[n][3]);
-              if (st.kind == kFC2) {  // the tokens' own scales of these columns
-                const float b0 = __uint_as_float(lds32(bs_s + min(8 * n + 2 * q, st.n - 1) * L::BS_ROW + kb / 32 * 4));
-                const float b1 = __uint_as_float(lds32(bs_s + min(8 * n + 2 * q + 1, st.n - 1) * L::BS_ROW + kb / 32 * 4));
-                d[0] *= b0; d[1] *= b1; d[2] *= b0; d[3] *= b1;
+            for (int n = 0; n < L::NT; ++n)
+              if (n < ntiles) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint4 v = lds128(bs_s + min(8 * n + 2 * q + i, st.n - 1) * L::BS_ROW +
+                                         (k_w / 32 + c4 * 4) * 4);
+                  ts[n][i][0] = __uint_as_float(v.x); ts[n][i][1] = __uint_as_float(v.y);
+                  ts[n][i][2] = __uint_as_float(v.z); ts[n][i][3] = __uint_as_float(v.w);
+                }
               }
-              acc[n][0] = fmaf(d[0], s0, acc[n][0]);
-              acc[n][1] = fmaf(d[1], s0, acc[n][1]);
-              acc[n][2] = fmaf(d[2], s1, acc[n][2]);
-              acc[n][3] = fmaf(d[3], s1, acc[n][3]);
+          }
+          // 16 bytes hold a 32-column block's codes of a row; the swizzle moves
+          // them by the row's place in its group of eight, which is g
+          const uint32_t sw16 = (((k_w % L::KB) / 32 + 4 * c4) ^ g) * 16;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4 b[L::NT];
+#pragma unroll
+            for (int n = 0; n < L::NT; ++n)
+              if (n < ntiles) b[n] = lds128(b_at[n] + (4 * c4 + c) * 64);
+#pragma unroll
+            for (int m = 0; m < L::MPW; ++m) {
+              uint32_t lo[4], hi[4];
+              const uint32_t at = a_at + m * m_step * L::A_ROW + (sw16 ^ (16 * c));
+              e2m1x8_to_f16(lds32(at), lo);
+              e2m1x8_to_f16(lds32(at + hi_row * L::A_ROW), hi);
+              const float s0 = __uint_as_float((c < 3 ? sw[m][0] << (23 - 8 * c) : sw[m][0] >> 1) & 0x7f800000u);
+              const float s1 = __uint_as_float((c < 3 ? sw[m][1] << (23 - 8 * c) : sw[m][1] >> 1) & 0x7f800000u);
+#pragma unroll
+              for (int n = 0; n < L::NT; ++n)
+                if (n < ntiles) {
+                  // the fp16 products of one block, then its scales in fp32
+                  float d[4];
+                  mma16816_zero(d, lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
+                  mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
+                  if (st.kind == kFC2) {
+                    d[0] *= ts[n][0][c]; d[1] *= ts[n][1][c];
+                    d[2] *= ts[n][0][c]; d[3] *= ts[n][1][c];
+                  }
+                  acc[m][n][0] = fmaf(d[0], s0, acc[m][n][0]);
+                  acc[m][n][1] = fmaf(d[1], s0, acc[m][n][1]);
+                  acc[m][n][2] = fmaf(d[2], s1, acc[m][n][2]);
+                  acc[m][n][3] = fmaf(d[3], s1, acc[m][n][3]);
+                }
             }
+          }
         }
       }
       __syncwarp();
@@ -743,24 +835,27 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       if (!st.last) continue;
 
       // ---- the unit's end: the warps' sums meet ----
-      // One meeting a unit: the buffers alternate, so the next unit's sums go
+      // One meeting a unit where there are two buffers: they alternate, so the next unit's sums go
       // elsewhere while this unit's are read, and the unit after that comes
       // past the next meeting.  The results are written by the first warps,
       // counted from a warp that moves on with every unit, so that the wait for
       // the stores' way to the L2 falls on another warp each time.
-      float* mine = red + (unit & 1) * (L::RED / 8);
+      float* mine = red + (L::REDS == 2 ? (unit & 1) * (L::RED1 / 4) : 0);
+      if (L::REDS == 1 && unit > 0 && !meet()) break;  // one buffer: the last unit's sums are read
 #pragma unroll
-      for (int n = 0; n < L::NT; ++n) {
-        if (n < ntiles) {
-          float* d = mine + (ki * L::NB + 8 * n + 2 * q) * L::RED_TOK + 16 * mi + g;
-          d[0] = acc[n][0];
-          d[L::RED_TOK] = acc[n][1];
-          d[8] = acc[n][2];
-          d[L::RED_TOK + 8] = acc[n][3];
+      for (int m = 0; m < L::MPW; ++m)
+#pragma unroll
+        for (int n = 0; n < L::NT; ++n) {
+          if (n < ntiles) {
+            float* d = mine + (ki * L::NB + 8 * n + 2 * q) * L::RED_TOK + 16 * (mi + m) + g;
+            d[0] = acc[m][n][0];
+            d[L::RED_TOK] = acc[m][n][1];
+            d[8] = acc[m][n][2];
+            d[L::RED_TOK + 8] = acc[m][n][3];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-      }
       if (!meet()) break;
       auto sum = [&](int tok, int row) {
         float v = 0.f;
@@ -792,7 +887,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           }
           const int64_t at = (int64_t)pos * cf.F + st.r0 + f;
           if constexpr (L::W4) {
-            // one token's 32 hidden units are a warp's: fp16 with a power-of-two
+            // a warp has 32 hidden units of one token: fp16 with a power-of-two
             // scale of their own (11 significant bits, half a step 2^-11 of
             // values down to 2^-29 of the largest)
             uint32_t m = __float_as_uint(v) & 0x7fffffffu;
@@ -801,7 +896,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
             const float bsc = f16_block_scale(m);
             if (valid) {
               static_cast<__half*>(p.hidden)[at] = __float2half_rn(v * (1.f / bsc));
-              if (f == 0) p.hidden_s[(int64_t)pos * (cf.F / 32) + st.r0 / 32] = bsc;
+              if (lane == 0) p.hidden_s[(int64_t)pos * (cf.F / 32) + (st.r0 + f) / 32] = bsc;
             }
           } else {
             // bf16, as moe_layer_fwd keeps them: FC2's operand type
@@ -821,56 +916,76 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
         if (lane == 0) red_release(done2, 1);
       }
     }
-    // ---- combine: every block's share, two columns a thread ----
-    int all = 0;
-    if (finish && lane == 0) all = wait_count(done2, ctl.fc2_writers, wc);
-    if (__shfl_sync(0xffffffffu, all, 0)) {
-      ld_acquire(done2);  // every lane's own
-      const int64_t pairs2 = (int64_t)cf.T * cf.h / 2;
-      const int slots = cf.K + (cf.n_shared ? 1 : 0);
-      for (int64_t i = ((int64_t)warp * gridDim.x + blockIdx.x) * 32 + lane; i < pairs2;
-           i += (int64_t)gridDim.x * L::NW * 32) {
-        const int t = (int)(2 * i / cf.h), r = (int)(2 * i - (int64_t)t * cf.h);
-        float2 y = make_float2(0.f, 0.f);
-        constexpr int kBatch = 4;  // slots whose loads go out together
-        for (int k0 = 0; k0 < slots; k0 += kBatch) {
-          float2 o[kBatch];
-          float w[kBatch];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int k = k0 + j;
-            const bool shared = k == cf.K;
-            const int pr = t * cf.K + min(k, cf.K - 1);
-            const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
-            const bool there = k < slots && pos >= 0;  // else past the end, or dropped
-            w[j] = shared ? 1.f : ctl.prob[pr];
-            o[j] = make_float2(0.f, 0.f);
-            if (!there) w[j] = 0.f;
-            if (there && cf.has_bias && !shared) {
-              const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
-              o[j] = make_float2(to_f32(b[0]), to_f32(b[1]));
-            }
-            if (there) {
-              const float* src = p.ypart + (int64_t)pos * cf.h + r;
-              const int64_t step = (int64_t)p.S * cf.h;
-              for (int s = 0; s < p.ksplit; ++s) {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(src + s * step));
-                o[j].x += v.x;
-                o[j].y += v.y;
-              }
-            }
+    // ---- combine: every block's share ----
+    // A warp takes 16 columns of a token, eight slots at once: lanes 4 s + c hold
+    // columns 4 c .. 4 c + 3 of slot s, and a tree adds the slots (a fixed order).
+    const int cols16 = (cf.h + 15) / 16;
+    const int64_t items = (int64_t)cf.T * cols16;
+    const int slots = cf.K + (cf.n_shared ? 1 : 0);
+    finish = finish && (int64_t)blockIdx.x < items;
+    if (finish && warp == 0) {  // one warp of a block that has a share watches the count
+      int all = 0;
+      if (lane == 0) all = wait_count(done2, ctl.fc2_writers, wc);
+      __shfl_sync(0xffffffffu, all, 0);
+    }
+    if (finish && meet() && ld_acquire(done2) >= ctl.fc2_writers) {
+      for (int64_t i = (int64_t)warp * gridDim.x + blockIdx.x; i < items; i += (int64_t)gridDim.x * L::NW) {
+        const int t = (int)(i / cols16), r = (int)(i - (int64_t)t * cols16) * 16 + 4 * q;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k = g; k < slots; k += 8) {
+          const bool shared = k == cf.K;
+          const int pr = t * cf.K + k;
+          const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
+          if (pos < 0 || r >= cf.h) continue;  // dropped, or past the row
+          const float w = shared ? 1.f : ctl.prob[pr];
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cf.has_bias && !shared) {
+            const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
+            o = make_float4(to_f32(b[0]), to_f32(b[1]), to_f32(b[2]), to_f32(b[3]));
           }
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            y.x = fmaf(w[j], o[j].x, y.x);
-            y.y = fmaf(w[j], o[j].y, y.y);
+          const float* src = p.ypart + (int64_t)pos * cf.h + r;
+          for (int s = 0; s < p.ksplit; ++s) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)s * p.S * cf.h));
+            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
           }
+          y.x = fmaf(w, o.x, y.x); y.y = fmaf(w, o.y, y.y);
+          y.z = fmaf(w, o.z, y.z); y.w = fmaf(w, o.w, y.w);
         }
-        *reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r) = __floats2bfloat162_rn(y.x, y.y);
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) {
+          y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
+          y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+          y.z += __shfl_xor_sync(0xffffffffu, y.z, o);
+          y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
+        }
+        if (g == 0 && r < cf.h) {
+          __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r);
+          dst[0] = __floats2bfloat162_rn(y.x, y.y);
+          dst[1] = __floats2bfloat162_rn(y.z, y.w);
+        }
       }
     }
   }
   __syncthreads();
+}
+
+// Launches a kernel that may start while the one before it drains; it waits
+// (pdl_wait) before it reads what that one writes.
+template <typename... KArgs, typename... Args>
+cudaError_t few_pdl_launch(void (*kern)(KArgs...), int grid, int block, size_t smem, cudaStream_t s,
+                           const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // A map of up to three dimensions, zero fill outside.
@@ -922,17 +1037,7 @@ cudaError_t few_launch(FewParams& p, const __half* xh, cudaStream_t s) {
   const int smem = stages * L::STAGE + fixed;
   cudaError_t e = cudaFuncSetAttribute(few_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.a.sms);
-  cfg.blockDim = dim3(L::THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_kernel<L>, p);
+  return few_pdl_launch(few_kernel<L>, p.a.sms, L::THREADS, smem, s, p);
 }
 
 }  // namespace
@@ -942,8 +1047,11 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   const FewLayout L = few_layout(c);
   FewParams p{};
   p.a = a;
-  p.parts = reinterpret_cast<float*>(a.ws + L.parts);
-  p.kparts = few_kparts(c);
+  float* parts = reinterpret_cast<float*>(a.ws + L.parts);
+  const int kparts = few_kparts(c);
+  p.idx = reinterpret_cast<int32_t*>(a.ws + L.idx);
+  p.prob = reinterpret_cast<float*>(a.ws + L.prob);
+  p.pairs_pad = few_pairs_pad(c);
   p.sync = reinterpret_cast<int32_t*>(a.ws + L.sync);
   __half* xh = reinterpret_cast<__half*>(a.ws + L.xh);
   p.xs = reinterpret_cast<float*>(a.ws + L.xs);
@@ -953,22 +1061,28 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   p.S = c.T * c.K + (c.n_shared ? c.T : 0);
   p.ksplit = few_ksplit(c);
   p.wait_limit_ns = 2000000000ull;
-  p.r.T = c.T; p.r.E = c.E; p.r.K = c.K; p.r.h = c.h; p.r.score = c.score;
-  p.r.renorm = (c.flags & MOE_FLAG_RENORM) != 0;
-  p.r.force_balance = (c.flags & MOE_FLAG_FORCE_BALANCE) != 0;
-  p.r.sel_bias = a.sel_bias;
-  const int route_blocks = (int)ceil_div((int64_t)c.E * p.kparts, 8);
+  RouterArgs r{};
+  r.T = c.T; r.E = c.E; r.K = c.K; r.h = c.h; r.score = c.score;
+  r.renorm = (c.flags & MOE_FLAG_RENORM) != 0;
+  r.force_balance = (c.flags & MOE_FLAG_FORCE_BALANCE) != 0;
+  r.sel_bias = a.sel_bias;
+  r.topk_idx = const_cast<int32_t*>(p.idx);
+  r.topk_prob = const_cast<float*>(p.prob);
+  const int route_blocks = (int)ceil_div((int64_t)c.E * kparts * ceil_div(c.T, kRouteTok), 8);
   few_router_kernel<<<route_blocks + (mxfp4 ? c.T : 0), 256, 0, s>>>(
-      a.x, a.w_r, c.T, c.E, c.h, p.kparts, const_cast<float*>(p.parts), route_blocks,
+      a.x, a.w_r, c.T, c.E, c.h, kparts, parts, route_blocks,
       xh, const_cast<float*>(p.xs), p.sync, (int)few_sync_words(c));
   cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = few_pdl_launch(few_select_kernel, c.T, 256, 0, s,
+                       const_cast<const float*>(parts), kparts, a.gate_bias, r, p.pairs_pad,
+                       a.idx_out, a.prob_out);
   if (e != cudaSuccess) return e;
   if (mxfp4)
-    return c.T <= 8 ? few_launch<FewTile<true, 4, 1, 16, 512>>(p, xh, s)
-                    : few_launch<FewTile<true, 4, 2, 16, 512>>(p, xh, s);
-  if (c.T <= 8) return few_launch<FewTile<false, 2, 1, 8, 512>>(p, xh, s);
-  if (c.T <= 16) return few_launch<FewTile<false, 2, 2, 8, 512>>(p, xh, s);
-  return few_launch<FewTile<false, 2, 4, 8, 256>>(p, xh, s);
+    return c.T <= 8 ? few_launch<FewTile<true, 8, 2, 1, 16, 512>>(p, xh, s)
+                    : few_launch<FewTile<true, 8, 2, 2, 16, 512>>(p, xh, s);
+  if (c.T <= 8) return few_launch<FewTile<false, 4, 2, 1, 8, 512>>(p, xh, s);
+  return few_launch<FewTile<false, 4, 2, 2, 8, 256>>(p, xh, s);
 }
 
 }  // namespace moe

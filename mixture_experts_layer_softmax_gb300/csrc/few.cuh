@@ -24,8 +24,13 @@ inline int few_ksplit(const moe_config_t& c) {
   return (int)ceil_div(c.F, 4096);
 }
 
+// The selection (expert and weight of every pair) is kept in several copies,
+// whole 128-byte lines apart, so that the SMs do not all read the same lines.
+constexpr int kFewCopies = 16;
+inline int few_pairs_pad(const moe_config_t& c) { return (c.T * c.K + 31) / 32 * 32; }
+
 struct FewLayout {
-  size_t sync, parts, xh, xs, a, as, ypart, total;
+  size_t sync, parts, idx, prob, xh, xs, a, as, ypart, total;
 };
 // int32 words at `sync`: the unit counter, the warps that finished FC2 results,
 // and those that finished FC1 results per busy expert (E + 1).
@@ -43,6 +48,8 @@ inline FewLayout few_layout(const moe_config_t& c) {
   };
   w.sync = take(few_sync_words(c) * 4);
   w.parts = take((size_t)few_kparts(c) * T * c.E * 4);
+  w.idx = take((size_t)kFewCopies * few_pairs_pad(c) * 4);
+  w.prob = take((size_t)kFewCopies * few_pairs_pad(c) * 4);
   w.xh = take(T * c.h * 2);              // tokens in fp16 (MXFP4 weights)
   w.xs = take(T * 4);                    // and their power-of-two scales
   w.a = take(S * c.F * 2);               // hidden values, 16 bits
