@@ -41,6 +41,8 @@
 // moe_layer_fwd.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "few.cuh"
 #include "mx.cuh"
 #include "router_select.cuh"
@@ -241,12 +243,13 @@ enum { kEnd = 0, kFC1 = 1, kFC2 = 2 };
 struct alignas(16) FewStage {
   int kind;   // kEnd, kFC1, kFC2
   int last;   // the unit's last stage
+  int kc;     // columns in this stage
   int entry;  // busy expert (index into the list)
   int pos0;   // first row of the unit in the sorted pair list
   int n;      // its rows (tokens)
   int r0;     // first weight row (FC1: first hidden unit)
-  int k0, kc; // its columns in this stage
   int ks;     // slice of F (FC2)
+  int k0;     // first column
   int pad[3];
 };
 
@@ -725,114 +728,136 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     };
     int unit = 0;  // units this block has finished
     bool finish = false;
+    // The stages of one unit, the first of which is there (its weights).  TWO: a
+    // SwiGLU FC1 unit, whose m-tiles' upper halves (up rows) lie in a block of
+    // their own.  What does not change from stage to stage is worked out once:
+    // with 4-bit weights the instructions are what bounds these loops.
+    auto stages = [&](auto two_c, const FewStage& st) -> bool {
+      constexpr bool TWO = decltype(two_c)::value;
+      constexpr int M_STEP = TWO ? 8 : 16, HI = (TWO ? 8 * L::MT : 8) * L::A_ROW;
+      const int ntiles = (st.n + 7) >> 3;
+      const int m_row = M_STEP * mi + g;
+      // offsets within a stage: the lane's weight rows and token rows (past the
+      // last token, the last)
+      const uint32_t a_off = (k_w / L::KB * L::RT + m_row) * L::A_ROW +
+                             (L::W4 ? 4 * q : (k_w % L::KB + 8 * q) * 2);
+      uint32_t b_off[L::NT], sf_off[L::MPW][2], ts_off[L::NT][2];
+#pragma unroll
+      for (int n = 0; n < L::NT; ++n) {
+        b_off[n] = L::A_BYTES + (k_w / L::KB * L::NB + min(8 * n + g, st.n - 1)) * L::B_ROW +
+                   (k_w % L::KB + 8 * q) * 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ts_off[n][i] = L::A_BYTES + L::B_BYTES + L::SF +
+                         min(8 * n + 2 * q + i, st.n - 1) * L::BS_ROW + k_w / 32 * 4;
+      }
+#pragma unroll
+      for (int m = 0; m < L::MPW; ++m) {
+        const int i0 = (st.r0 + m_row + m * M_STEP) & 127, i1 = TWO ? i0 : i0 + 8;
+        const uint32_t at = L::A_BYTES + L::B_BYTES + k_w / 128 * mx::ATOM;
+        sf_off[m][0] = at + 16 * (i0 & 31) + 4 * (i0 >> 5);
+        sf_off[m][1] = at + (TWO ? L::SF / 2 : 0) + 16 * (i1 & 31) + 4 * (i1 >> 5);
+      }
+      // 16 bytes hold a 32-column block's codes of a row; the swizzle moves them by
+      // the row's place in its group of eight, which is g
+      [[maybe_unused]] const uint32_t sw16 = ((k_w % L::KB) / 32 ^ g) * 16;
+      int kc = st.kc, last = st.last;
+      for (;;) {
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.full_t[stage]), phase, wc)) return false;
+        const uint32_t base = ring0 + stage * L::STAGE, a_at = base + a_off;
+        if constexpr (!L::W4) {
+#pragma unroll
+          for (int c = 0; c < L::KW / 32; ++c) {
+            if (k_w + c * 32 >= kc) break;  // (the boxes are zero past the matrix)
+            uint4 b[L::NT];
+#pragma unroll
+            for (int n = 0; n < L::NT; ++n)
+              if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + c * 64);
+#pragma unroll
+            for (int m = 0; m < L::MPW; ++m) {
+              const uint4 lo = lds128(a_at + m * M_STEP * L::A_ROW + c * 64);
+              const uint4 hi = lds128(a_at + m * M_STEP * L::A_ROW + HI + c * 64);
+#pragma unroll
+              for (int n = 0; n < L::NT; ++n)
+                if (L::NT == 1 || n < ntiles) {
+                  mma16816<false>(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n].x, b[n].y);
+                  mma16816<false>(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n].z, b[n].w);
+                }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c4 = 0; c4 < L::KW / 128; ++c4) {  // 128 columns: one word of scales a row
+            if (k_w + c4 * 128 >= kc) break;
+            uint32_t sw[L::MPW][2];
+#pragma unroll
+            for (int m = 0; m < L::MPW; ++m) {
+              sw[m][0] = lds32(base + sf_off[m][0] + c4 * mx::ATOM);
+              sw[m][1] = lds32(base + sf_off[m][1] + c4 * mx::ATOM);
+            }
+            uint4 ts[L::NT][2];  // the tokens' own scales of these columns (FC2)
+            if constexpr (!TWO) {
+#pragma unroll
+              for (int n = 0; n < L::NT; ++n)
+                if (L::NT == 1 || n < ntiles) {
+                  ts[n][0] = lds128(base + ts_off[n][0] + c4 * 16);
+                  ts[n][1] = lds128(base + ts_off[n][1] + c4 * 16);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint4 b[L::NT];
+#pragma unroll
+              for (int n = 0; n < L::NT; ++n)
+                if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + (4 * c4 + c) * 64);
+              const uint32_t at = a_at + (sw16 ^ (64 * c4 + 16 * c));
+#pragma unroll
+              for (int m = 0; m < L::MPW; ++m) {
+                uint32_t lo[4], hi[4];
+                e2m1x8_to_f16(lds32(at + m * M_STEP * L::A_ROW), lo);
+                e2m1x8_to_f16(lds32(at + m * M_STEP * L::A_ROW + HI), hi);
+                const float s0 = __uint_as_float((c < 3 ? sw[m][0] << (23 - 8 * c) : sw[m][0] >> 1) & 0x7f800000u);
+                const float s1 = __uint_as_float((c < 3 ? sw[m][1] << (23 - 8 * c) : sw[m][1] >> 1) & 0x7f800000u);
+#pragma unroll
+                for (int n = 0; n < L::NT; ++n)
+                  if (L::NT == 1 || n < ntiles) {
+                    // the fp16 products of one block, then its scales in fp32
+                    float d[4];
+                    mma16816_zero(d, lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
+                    mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
+                    if constexpr (!TWO) {
+                      const float t0 = __uint_as_float(c == 0 ? ts[n][0].x : c == 1 ? ts[n][0].y : c == 2 ? ts[n][0].z : ts[n][0].w);
+                      const float t1 = __uint_as_float(c == 0 ? ts[n][1].x : c == 1 ? ts[n][1].y : c == 2 ? ts[n][1].z : ts[n][1].w);
+                      d[0] *= t0; d[1] *= t1; d[2] *= t0; d[3] *= t1;
+                    }
+                    acc[m][n][0] = fmaf(d[0], s0, acc[m][n][0]);
+                    acc[m][n][1] = fmaf(d[1], s0, acc[m][n][1]);
+                    acc[m][n][2] = fmaf(d[2], s1, acc[m][n][2]);
+                    acc[m][n][3] = fmaf(d[3], s1, acc[m][n][3]);
+                  }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.empty[stage]));
+        if (++stage == p.stages) { stage = 0; phase ^= 1; }
+        if (last) return true;
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.full_w[stage]), phase, wc)) return false;
+        const int4 h = *reinterpret_cast<const int4*>(&ctl.st[stage]);
+        last = h.y;
+        kc = h.z;
+      }
+    };
     for (;;) {
       if (!tc::mbar_wait(tc::smem_u32(&ctl.full_w[stage]), phase, wc)) break;
       const FewStage st = ctl.st[stage];
       if (st.kind == kEnd) { finish = true; break; }
-      if (!tc::mbar_wait(tc::smem_u32(&ctl.full_t[stage]), phase, wc)) break;
-      const uint32_t a_s = ring0 + stage * L::STAGE, b_s = a_s + L::A_BYTES;
-      const uint32_t sf_s = b_s + L::B_BYTES, bs_s = sf_s + L::SF;
+      bool done_all;
+      if (glu && st.kind == kFC1) done_all = stages(std::true_type{}, st);
+      else done_all = stages(std::false_type{}, st);
+      if (!done_all) break;
       const int ntiles = (st.n + 7) >> 3;
-      // rows of an m-tile's two halves: gate and up rows lie in two blocks
-      const bool two = glu && st.kind == kFC1;
-      const int m_step = two ? 8 : 16, hi_row = two ? 8 * L::MT : 8;
-      const int m_row = m_step * mi + g;
-      uint32_t b_at[L::NT];  // the lane's token rows; past the last one, the last
-#pragma unroll
-      for (int n = 0; n < L::NT; ++n)
-        b_at[n] = b_s + (k_w / L::KB * L::NB + min(8 * n + g, st.n - 1)) * L::B_ROW +
-                  (k_w % L::KB + 8 * q) * 2;
-      // the lane's weight rows
-      const uint32_t a_at = a_s + (k_w / L::KB * L::RT + m_row) * L::A_ROW +
-                            (L::W4 ? 4 * q : (k_w % L::KB + 8 * q) * 2);
-      if constexpr (!L::W4) {
-#pragma unroll
-        for (int c = 0; c < L::KW / 32; ++c) {
-          if (k_w + c * 32 >= st.kc) break;  // (the boxes are zero past the matrix)
-          uint4 b[L::NT];
-#pragma unroll
-          for (int n = 0; n < L::NT; ++n)
-            if (n < ntiles) b[n] = lds128(b_at[n] + c * 64);
-#pragma unroll
-          for (int m = 0; m < L::MPW; ++m) {
-            const uint4 lo = lds128(a_at + m * m_step * L::A_ROW + c * 64);
-            const uint4 hi = lds128(a_at + (m * m_step + hi_row) * L::A_ROW + c * 64);
-#pragma unroll
-            for (int n = 0; n < L::NT; ++n)
-              if (n < ntiles) {
-                mma16816<false>(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n].x, b[n].y);
-                mma16816<false>(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n].z, b[n].w);
-              }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int c4 = 0; c4 < L::KW / 128; ++c4) {  // 128 columns: one word of scales a row
-          if (k_w + c4 * 128 >= st.kc) break;
-          const uint32_t sf_at = sf_s + (k_w / 128 + c4) * mx::ATOM;
-          uint32_t sw[L::MPW][2];
-#pragma unroll
-          for (int m = 0; m < L::MPW; ++m) {
-            const int i0 = (st.r0 + m_row + m * m_step) & 127, i1 = two ? i0 : i0 + 8;
-            sw[m][0] = lds32(sf_at + 16 * (i0 & 31) + 4 * (i0 >> 5));
-            sw[m][1] = lds32(sf_at + (two ? L::SF / 2 : 0) + 16 * (i1 & 31) + 4 * (i1 >> 5));
-          }
-          // the tokens' own scales of these columns (FC2)
-          float ts[L::NT][2][4];
-          if (st.kind == kFC2) {
-#pragma unroll
-            for (int n = 0; n < L::NT; ++n)
-              if (n < ntiles) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint4 v = lds128(bs_s + min(8 * n + 2 * q + i, st.n - 1) * L::BS_ROW +
-                                         (k_w / 32 + c4 * 4) * 4);
-                  ts[n][i][0] = __uint_as_float(v.x); ts[n][i][1] = __uint_as_float(v.y);
-                  ts[n][i][2] = __uint_as_float(v.z); ts[n][i][3] = __uint_as_float(v.w);
-                }
-              }
-          }
-          // 16 bytes hold a 32-column block's codes of a row; the swizzle moves
-          // them by the row's place in its group of eight, which is g
-          const uint32_t sw16 = (((k_w % L::KB) / 32 + 4 * c4) ^ g) * 16;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4 b[L::NT];
-#pragma unroll
-            for (int n = 0; n < L::NT; ++n)
-              if (n < ntiles) b[n] = lds128(b_at[n] + (4 * c4 + c) * 64);
-#pragma unroll
-            for (int m = 0; m < L::MPW; ++m) {
-              uint32_t lo[4], hi[4];
-              const uint32_t at = a_at + m * m_step * L::A_ROW + (sw16 ^ (16 * c));
-              e2m1x8_to_f16(lds32(at), lo);
-              e2m1x8_to_f16(lds32(at + hi_row * L::A_ROW), hi);
-              const float s0 = __uint_as_float((c < 3 ? sw[m][0] << (23 - 8 * c) : sw[m][0] >> 1) & 0x7f800000u);
-              const float s1 = __uint_as_float((c < 3 ? sw[m][1] << (23 - 8 * c) : sw[m][1] >> 1) & 0x7f800000u);
-#pragma unroll
-              for (int n = 0; n < L::NT; ++n)
-                if (n < ntiles) {
-                  // the fp16 products of one block, then its scales in fp32
-                  float d[4];
-                  mma16816_zero(d, lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
-                  mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
-                  if (st.kind == kFC2) {
-                    d[0] *= ts[n][0][c]; d[1] *= ts[n][1][c];
-                    d[2] *= ts[n][0][c]; d[3] *= ts[n][1][c];
-                  }
-                  acc[m][n][0] = fmaf(d[0], s0, acc[m][n][0]);
-                  acc[m][n][1] = fmaf(d[1], s0, acc[m][n][1]);
-                  acc[m][n][2] = fmaf(d[2], s1, acc[m][n][2]);
-                  acc[m][n][3] = fmaf(d[3], s1, acc[m][n][3]);
-                }
-            }
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.empty[stage]));
-      if (++stage == p.stages) { stage = 0; phase ^= 1; }
-      if (!st.last) continue;
 
       // ---- the unit's end: the warps' sums meet ----
       // One meeting a unit where there are two buffers: they alternate, so the next unit's sums go
@@ -1078,11 +1103,16 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
                        const_cast<const float*>(parts), kparts, a.gate_bias, r, p.pairs_pad,
                        a.idx_out, a.prob_out);
   if (e != cudaSuccess) return e;
+  // Tokens a unit holds: 8 while experts have at most that many on average or
+  // half of it (what is more becomes a second unit, whose weights come from the
+  // L2), 16 beyond.  us with 8 / 16: bf16 T = 32, 2 of 8: 513 / 455; MXFP4 T = 13, 2
+  // of 8 (3 tokens an expert): 166 / 234; T = 64, 8 of 64 (8): 103 / 99.
+  const bool many = c.T > 8 && (int64_t)c.T * c.K > 4LL * c.E;
   if (mxfp4)
-    return c.T <= 8 ? few_launch<FewTile<true, 8, 2, 1, 16, 512>>(p, xh, s)
-                    : few_launch<FewTile<true, 8, 2, 2, 16, 512>>(p, xh, s);
-  if (c.T <= 8) return few_launch<FewTile<false, 4, 2, 1, 8, 512>>(p, xh, s);
-  return few_launch<FewTile<false, 4, 2, 2, 8, 256>>(p, xh, s);
+    return many ? few_launch<FewTile<true, 8, 2, 2, 16, 512>>(p, xh, s)
+                : few_launch<FewTile<true, 8, 2, 1, 16, 512>>(p, xh, s);
+  return many ? few_launch<FewTile<false, 4, 2, 2, 8, 256>>(p, xh, s)
+              : few_launch<FewTile<false, 4, 2, 1, 8, 512>>(p, xh, s);
 }
 
 }  // namespace moe
