@@ -21,18 +21,18 @@ MOE_D float e8m0_value(uint32_t c) {
   return __uint_as_float(c == 255u ? 0x7fc00000u : (c ? c << 23 : 0x00400000u));
 }
 
-// The group boundaries off[0 .. G] in shared memory and the first 128-row
-// tile rt[g] of each group (an exclusive scan of ceil(rows_g / 128)).  Every
-// thread of the block calls it.
-MOE_D void load_groups(const int32_t* __restrict__ offsets, int G, int* off, int* rt) {
-  for (int g = threadIdx.x; g <= G; g += blockDim.x) off[g] = __ldg(offsets + g);
+// The group boundaries off[0 .. G] in shared memory, kept within the rows, and
+// the 128-row tiles before each group, rt[0 .. G] (an exclusive scan of
+// ceil(rows_g / 128)).  Every thread of the block calls it.
+MOE_D void load_groups(const int32_t* __restrict__ offsets, int G, int rows, int* off, int* rt) {
+  for (int g = threadIdx.x; g <= G; g += blockDim.x) off[g] = min(max(__ldg(offsets + g), 0), rows);
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int running = 0;
     for (int g0 = 0; g0 < G; g0 += 32) {
       const int g = g0 + lane;
-      const int v = g < G ? (off[g + 1] - off[g] + 127) / 128 : 0;
+      const int v = g < G ? (max(off[g + 1] - off[g], 0) + 127) / 128 : 0;
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -42,22 +42,9 @@ MOE_D void load_groups(const int32_t* __restrict__ offsets, int G, int* off, int
       if (g < G) rt[g] = running + incl - v;
       running += __shfl_sync(0xffffffffu, incl, 31);
     }
+    if (lane == 0) rt[G] = running;
   }
   __syncthreads();
-}
-
-// Tile and row within the tile of row r (false: r lies in no group).
-MOE_D bool find_row(const int* off, const int* rt, int G, int r, int64_t& tile, int& i) {
-  if (r < off[0] || r >= off[G]) return false;
-  int lo = 0, hi = G - 1;  // the last group with off[g] <= r
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (off[mid] <= r) lo = mid; else hi = mid - 1;
-  }
-  const int lr = r - off[lo];
-  tile = rt[lo] + lr / 128;
-  i = lr & 127;
-  return true;
 }
 
 }  // namespace mx
