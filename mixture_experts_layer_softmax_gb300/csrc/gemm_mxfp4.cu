@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ================= TMA producer =================
-    if (lane == 0) {
+    {  // the whole warp, one elected lane issuing: see the MMA issuer
+      const bool elected = tc::elect_one();
       int stage = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
       for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
@@ -377,22 +378,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           b_atom1 = b_atom0 + KB;
           two_b = nb * BN + 128 < p.N;  // a half past N has no scale atom to read
         }
-                bool ok = true;
+        bool ok = true;
         for (int ks = 0; ks < KS; ++ks) {
           if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
           const int kb = 2 * ks;
           const uint32_t sfb = (kb + 1 < KB ? 2 : 1) * ATOM;  // scale bytes per 128 rows
           const uint32_t fb = tc::smem_u32(&ctl.full[stage]);
-          tc::mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES + (two_b ? 3 : 2) * sfb);
-          const uint32_t a_dst = tc::smem_u32(sA + stage * A_BYTES);
-          const uint32_t b_dst = tc::smem_u32(sB + stage * B_BYTES);
-          const uint32_t sf_dst = tc::smem_u32(sSF + stage * SF_BYTES);
-          tc::tma_load_2d(a_dst, &tmA, ks * BKB, a_row, fb);
-          tc::tma_load_2d(b_dst, &tmB, ks * BKB, b_row0, fb);
-          tc::tma_load_2d(b_dst + B_BYTES / 2, &tmB, ks * BKB, b_row1, fb);
-          tc::bulk_load(sf_dst, p.a_sf + (a_atom + kb) * ATOM, sfb, fb);
-          tc::bulk_load(sf_dst + 2 * ATOM, p.b_sf + (b_atom0 + kb) * ATOM, sfb, fb);
-          if (two_b) tc::bulk_load(sf_dst + 4 * ATOM, p.b_sf + (b_atom1 + kb) * ATOM, sfb, fb);
+          if (elected) {
+            tc::mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES + (two_b ? 3 : 2) * sfb);
+            const uint32_t a_dst = tc::smem_u32(sA + stage * A_BYTES);
+            const uint32_t b_dst = tc::smem_u32(sB + stage * B_BYTES);
+            const uint32_t sf_dst = tc::smem_u32(sSF + stage * SF_BYTES);
+            tc::tma_load_2d(a_dst, &tmA, ks * BKB, a_row, fb);
+            tc::tma_load_2d(b_dst, &tmB, ks * BKB, b_row0, fb);
+            tc::tma_load_2d(b_dst + B_BYTES / 2, &tmB, ks * BKB, b_row1, fb);
+            tc::bulk_load(sf_dst, p.a_sf + (a_atom + kb) * ATOM, sfb, fb);
+            tc::bulk_load(sf_dst + 2 * ATOM, p.b_sf + (b_atom0 + kb) * ATOM, sfb, fb);
+            if (two_b) tc::bulk_load(sf_dst + 4 * ATOM, p.b_sf + (b_atom1 + kb) * ATOM, sfb, fb);
+          }
+          __syncwarp();
           issued |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
@@ -406,46 +410,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ================= MMA issuer =================
-    if (lane == 0) {
+    // The whole warp runs the loop, so that the descriptors are warp-uniform and
+    // stay in uniform registers; one elected lane issues.  (One lane running the
+    // loop alone moves every operand of every instruction there first: 1130
+    // cycles a stage against the MMAs' 512.)
+    {
+      const bool elected = tc::elect_one();
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const uint64_t a_base = tc::desc_kmajor_sw128(tc::smem_u32(sA));
+      const uint64_t b_base = tc::desc_kmajor_sw128(tc::smem_u32(sB));
+      const uint64_t sf_base = tc::desc_sf_atom(tc::smem_u32(sSF));
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
         if (!tc::mbar_wait(tc::smem_u32(&ctl.tmem_empty), acc_phase ^ 1, wc)) break;
         tc::fence_after_sync();
         for (int ks = 0; ks < KS; ++ks) {
           if (!tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), phase, wc)) { ok = false; break; }
           tc::fence_after_sync();
-          const uint32_t a0 = tc::smem_u32(sA + stage * A_BYTES);
-          const uint32_t b0 = tc::smem_u32(sB + stage * B_BYTES);
-          const uint32_t sf0 = tc::smem_u32(sSF + stage * SF_BYTES);
+          // addresses in 16-byte units, added to the descriptors
+          const uint64_t ad = a_base + (uint32_t)(stage * (A_BYTES >> 4));
+          const uint64_t bd = b_base + (uint32_t)(stage * (B_BYTES >> 4));
+          const uint64_t sd = sf_base + (uint32_t)(stage * (SF_BYTES >> 4));
           const uint32_t sfa = tmem_base + SF_COL0 + stage * SF_STRIDE;
-          const int atoms = 2 * ks + 1 < KB ? 2 : 1;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (j >= atoms) break;
+          const bool two = 2 * ks + 1 < KB;  // both atoms
+          if (elected) {
             // atom j: A scales in columns 4j .. 4j+3, B scales in 8 + 8j .. 8 + 8j + 7
-            tc::tmem_cp_32x128b_warpx4(sfa + 4 * j, tc::desc_sf_atom(sf0 + j * ATOM));
-            tc::tmem_cp_32x128b_warpx4(sfa + 8 + 8 * j, tc::desc_sf_atom(sf0 + (2 + j) * ATOM));
-            tc::tmem_cp_32x128b_warpx4(sfa + 12 + 8 * j, tc::desc_sf_atom(sf0 + (4 + j) * ATOM));
+            tc::tmem_cp_32x128b_warpx4(sfa, sd);
+            tc::tmem_cp_32x128b_warpx4(sfa + 8, sd + 2 * (ATOM >> 4));
+            tc::tmem_cp_32x128b_warpx4(sfa + 12, sd + 4 * (ATOM >> 4));
+            // 64 columns (32 bytes, two blocks) an MMA
+            tc::mma_mxf4(tmem_base, ad, bd, tc::idesc_mxf4_e2m1(BM, BN, 0, 0), sfa, sfa + 8, ks != 0);
+            tc::mma_mxf4(tmem_base, ad + 2, bd + 2, tc::idesc_mxf4_e2m1(BM, BN, 2, 2), sfa, sfa + 8, 1);
+            if (two) {
+              tc::tmem_cp_32x128b_warpx4(sfa + 4, sd + (ATOM >> 4));
+              tc::tmem_cp_32x128b_warpx4(sfa + 16, sd + 3 * (ATOM >> 4));
+              tc::tmem_cp_32x128b_warpx4(sfa + 20, sd + 5 * (ATOM >> 4));
+              tc::mma_mxf4(tmem_base, ad + 4, bd + 4, tc::idesc_mxf4_e2m1(BM, BN, 0, 0), sfa + 4, sfa + 16, 1);
+              tc::mma_mxf4(tmem_base, ad + 6, bd + 6, tc::idesc_mxf4_e2m1(BM, BN, 2, 2), sfa + 4, sfa + 16, 1);
+            }
+            tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 64 columns (32 bytes, two blocks) an MMA
-            if ((k >> 1) >= atoms) break;
-            tc::mma_mxf4(tmem_base, tc::desc_kmajor_sw128(a0 + k * 32),
-                         tc::desc_kmajor_sw128(b0 + k * 32),
-                         tc::idesc_mxf4_e2m1(BM, BN, 2 * (k & 1), 2 * (k & 1)), sfa + 4 * (k >> 1),
-                         sfa + 8 + 8 * (k >> 1), (ks | k) != 0);
-          }
-          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
-        tc::mma_commit(tc::smem_u32(&ctl.tmem_full));
+        if (elected) tc::mma_commit(tc::smem_u32(&ctl.tmem_full));
         acc_phase ^= 1;
       }
+      __syncwarp();
       if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
-        tc::mma_commit(tc::smem_u32(&ctl.drain));
+        if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain));
         tc::mbar_wait(tc::smem_u32(&ctl.drain), 0, wdrain);
       }
     }

@@ -139,6 +139,19 @@ MOE_D void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
                : "memory");
 }
 
+// True on one lane of the (converged) warp, the same one each time.
+MOE_D bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P1;\n\t"
+      "elect.sync _|P1, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, P1;\n\t}"
+      : "=r"(ok)
+      :
+      : "memory");
+  return ok != 0;
+}
+
 // ---- TMA --------------------------------------------------------------------
 MOE_D void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,
                        uint32_t bar) {
