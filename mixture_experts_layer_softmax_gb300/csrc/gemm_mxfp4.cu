@@ -15,14 +15,14 @@
 //          0-3), code = sign << 3 | exponent << 1 | mantissa;
 //   scales in the atoms of mx.cuh, the same as MXFP8's.
 //
-// GEMM kernel (persistent, 1 CTA per SM, 320 threads), the roles of the MXFP8
+// GEMM kernel (persistent, 1 CTA per SM, 576 threads), the roles of the MXFP8
 // kernel with twice the columns per stage:
 //   warp 0     TMA producer: 4 stages of {A 128 x 128 B, B 256 x 128 B} = 256
 //              columns (128-byte swizzle) plus two scale atoms per 128 rows.
 //   warp 1     TMEM owner and MMA issuer: per stage, tcgen05.cp of six atoms
 //              into the stage's 24 TMEM columns, then 4 MMAs M128 N256 K64
 //              (atom k / 2, scale bytes 2 (k % 2) and the next).
-//   warps 2-9  epilogue, as in the MXFP8 kernel; FC1 can re-quantise a.
+//   warps 2-17 epilogue; FC1 can re-quantise a.
 // K is a multiple of 128; an odd last 128 columns are half a stage (the box's
 // other half is zero fill and gets no MMA).
 // Every wait is bounded; a wait that gives up records MOE_ERR_TIMEOUT and
@@ -43,7 +43,8 @@ constexpr int A_BYTES = BM * BKB;   // 16 KB
 constexpr int B_BYTES = BN * BKB;   // 32 KB
 constexpr int SF_BYTES = 6 * ATOM;  // two atoms per 128 rows of A and B
 constexpr int STAGES = 4;
-constexpr int kThreads = 320;  // producer, MMA, 8 epilogue warps
+constexpr int kEpiWarps = 16;  // four per TMEM lane quarter, each a quarter of the columns
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, MMA, epilogue
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t SF_COL0 = 256, SF_STRIDE = 32;  // per stage: A scales +0..7, B +8..23
 
@@ -58,6 +59,7 @@ struct Mx4Params {
   uint8_t* out_q;          // FC1: codes of a [P, N / 2] or null
   uint8_t* out_sf;         // FC1: scale atoms of a
   int E, Kd, N, Nb;
+  bool wide;               // out is 32-byte aligned (its rows are multiples of 256 bytes)
   int* status;
   uint64_t wait_limit_ns;
 };
@@ -99,6 +101,52 @@ MOE_D uint32_t e2m1x8(const float* v) {
 MOE_D uint32_t pack_bf16x2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// SiLU with the approximate exponential and reciprocal (each within 2 units in
+// the last place of fp32 or so, far inside the output's bf16 or E2M1 step): the
+// exact ones kept the epilogue warps busy for longer than the tile's MMAs.
+// (exp(-z) overflowing gives -0, SiLU's limit; NaN stays.)
+MOE_D float silu_fast(float z) { return z * __fdividef(1.f, 1.f + __expf(-z)); }
+
+// 32 lanes x two groups of 32 columns: both loads in flight, then one wait, in one
+// asm statement (no register is read before the data has arrived).
+MOE_D void tmem_ld_x32x2(uint32_t ta, uint32_t tb, float (&a)[32], float (&b)[32]) {
+#define MOE_F8(v, i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), \
+                     "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : MOE_F8(a, 0), MOE_F8(a, 8), MOE_F8(a, 16), MOE_F8(a, 24), MOE_F8(b, 0), MOE_F8(b, 8),
+        MOE_F8(b, 16), MOE_F8(b, 24)
+      : "r"(ta), "r"(tb)
+      : "memory");
+#undef MOE_F8
+}
+
+// 32 values of a row as bf16: 32-byte stores (whole sectors) where the output
+// allows them, 16-byte ones elsewhere.
+MOE_D void store_row32(__nv_bfloat16* dst, const float (&a)[32], bool wide) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * j),
+                   "r"(w[8 * j]), "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]),
+                   "r"(w[8 * j + 4]), "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
 }
 
 // ---- quantiser and its inverse ----------------------------------------------------
@@ -309,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(tc::smem_u32(&ctl.empty[s]), 1);
     }
     tc::mbar_init(tc::smem_u32(&ctl.tmem_full), 1);
-    tc::mbar_init(tc::smem_u32(&ctl.tmem_empty), 8);
+    tc::mbar_init(tc::smem_u32(&ctl.tmem_empty), kEpiWarps);
     tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
     tc::fence_barrier_init();
@@ -466,11 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ================= epilogue (warps 2..9) =================
-    // two warps per TMEM lane quarter, each taking half of the tile's columns;
-    // each releases the accumulator as soon as its TMEM reads are done
+    // ================= epilogue (warps 2..17) =================
+    // four warps per TMEM lane quarter, each taking a quarter of the tile's
+    // columns; each releases the accumulator as soon as its TMEM reads are done
+    // (eight warps with twice the columns spilled, and left too few instructions
+    // in flight: FC1 at 16384 rows 698 us)
     const int q = warp & 3;          // TMEM lane quarter this warp may access
-    const int hf = (warp - 2) >> 2;  // which half of the columns
+    const int qt = (warp - 2) >> 2;  // which quarter of the columns
     uint32_t acc_phase = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       int e, mb, nb;
@@ -482,86 +532,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = mb * BM + i < m_e;
       const int64_t row = (int64_t)ctl.off[e] + mb * BM + i;
       const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+      // all of the warp's TMEM reads in flight together, then the release, then
+      // the math; a warp whose rows are all past the expert's end only releases
+      const bool any = mb * BM + q * 32 < m_e;
+      float v[2][32];
+      if (any) {
+        const uint32_t c0 = MODE == kSwiGLU ? qt * 32 : qt * 64;
+        const uint32_t c1 = MODE == kSwiGLU ? 128 + qt * 32 : qt * 64 + 32;
+        tmem_ld_x32x2(tbase + c0, tbase + c1, v[0], v[1]);
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tmem_empty));
+      acc_phase ^= 1;
+      if (!any) continue;
       if (MODE == kSwiGLU) {
-        // columns: gate hf*64 .. +63 and the matching up columns (two 32-wide chunks)
+        // columns: gate qt*32 .. +31 and the matching up columns
         const float pr = (p.prob && valid) ? __ldg(p.prob + row) : 1.f;
-        // all of this warp's TMEM reads first (gate and up, two 32-column
-        // chunks each), then the release, then the math: the next tile's MMAs
-        // need not wait for the SiLU evaluations
-        uint32_t g[2][32], u[2][32];
+        const int n = nb * 128 + qt * 32;
+        float (&a)[32] = v[0];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = hf * 64 + c * 32;
-          tc::tmem_ld_32x32b_x32(tbase + col, g[c]);
-          tc::tmem_ld_32x32b_x32(tbase + 128 + col, u[c]);
-        }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tmem_empty));
-        float a[2][32];
+        for (int j = 0; j < 32; ++j) a[j] = pr * (silu_fast(v[0][j]) * v[1][j]);
+        if (valid && p.out) store_row32(p.out + row * p.N + n, a, p.wide);
+        if (p.out_q) {  // one block of FC2's A operand
+          uint32_t abits = 0;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+          for (int j = 0; j < 32; ++j) abits = max(abits, __float_as_uint(a[j]) & 0x7fffffffu);
+          const uint32_t code = e8m0_code(abits);
+          const float inv = e8m0_inverse(code);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            a[c][j] = pr * (silu_f(__uint_as_float(g[c][j])) * __uint_as_float(u[c][j]));
-        uint32_t codes = 0;  // this warp's 2 of the row's 4 block scales
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int n = nb * 128 + hf * 64 + c * 32;
-          if (valid && p.out) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint4 w;
-              w.x = pack_bf16x2(a[c][j], a[c][j + 1]);
-              w.y = pack_bf16x2(a[c][j + 2], a[c][j + 3]);
-              w.z = pack_bf16x2(a[c][j + 4], a[c][j + 5]);
-              w.w = pack_bf16x2(a[c][j + 6], a[c][j + 7]);
-              *reinterpret_cast<uint4*>(p.out + row * p.N + n + j) = w;
-            }
-          }
-          if (p.out_q) {
-            uint32_t abits = 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) abits = max(abits, __float_as_uint(a[c][j]) & 0x7fffffffu);
-            const uint32_t code = e8m0_code(abits);
-            const float inv = e8m0_inverse(code);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) a[c][j] *= inv;
-            codes |= code << (8 * c);
-            if (valid)
-              *reinterpret_cast<uint4*>(p.out_q + (row * p.N + n) / 2) =
-                  make_uint4(e2m1x8(a[c]), e2m1x8(a[c] + 8), e2m1x8(a[c] + 16), e2m1x8(a[c] + 24));
+          for (int j = 0; j < 32; ++j) a[j] *= inv;
+          if (valid) {
+            *reinterpret_cast<uint4*>(p.out_q + (row * p.N + n) / 2) =
+                make_uint4(e2m1x8(a), e2m1x8(a + 8), e2m1x8(a + 16), e2m1x8(a + 24));
+            // its scale: atom (rtile[e] + mb, kb = nb), row i, block qt
+            p.out_sf[mx::atom_word(ctl.rtile[e] + mb, p.N / 128, nb, i) + qt] = (uint8_t)code;
           }
         }
-        if (p.out_q)  // FC2's A operand: atom (rtile[e] + mb, kb = nb), row i, blocks 2 hf, 2 hf + 1
-          *reinterpret_cast<uint16_t*>(
-              p.out_sf + mx::atom_word(ctl.rtile[e] + mb, p.N / 128, nb, i) + 2 * hf) =
-              (uint16_t)(valid ? codes : 0u);
-      } else {
-        // columns hf*128 .. +127: all four 32-column loads first, then release
-        uint32_t r[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld_32x32b_x32(tbase + hf * 128 + c * 32, r[c]);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tmem_empty));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n = nb * BN + hf * 128 + c * 32;
-          if (valid && n < p.N) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(r[c][j]), __uint_as_float(r[c][j + 1]));
-              w.y = pack_bf16x2(__uint_as_float(r[c][j + 2]), __uint_as_float(r[c][j + 3]));
-              w.z = pack_bf16x2(__uint_as_float(r[c][j + 4]), __uint_as_float(r[c][j + 5]));
-              w.w = pack_bf16x2(__uint_as_float(r[c][j + 6]), __uint_as_float(r[c][j + 7]));
-              *reinterpret_cast<uint4*>(p.out + row * p.N + n + j) = w;
-            }
-          }
+      } else if (valid) {
+        // columns qt*64 .. +63
+        const int n = nb * BN + qt * 64;
+        if (n < p.N) {
+          store_row32(p.out + row * p.N + n, v[0], p.wide);
+          store_row32(p.out + row * p.N + n + 32, v[1], p.wide);
         }
       }
-      acc_phase ^= 1;
     }
   }
   tc::fence_before_sync();
@@ -635,6 +650,7 @@ cudaError_t launch_grouped_gemm_mxfp4(bool swiglu, int P, const uint8_t* A, cons
   p.offsets = offsets; p.prob = prob; p.a_sf = A_sf; p.b_sf = B_sf;
   p.out = static_cast<__nv_bfloat16*>(out); p.out_q = out_q; p.out_sf = out_sf;
   p.E = E; p.Kd = Kd; p.N = N; p.Nb = Nb;
+  p.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;
   const int nblk = swiglu ? (N + 127) / 128 : (N + BN - 1) / BN;
