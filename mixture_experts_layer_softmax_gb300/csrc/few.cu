@@ -653,53 +653,66 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     __syncwarp();
   } else if (warp == L::NW + 1) {
     // ================= tokens =================
-    if (lane == 0) {
-      int stage = 0, ready = -1;
-      uint32_t phase = 0, issued = 0, issued_par = 0;
-      for (;;) {
-        if (!tc::mbar_wait(tc::smem_u32(&ctl.told[stage]), phase, wc)) break;
-        const FewStage st = ctl.st[stage];
-        if (st.kind == kEnd) break;
-        if (st.kind == kFC2 && ready != st.entry) {  // the expert's hidden values
-          const int writers = few_writers_of(ctl.ent_n[st.entry], L::NB, width1, L::NW);
-          if (!wait_count(done + st.entry, nrb1 * writers, wc)) break;
-          fence_proxy_async_global();
-          ready = st.entry;
-        }
-        const uint32_t fb = tc::smem_u32(&ctl.full_t[stage]);
-        const uint32_t b_dst = ring0 + stage * L::STAGE + L::A_BYTES;
-        const int nkb = (st.kc + L::KB - 1) / L::KB;
-        if (st.kind == kFC1) {  // tokens anywhere: four rows a load, the last one repeated
-          const int n4 = (st.n + 3) / 4;
-          tc::mbar_arrive_expect_tx(fb, nkb * n4 * 4 * L::B_ROW);
-          for (int i = 0; i < n4; ++i) {
-            int row[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) row[r] = ctl.tok_of[st.pos0 + min(4 * i + r, st.n - 1)];
-            for (int b = 0; b < nkb; ++b)
-              tc::tma_gather4(b_dst + (b * L::NB + 4 * i) * L::B_ROW, &p.x, st.k0 + b * L::KB,
-                              row[0], row[1], row[2], row[3], fb);
-          }
-        } else {  // rows of the sorted list: boxes of eight
-          const int n8 = (st.n + 7) / 8;
-          tc::mbar_arrive_expect_tx(fb, n8 * (nkb * 8 * L::B_ROW + 8 * L::BS_ROW));
-          for (int i = 0; i < n8; ++i) {
-            for (int b = 0; b < nkb; ++b)
-              tc::tma_load_2d(b_dst + (b * L::NB + 8 * i) * L::B_ROW, &p.act, st.k0 + b * L::KB,
-                              st.pos0 + 8 * i, fb);
-            if (L::W4)
-              tc::tma_load_2d(b_dst + L::B_BYTES + L::SF + 8 * i * L::BS_ROW, &p.act_s, st.k0 / 32,
-                              st.pos0 + 8 * i, fb);
-          }
-        }
-        issued |= 1u << stage;
-        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == p.stages) { stage = 0; phase ^= 1; }
+    // (the whole warp runs the loop, one elected lane issues: the addresses stay
+    // in uniform registers)
+    const bool elected = tc::elect_one();
+    int stage = 0, ready = -1;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    int row[2 * L::NT][4];  // FC1: the unit's tokens, four rows a load
+    for (;;) {
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.told[stage]), phase, wc)) break;
+      const FewStage st = ctl.st[stage];
+      if (st.kind == kEnd) break;
+      if (st.kind == kFC2 && ready != st.entry) {  // the expert's hidden values
+        const int writers = few_writers_of(ctl.ent_n[st.entry], L::NB, width1, L::NW);
+        int up = 0;
+        if (lane == 0) up = wait_count(done + st.entry, nrb1 * writers, wc);
+        if (!__shfl_sync(0xffffffffu, up, 0)) break;
+        ld_acquire(done + st.entry);  // every lane's own
+        fence_proxy_async_global();
+        ready = st.entry;
       }
-      for (int s = 0; s < p.stages; ++s)
-        if ((issued >> s) & 1u)
-          tc::mbar_wait(tc::smem_u32(&ctl.full_t[s]), (issued_par >> s) & 1u, wdrain);
+      const uint32_t fb = tc::smem_u32(&ctl.full_t[stage]);
+      const uint32_t b_dst = ring0 + stage * L::STAGE + L::A_BYTES;
+      const int nkb = (st.kc + L::KB - 1) / L::KB;
+      if (st.kind == kFC1) {  // tokens anywhere: the last one repeated
+        if (st.k0 == 0) {  // a unit's first stage
+          const int mine = ctl.tok_of[st.pos0 + min(lane, st.n - 1)];
+#pragma unroll
+          for (int i = 0; i < 2 * L::NT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) row[i][r] = __shfl_sync(0xffffffffu, mine, 4 * i + r);
+        }
+        const int n4 = (st.n + 3) / 4;
+        if (elected) {
+          tc::mbar_arrive_expect_tx(fb, nkb * n4 * 4 * L::B_ROW);
+#pragma unroll
+          for (int i = 0; i < 2 * L::NT; ++i)
+            if (i < n4)
+              for (int b = 0; b < nkb; ++b)
+                tc::tma_gather4(b_dst + (b * L::NB + 4 * i) * L::B_ROW, &p.x, st.k0 + b * L::KB,
+                                row[i][0], row[i][1], row[i][2], row[i][3], fb);
+        }
+      } else if (elected) {  // rows of the sorted list: boxes of eight
+        const int n8 = (st.n + 7) / 8;
+        tc::mbar_arrive_expect_tx(fb, n8 * (nkb * 8 * L::B_ROW + 8 * L::BS_ROW));
+        for (int i = 0; i < n8; ++i) {
+          for (int b = 0; b < nkb; ++b)
+            tc::tma_load_2d(b_dst + (b * L::NB + 8 * i) * L::B_ROW, &p.act, st.k0 + b * L::KB,
+                            st.pos0 + 8 * i, fb);
+          if (L::W4)
+            tc::tma_load_2d(b_dst + L::B_BYTES + L::SF + 8 * i * L::BS_ROW, &p.act_s, st.k0 / 32,
+                            st.pos0 + 8 * i, fb);
+        }
+      }
+      __syncwarp();
+      issued |= 1u << stage;
+      issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+      if (++stage == p.stages) { stage = 0; phase ^= 1; }
     }
+    for (int s = 0; s < p.stages; ++s)
+      if ((issued >> s) & 1u)
+        tc::mbar_wait(tc::smem_u32(&ctl.full_t[s]), (issued_par >> s) & 1u, wdrain);
     __syncwarp();
   } else {
     // ================= consumers =================
@@ -954,28 +967,36 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       __shfl_sync(0xffffffffu, all, 0);
     }
     if (finish && meet() && ld_acquire(done2) >= ctl.fc2_writers) {
+#pragma unroll 2
       for (int64_t i = (int64_t)warp * gridDim.x + blockIdx.x; i < items; i += (int64_t)gridDim.x * L::NW) {
         const int t = (int)(i / cols16), r = (int)(i - (int64_t)t * cols16) * 16 + 4 * q;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int k = g; k < slots; k += 8) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), o[3];
+        float w[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {  // up to 17 slots: all their loads go out together
+          const int k = g + 8 * j;
           const bool shared = k == cf.K;
-          const int pr = t * cf.K + k;
+          const int pr = t * cf.K + min(k, cf.K - 1);
           const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
-          if (pos < 0 || r >= cf.h) continue;  // dropped, or past the row
-          const float w = shared ? 1.f : ctl.prob[pr];
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          const bool there = k < slots && pos >= 0 && r < cf.h;  // else dropped, or past the row
+          o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          w[j] = !there ? 0.f : shared ? 1.f : ctl.prob[pr];
+          if (!there) continue;
           if (cf.has_bias && !shared) {
             const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
-            o = make_float4(to_f32(b[0]), to_f32(b[1]), to_f32(b[2]), to_f32(b[3]));
+            o[j] = make_float4(to_f32(b[0]), to_f32(b[1]), to_f32(b[2]), to_f32(b[3]));
           }
           const float* src = p.ypart + (int64_t)pos * cf.h + r;
+#pragma unroll 4
           for (int s = 0; s < p.ksplit; ++s) {
             const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)s * p.S * cf.h));
-            o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+            o[j].x += v.x; o[j].y += v.y; o[j].z += v.z; o[j].w += v.w;
           }
-          y.x = fmaf(w, o.x, y.x); y.y = fmaf(w, o.y, y.y);
-          y.z = fmaf(w, o.z, y.z); y.w = fmaf(w, o.w, y.w);
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+          y.x = fmaf(w[j], o[j].x, y.x); y.y = fmaf(w[j], o[j].y, y.y);
+          y.z = fmaf(w[j], o[j].z, y.z); y.w = fmaf(w[j], o[j].w, y.w);
         }
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) {
