@@ -437,12 +437,12 @@ template <bool F16>
 MOE_D void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                     uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                  "{%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                  "{%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -451,7 +451,7 @@ MOE_D void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
 // The fp16 product alone (a zero addend).
 MOE_D void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                          uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
                "{%8,%9}, {%10,%10,%10,%10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -486,18 +486,10 @@ MOE_D void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t
       : "memory");
 }
 
-MOE_D uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-MOE_D uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
+// Loads from the ring: ordinary loads, which the compiler may move among the
+// products but not across a barrier's wait.
+MOE_D uint32_t lds32(const uint8_t* a) { return *reinterpret_cast<const uint32_t*>(a); }
+MOE_D uint4 lds128(const uint8_t* a) { return *reinterpret_cast<const uint4*>(a); }
 
 // Rows of FC1's output of a unit: hidden units (a SwiGLU unit holds the gate
 // and up rows of RT / 2 of them, in groups of eight: each m-tile has eight
@@ -506,9 +498,10 @@ template <class L> MOE_HD int few_rows1(bool glu) { return glu ? L::RT / 2 : L::
 
 template <class L>
 __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constant__ FewParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (the ring's offset, not a rounded pointer: the compiler must see that its loads
+  // are from shared memory)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const moe_config_t& cf = p.a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool glu = cf.act == MOE_ACT_SWIGLU;
@@ -777,7 +770,8 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       int kc = st.kc, last = st.last;
       for (;;) {
         if (!tc::mbar_wait(tc::smem_u32(&ctl.full_t[stage]), phase, wc)) return false;
-        const uint32_t base = ring0 + stage * L::STAGE, a_at = base + a_off;
+        const uint8_t* base = ring + stage * L::STAGE;
+        const uint8_t* a_at = base + a_off;
         if constexpr (!L::W4) {
 #pragma unroll
           for (int c = 0; c < L::KW / 32; ++c) {
@@ -823,7 +817,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 #pragma unroll
               for (int n = 0; n < L::NT; ++n)
                 if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + (4 * c4 + c) * 64);
-              const uint32_t at = a_at + (sw16 ^ (64 * c4 + 16 * c));
+              const uint8_t* at = a_at + (sw16 ^ (64 * c4 + 16 * c));
 #pragma unroll
               for (int m = 0; m < L::MPW; ++m) {
                 uint32_t lo[4], hi[4];
