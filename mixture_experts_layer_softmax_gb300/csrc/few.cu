@@ -268,7 +268,7 @@ struct FewCtl {
   int ent_n[kMaxEntries];        // pairs
   int cum1[kMaxEntries + 1], cum2[kMaxEntries + 1];  // units before entry j
   int start[kMaxEntries];                // first sorted pair of an expert
-  unsigned long long mask[kMaxEntries];  // tokens of an expert
+  uint32_t mask[2][kMaxEntries];         // tokens of an expert: 0 .. 31, 32 .. 63
   int idx[kMaxPairs];
   float prob[kMaxPairs];
   int16_t pos_of[kMaxPairs];     // sorted position of pair p, -1: dropped
@@ -342,9 +342,15 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
   for (int p = threadIdx.x; p < P; p += L::THREADS) {
     const int e = c.idx[p];
     if (e < 0 || e >= cf.E) report(status, MOE_ERR_DEVICE_BOUNDS);
-    else atomicOr(&c.mask[e], 1ull << (p / cf.K));
+    else {
+      const int t = p / cf.K;
+      atomicOr(&c.mask[t >> 5][e], 1u << (t & 31));
+    }
   }
-  if (threadIdx.x == 0 && cf.n_shared) c.mask[cf.E] = ~0ull >> (64 - cf.T);
+  if (threadIdx.x < 2 && cf.n_shared) {
+    const int n = cf.T - 32 * (int)threadIdx.x;  // tokens in this word
+    c.mask[threadIdx.x][cf.E] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
+  }
   __syncthreads();
   // busy experts in order, 32 experts a step (the shared expert is one more);
   // a loop of few instructions, as they are fetched once
@@ -354,12 +360,15 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
 #pragma unroll 1
     for (int e0 = 0; e0 < last; e0 += 32) {
       const int e = e0 + lane;
-      int n = e < last ? __popcll(c.mask[e]) : 0;
+      int n = e < last ? __popc(c.mask[0][e]) + __popc(c.mask[1][e]) : 0;
       if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
       const uint32_t busy = __ballot_sync(0xffffffffu, n > 0);
       if (busy == 0) continue;
       const int sub = (n + L::NB - 1) / L::NB;
       int ip = n, is = sub;
+      if (!__any_sync(0xffffffffu, n > 1)) {  // at most one token an expert: count the busy ones
+        ip = is = __popc(busy & (0xffffffffu >> (31 - lane)));
+      } else
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int a = __shfl_up_sync(0xffffffffu, ip, o), b = __shfl_up_sync(0xffffffffu, is, o);
@@ -391,7 +400,9 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
     const int e = c.idx[p], t = p / cf.K;
     int pos = -1;
     if (e >= 0 && e < cf.E) {
-      const int rank = __popcll(c.mask[e] & ((1ull << t) - 1));
+      const uint32_t below = (1u << (t & 31)) - 1;
+      const int rank = t < 32 ? __popc(c.mask[0][e] & below)
+                              : __popc(c.mask[0][e]) + __popc(c.mask[1][e] & below);
       if (cf.capacity == 0 || rank < cf.capacity) {
         pos = c.start[e] + rank;
         c.tok_of[pos] = (uint8_t)t;
@@ -523,7 +534,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     tc::fence_proxy_async_smem();
     for (const CUtensorMap* m : {&p.w1, &p.w2, &p.x, &p.act}) tc::prefetch_tensormap(m);
   }
-  for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[e] = 0ull;
+  for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[0][e] = ctl.mask[1][e] = 0u;
   pdl_wait();  // the selection, and with it the cleared counters and the fp16 tokens
   int32_t* claim = p.sync;
   // the first unit's number comes while the list is made
@@ -949,10 +960,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       }
     }
     // ---- combine: every block's share ----
-    // A warp takes 16 columns of a token, eight slots at once: lanes 4 s + c hold
-    // columns 4 c .. 4 c + 3 of slot s, and a tree adds the slots (a fixed order).
-    const int cols16 = (cf.h + 15) / 16;
-    const int64_t items = (int64_t)cf.T * cols16;
+    // A warp takes 64 columns of a token, eight slots at once: lanes 4 s + c hold
+    // columns 16 i + 4 c .. + 3 of slot s, and a tree adds the slots (a fixed order).
+    constexpr int kCols = 64;
+    const int col_blocks = (cf.h + kCols - 1) / kCols;
+    const int64_t items = (int64_t)cf.T * col_blocks;
     const int slots = cf.K + (cf.n_shared ? 1 : 0);
     finish = finish && (int64_t)blockIdx.x < items;
     if (finish && warp == 0) {  // one warp of a block that has a share watches the count
@@ -961,48 +973,59 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       __shfl_sync(0xffffffffu, all, 0);
     }
     if (finish && meet() && ld_acquire(done2) >= ctl.fc2_writers) {
-#pragma unroll 2
       for (int64_t i = (int64_t)warp * gridDim.x + blockIdx.x; i < items; i += (int64_t)gridDim.x * L::NW) {
-        const int t = (int)(i / cols16), r = (int)(i - (int64_t)t * cols16) * 16 + 4 * q;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), o[3];
-        float w[3];
+        const int t = (int)(i / col_blocks), r = (int)(i - (int64_t)t * col_blocks) * kCols + 4 * q;
+        float4 y[4];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {  // up to 17 slots: all their loads go out together
-          const int k = g + 8 * j;
+        for (int c = 0; c < 4; ++c) y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k = g; k < slots; k += 8) {
           const bool shared = k == cf.K;
-          const int pr = t * cf.K + min(k, cf.K - 1);
+          const int pr = t * cf.K + k;
           const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
-          const bool there = k < slots && pos >= 0 && r < cf.h;  // else dropped, or past the row
-          o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          w[j] = !there ? 0.f : shared ? 1.f : ctl.prob[pr];
-          if (!there) continue;
+          if (pos < 0) continue;  // dropped
+          const float w = shared ? 1.f : ctl.prob[pr];
+          const float* src = p.ypart + (int64_t)pos * cf.h + r;
+          float4 o[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (cf.has_bias && !shared) {
             const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
-            o[j] = make_float4(to_f32(b[0]), to_f32(b[1]), to_f32(b[2]), to_f32(b[3]));
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (r + 16 * c < cf.h)
+                o[c] = make_float4(to_f32(b[16 * c]), to_f32(b[16 * c + 1]), to_f32(b[16 * c + 2]), to_f32(b[16 * c + 3]));
           }
-          const float* src = p.ypart + (int64_t)pos * cf.h + r;
-#pragma unroll 4
+#pragma unroll 2
           for (int s = 0; s < p.ksplit; ++s) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)s * p.S * cf.h));
-            o[j].x += v.x; o[j].y += v.y; o[j].z += v.z; o[j].w += v.w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (r + 16 * c < cf.h) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)s * p.S * cf.h + 16 * c));
+                o[c].x += v.x; o[c].y += v.y; o[c].z += v.z; o[c].w += v.w;
+              }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            y[c].x = fmaf(w, o[c].x, y[c].x); y[c].y = fmaf(w, o[c].y, y[c].y);
+            y[c].z = fmaf(w, o[c].z, y[c].z); y[c].w = fmaf(w, o[c].w, y[c].w);
           }
         }
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          y.x = fmaf(w[j], o[j].x, y.x); y.y = fmaf(w[j], o[j].y, y.y);
-          y.z = fmaf(w[j], o[j].z, y.z); y.w = fmaf(w[j], o[j].w, y.w);
-        }
+        for (int c = 0; c < 4; ++c) {
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) {
-          y.x += __shfl_xor_sync(0xffffffffu, y.x, o);
-          y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
-          y.z += __shfl_xor_sync(0xffffffffu, y.z, o);
-          y.w += __shfl_xor_sync(0xffffffffu, y.w, o);
-        }
-        if (g == 0 && r < cf.h) {
-          __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r);
-          dst[0] = __floats2bfloat162_rn(y.x, y.y);
-          dst[1] = __floats2bfloat162_rn(y.z, y.w);
+          for (int o = 4; o <= 16; o <<= 1) {
+            y[c].x += __shfl_xor_sync(0xffffffffu, y[c].x, o);
+            y[c].y += __shfl_xor_sync(0xffffffffu, y[c].y, o);
+            y[c].z += __shfl_xor_sync(0xffffffffu, y[c].z, o);
+            y[c].w += __shfl_xor_sync(0xffffffffu, y[c].w, o);
+          }
+          if (g == c && r + 16 * c < cf.h) {
+            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r + 16 * c);
+            dst[0] = __floats2bfloat162_rn(y[c].x, y[c].y);
+            dst[1] = __floats2bfloat162_rn(y[c].z, y[c].w);
+          }
         }
       }
     }
