@@ -379,11 +379,14 @@ moe_status_t moe_layer_fwd(const moe_config_t* cfg, const void* x, const float* 
  * where the layer's time is the bytes of the busy experts' weights: those
  * weights are read once and the rows of all tokens multiplied as they pass.
  * bf16 configurations without SAVE_FOR_BWD and without loss weights (else
- * MOE_ERR_UNSUPPORTED, as for T > 64).  p is applied to the expert's output.
- * Results may differ from moe_layer_fwd's in the last bits (other orders of
- * the fp32 sums).  Bitwise reproducible.  ws: moe_workspace_size(cfg) bytes, no
- * state of an earlier call is read, and what a moe_layer_fwd left there for a
- * backward is overwritten. */
+ * MOE_ERR_UNSUPPORTED, as for T > 64 and for sizes whose units of work do not
+ * fit 31 bits).  p is applied to the expert's output in fp32; the expert's
+ * hidden values are kept in bf16, as in moe_layer_fwd.  Results may differ from
+ * moe_layer_fwd's in the last bits (other orders of the fp32 sums).  Bitwise
+ * reproducible.  MOE_FLAG_GEMM_* and MOE_FLAG_HIST_FROM_ROUTER have no effect.
+ * ws: moe_workspace_size(cfg) bytes; no state of an earlier call is read, what
+ * a moe_layer_fwd left there for a backward is overwritten, and calls that can
+ * overlap on the GPU need a workspace each. */
 moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const void* x, const float* w_r,
                                const float* gate_bias, const float* sel_bias, const void* w1,
                                const void* b1, const void* w2, const void* b2,
@@ -393,9 +396,11 @@ moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const void* x, const flo
 
 /* The same with the expert weights in MXFP4 (as moe_mxfp4_quantize writes them:
  * W1 [E*2F, h] in uniform groups of 2F rows, W2 [E*h, F] in uniform groups of
- * h rows, the shared expert's as one group); activations stay 16-bit, the
- * products are of the weights' exact values.  SwiGLU, h and F multiples of 128
- * (else MOE_ERR_UNSUPPORTED). */
+ * h rows, the shared expert's as one group).  The weights enter with their exact
+ * values (a block of scale code 0, 2^-127, as zeros); tokens and hidden values
+ * as fp16 with a power-of-two scale per token, or per token and 32 hidden
+ * units: exact for bf16 tokens down to 2^-29 of the token's largest value.
+ * SwiGLU, h and F multiples of 128 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_layer_fwd_few_mxfp4(const moe_config_t* cfg, const void* x, const float* w_r,
                                      const float* gate_bias, const float* sel_bias,
                                      const uint8_t* w1_q, const uint8_t* w1_sf,

@@ -735,6 +735,7 @@ moe_status_t check_few(const moe_config_t* cfg, const void* x, const float* w_r,
   if (c.dtype != MOE_BF16 || c.T > kFewMaxT || (c.flags & MOE_FLAG_SAVE_FOR_BWD) ||
       c.aux_loss_coeff != 0.f || c.z_loss_coeff != 0.f)
     return MOE_ERR_UNSUPPORTED;
+  if (!few_counts_fit(c)) return MOE_ERR_UNSUPPORTED;
   if (c.T > 0 && (!x || !w_r || !y)) return MOE_ERR_INVALID_ARG;
   if (!al16(x) || !al16(w_r) || !al16(y)) return MOE_ERR_INVALID_ARG;
   return check_ws(cfg, ws, ws_bytes);

@@ -29,6 +29,14 @@ inline int few_ksplit(const moe_config_t& c) {
 constexpr int kFewCopies = 16;
 inline int few_pairs_pad(const moe_config_t& c) { return (c.T * c.K + 31) / 32 * 32; }
 
+// Whether every count of units and of finished warps fits 31 bits, with the
+// smallest units (8 tokens, 64 rows) and the most writers (16 a unit).
+inline bool few_counts_fit(const moe_config_t& c) {
+  const int64_t subs = (int64_t)c.T * c.K + (c.n_shared ? ceil_div(c.T, 8) : 0);
+  const int64_t r1 = c.act == MOE_ACT_SWIGLU ? 2LL * c.F : c.F, most = (1LL << 31) / 16;
+  return subs * ceil_div(r1, 64) < most && subs * ceil_div(c.h, 64) * few_ksplit(c) < most;
+}
+
 struct FewLayout {
   size_t sync, parts, idx, prob, xh, xs, a, as, ypart, total;
 };

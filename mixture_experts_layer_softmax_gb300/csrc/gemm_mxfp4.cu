@@ -165,6 +165,9 @@ struct Tile {
   int64_t scale;     // scale tile, -1: none
 };
 
+// Scale tiles a buffer has room for (descending offsets could ask for more).
+MOE_D int64_t tiles_room(int rows, int G) { return ((int64_t)rows + 127) / 128 + G; }
+
 MOE_D int64_t tiles_total(const Tiles& t, bool ragged, int rows, int G, int urows) {
   if (!ragged) return (int64_t)G * ((urows + 127) / 128);
   return (int64_t)t.rt[G] + (t.off[0] + 127) / 128 + (rows - t.off[G] + 127) / 128;
@@ -186,6 +189,7 @@ MOE_D Tile tile_at(const Tiles& t, bool ragged, int rows, int G, int urows, int6
     }
     o.row0 = t.off[lo] + (int)(i - t.rt[lo]) * 128;
     o.rows = min(128, t.off[lo + 1] - o.row0);
+    if (i >= tiles_room(rows, G)) o.scale = -1;
   } else {
     int k = (int)(i - t.rt[G]);
     const int before = (t.off[0] + 127) / 128;
@@ -294,6 +298,7 @@ __global__ void __launch_bounds__(256)
     const int64_t ti = un / KB;
     const int kb = (int)(un - ti * KB);
     const Tile tile = tile_at(s_t, ragged, rows, G, urows, ti);
+    if (tile.scale < 0) continue;
     uint32_t codes[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {

@@ -82,6 +82,8 @@ def test_few_tokens(M, call):
     for kw in (dict(T=65), dict(dtype=M.MOE_F32), dict(aux_loss_coeff=0.1), dict(z_loss_coeff=0.1),
                dict(flags=M.MOE_FLAG_SAVE_FOR_BWD | M.MOE_FLAG_VALIDATE_ONLY), dict(E=300)):
         assert call(M, _cfg(M, **kw)) == M.MOE_ERR_UNSUPPORTED
+    huge = _cfg(M, T=64, K=8, h=1 << 20, F=1 << 20)                # units past 31 bits
+    assert call(M, huge) == M.MOE_ERR_UNSUPPORTED
     for kw in (dict(K=9), dict(T=-1), dict(capacity=-1)):
         assert call(M, _cfg(M, **kw)) == M.MOE_ERR_INVALID_ARG
     for name in ("x", "w_r", "w1", "w2", "y"):

@@ -335,3 +335,80 @@ def test_mxfp4_set_as_a_server_uses_it():
     # (x and a) stay below the sum of both, as norms
     assert (y.float() - few.y.float()).norm() <= 0.5 * few.y.float().norm()
     assert (y.float() - few.y.float()).norm() > 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_nothing_is_written_outside_the_buffers(mx):
+    """The workspace and every output between guard bytes; dirty inside."""
+    M = lib()
+    for kw in (dict(T=1, h=128, E=8, K=2, F=128), dict(T=33, h=640, E=7, K=5, F=384, shared=1),
+               dict(T=64, h=256, E=256, K=16, F=256, force=True)):
+        f = Few(mx=mx, seed=31, **kw).device(M)
+        n, G = f.ws.numel(), 8192
+        big = torch.full((n + 2 * G,), 0x5A, dtype=torch.uint8, device="cuda")
+        y = torch.full((f.T + 8, f.h), 3.0, dtype=torch.bfloat16, device="cuda")
+        idx = torch.full((f.T + 8, f.K), -7, dtype=torch.int32, device="cuda")
+        prob = torch.full((f.T + 8, f.K), -7.0, device="cuda")
+        f.idx, f.prob, f.y = idx[4:-4], prob[4:-4], y[4:-4]
+        # rows of 2 * 128 bytes and more keep y's first row 16-byte aligned
+        f.call(M, ws=big[G:G + n])
+        torch.cuda.synchronize()
+        assert M.moe_get_error() == M.MOE_OK
+        assert (big[:G] == 0x5A).all() and (big[G + n:] == 0x5A).all()
+        for b, v in ((y, 3.0), (idx, -7), (prob, -7.0)):
+            assert (b[:4] == v).all() and (b[-4:] == v).all()
+        f.check(M)
+
+
+def test_mxfp4_blocks_of_nan_and_zero_scales():
+    """A weight block of NaN scale makes its output columns NaN, for the tokens of
+    its expert alone; a block of zeros (scale code 0) adds nothing."""
+    M = lib()
+    f = Few(T=6, h=256, E=3, K=1, F=128, mx=True, force=True, seed=5)
+    w2 = f.w2_bf16.copy()
+    w2[1, 40, 64:96] = np.nan          # expert 1 (tokens 1 and 4), output column 40
+    w2[2, 7, 32:64] = 0.0
+    f.w2_bf16, clean = w2, f.w2.copy()
+    clean[1, 40, 64:96] = 0.0
+    clean[2, 7, 32:64] = 0.0
+    f.w2 = clean
+    f.device(M)
+    f.call(M)
+    torch.cuda.synchronize()
+    assert M.moe_get_error() == M.MOE_OK
+    y = to_np(f.y)
+    nan = np.isnan(y)
+    assert nan[[1, 4], 40].all() and nan.sum() == 2
+    f.y = torch.where(torch.isnan(f.y), torch.zeros_like(f.y), f.y)
+    keep = np.ones((6, 256), bool)
+    keep[[1, 4], 40] = False
+    ref, tol = np.zeros((6, 256)), np.zeros((6, 256))
+    for t in range(6):
+        o, do = f.expert(f.x[t:t + 1].astype(np.float64), f.w1[t % 3], f.w2[t % 3], None, None)
+        ref[t], tol[t] = o[0], do[0]
+    tol += 2.0 ** -8 * (np.abs(ref) + tol)
+    assert (np.abs(to_np(f.y) - ref) <= tol)[keep].all()
+
+
+def test_in_place_and_long_rows():
+    """y may be x; a long second projection takes several slices of F."""
+    M = lib()
+    f = run(T=3, h=512, E=2, K=1, F=9000)
+    want = f.y.clone()
+    f.call(M, y=f.d["x"])
+    torch.cuda.synchronize()
+    assert torch.equal(f.d["x"], want)
+
+
+def test_injected_failure_enqueues_nothing():
+    M = lib()
+    f = Few(T=4, h=128, E=4, K=2, F=128).device(M)
+    assert M.moe_test_inject_cuda_failure(1) == 0
+    with pytest.raises(M.MoeError) as e:
+        f.call(M)
+    assert e.value.status == M.MOE_ERR_CUDA
+    torch.cuda.synchronize()
+    assert torch.isnan(f.y).all() and (f.idx == -1).all()
+    f.call(M)
+    torch.cuda.synchronize()
+    f.check(M)

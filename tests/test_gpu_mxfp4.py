@@ -285,3 +285,75 @@ def test_two_streams_and_graph_replay():
     torch.cuda.synchronize()
     assert torch.equal(a, got) and not torch.equal(a, want)
     assert M.moe_get_error() == M.MOE_OK
+
+
+def test_nothing_is_written_outside_the_buffers():
+    """Codes, scales, values and product outputs between guard bytes."""
+    M = lib()
+    for rows, K, offsets, groups in SHAPES:
+        x = to_dev(hard_rows(np.random.default_rng(rows), rows, K), "bf16")
+        nsf, G = M.moe_mxfp8_scale_bytes(rows, K, groups), 4096
+        q = torch.full((rows * K // 2 + 2 * G,), 0x77, dtype=torch.uint8, device="cuda")
+        sf = torch.full((nsf + 2 * G,), 0x77, dtype=torch.uint8, device="cuda")
+        out = torch.full((rows * K + 2 * G,), 5.0, dtype=torch.bfloat16, device="cuda")
+        od = None if offsets is None else torch.from_numpy(np.asarray(offsets, np.int32)).cuda()
+        M.moe_mxfp4_quantize(rows, K, groups, od, x, q[G:-G], sf[G:-G])
+        M.moe_mxfp4_dequantize(rows, K, groups, od, q[G:-G], sf[G:-G], out[G:-G])
+        torch.cuda.synchronize()
+        for b, v in ((q, 0x77), (sf, 0x77), (out, 5.0)):
+            assert (b[:G] == v).all() and (b[-G:] == v).all()
+    c = _case(seed=11, T=131, K=2, E=5, h=384, F=128, skew=True)
+    P, E, h, F, offs = c["P"], c["E"], c["h"], c["F"], c["offsets"]
+    cfg = M.make_config(c["T"], h, E, c["K"], F)
+    od = torch.from_numpy(offs.astype(np.int32)).cuda()
+    xq, xsf = quantize_dev(M, c["x"], E, offs)
+    w1q, w1sf = quantize_dev(M, c["w1"], E)
+    w2q, w2sf = quantize_dev(M, c["w2"], E)
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    nsf = M.moe_mxfp8_scale_bytes(P, F, E)
+    for shift in (0, 8):                # outputs on a 32-byte boundary, and 16 bytes off it
+        a = torch.full((P * F + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
+        y = torch.full((P * h + 64,), 5.0, dtype=torch.bfloat16, device="cuda")
+        aq, asf = torch.full((P * F // 2 + 64,), 0x77, **u8), torch.full((nsf + 64,), 0x77, **u8)
+        av, yv = a[16 + shift:16 + shift + P * F], y[16 + shift:16 + shift + P * h]
+        M.moe_expert_fc1_mxfp4(cfg, xq, xsf, od, None, w1q, w1sf, av, aq[32:-32], asf[32:-32])
+        M.moe_expert_fc2_mxfp4(cfg, aq[32:-32], asf[32:-32], od, w2q, w2sf, yv)
+        torch.cuda.synchronize()
+        assert M.moe_get_error() == M.MOE_OK
+        for b, v in ((aq, 0x77), (asf, 0x77)):
+            assert (b[:32] == v).all() and (b[-32:] == v).all()
+        for b, n in ((a, P * F), (y, P * h)):
+            assert (b[:16 + shift] == 5).all() and (b[16 + shift + n:] == 5).all()
+        if shift == 0:
+            first = av.clone(), yv.clone()
+        else:
+            assert torch.equal(av, first[0]) and torch.equal(yv, first[1])
+
+
+def test_descending_offsets_stay_in_bounds():
+    """Offsets are the caller's promise; a broken one must not reach past the
+    scale buffer (the kernel cuts boundaries to the rows and tiles to the room)."""
+    M = lib()
+    rows, K, G = 300, 256, 6
+    off = torch.tensor([0, 300, 0, 300, -5, 300, 1 << 30], dtype=torch.int32, device="cuda")
+    n = M.moe_mxfp8_scale_bytes(rows, K, G)
+    x = torch.ones(rows, K, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(rows, K // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.full((n + 8192,), 0x77, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    M.moe_mxfp4_quantize(rows, K, G, off, x, q, sf[:n])
+    M.moe_mxfp4_dequantize(rows, K, G, off, q, sf[:n], out)
+    torch.cuda.synchronize()
+    assert (sf[n:] == 0x77).all()
+
+
+def test_injected_failure_enqueues_nothing():
+    M = lib()
+    x = torch.ones(16, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.full((16, 64), 0x77, dtype=torch.uint8, device="cuda")
+    sf = torch.full((M.moe_mxfp8_scale_bytes(16, 128, 1),), 0x77, dtype=torch.uint8, device="cuda")
+    assert M.moe_test_inject_cuda_failure(1) == 0
+    with pytest.raises(M.MoeError):
+        M.moe_mxfp4_quantize(16, 128, 1, None, x, q, sf)
+    torch.cuda.synchronize()
+    assert (q == 0x77).all() and (sf == 0x77).all()
