@@ -253,6 +253,7 @@ struct alignas(16) FewStage {
   int pad[3];
 };
 
+constexpr uint16_t kNoExpert = 0xffff;
 constexpr int kMaxEntries = 257, kMaxPairs = kFewMaxT * 16, kMaxStages = 12;
 
 struct FewCtl {
@@ -269,9 +270,9 @@ struct FewCtl {
   int cum1[kMaxEntries + 1], cum2[kMaxEntries + 1];  // units before entry j
   int start[kMaxEntries];                // first sorted pair of an expert
   uint32_t mask[2][kMaxEntries];         // tokens of an expert: 0 .. 31, 32 .. 63
-  int idx[kMaxPairs];
-  float prob[kMaxPairs];
+  uint16_t idx[kMaxPairs];       // expert of a pair (kNoExpert: out of range)
   int16_t pos_of[kMaxPairs];     // sorted position of pair p, -1: dropped
+  float xs[kFewMaxT];            // scales of the fp16 tokens (MXFP4 weights)
   uint8_t tok_of[kMaxPairs + kFewMaxT];  // token of a sorted position
 };
 
@@ -313,7 +314,7 @@ struct FewTile {
   static constexpr int BS_ROW = W4 ? KC / 32 * 4 : 0;
   static constexpr int STAGE = (A_BYTES + B_BYTES + SF + NB * BS_ROW + 1023) / 1024 * 1024;
   static constexpr int RED_TOK = RT + 4;  // padded token stride of the meeting buffer
-  static constexpr int REDS = NT >= 4 ? 1 : 2;  // meeting buffers
+  static constexpr int REDS = NT > 2 ? 1 : 2;  // meeting buffers (one of them fits beside more tokens)
   static constexpr int RED1 = KG * NB * RED_TOK * 4, RED = REDS * RED1;
   static constexpr int THREADS = 32 * (NW + 2);
   static_assert(MT % MPW == 0 && NW % MG == 0 && NW >= 8 && KB % KW == 0 &&
@@ -341,8 +342,9 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, P = cf.T * cf.K;
   for (int p = threadIdx.x; p < P; p += L::THREADS) {
     const int e = c.idx[p];
-    if (e < 0 || e >= cf.E) report(status, MOE_ERR_DEVICE_BOUNDS);
-    else {
+    if (e == kNoExpert) {
+      report(status, MOE_ERR_DEVICE_BOUNDS);
+    } else {
       const int t = p / cf.K;
       atomicOr(&c.mask[t >> 5][e], 1u << (t & 31));
     }
@@ -399,7 +401,7 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
   for (int p = threadIdx.x; p < P; p += L::THREADS) {
     const int e = c.idx[p], t = p / cf.K;
     int pos = -1;
-    if (e >= 0 && e < cf.E) {
+    if (e != kNoExpert) {
       const uint32_t below = (1u << (t & 31)) - 1;
       const int rank = t < 32 ? __popc(c.mask[0][e] & below)
                               : __popc(c.mask[0][e]) + __popc(c.mask[1][e] & below);
@@ -539,11 +541,14 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
   int32_t* claim = p.sync;
   // the first unit's number comes while the list is made
   const int first_claim = threadIdx.x == 32 * L::NW ? atomicAdd(claim, 1) : 0;
+  const int64_t at = (int64_t)(blockIdx.x % kFewCopies) * p.pairs_pad;  // this block's copy
   {
-    const int64_t at = (int64_t)(blockIdx.x % kFewCopies) * p.pairs_pad;
     for (int i = threadIdx.x; i < cf.T * cf.K; i += L::THREADS) {
-      ctl.idx[i] = __ldcg(p.idx + at + i);
-      ctl.prob[i] = __ldcg(p.prob + at + i);
+      const int e = __ldcg(p.idx + at + i);
+      ctl.idx[i] = e >= 0 && e < cf.E ? (uint16_t)e : kNoExpert;
+    }
+    if (L::W4 && threadIdx.x < cf.T) {
+      ctl.xs[threadIdx.x] = __ldcg(p.xs + threadIdx.x);
     }
   }
   __syncthreads();
@@ -909,17 +914,18 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const int rw = (warp + L::NW - unit % L::NW) % L::NW;  // place among the writers
       ++unit;
       const int width = st.kind == kFC1 ? width1 : L::RT;
-      if (rw >= few_writers(st.n, width, L::NW)) continue;
+      const int writers = few_writers(st.n, width, L::NW);
+      if (rw >= writers) continue;
       const int items = st.n * width;
       if (st.kind == kFC1) {
         const int e = ctl.ent_e[st.entry];
-        for (int i0 = rw * 32; i0 < items; i0 += 32 * L::NW) {  // whole warps (shuffles below)
+        for (int i0 = rw * 32; i0 < items; i0 += 32 * writers) {  // whole warps (shuffles below)
           const int i = i0 + lane;
           const int tok = min(i / width, st.n - 1), f = i % width;
           const bool valid = i < items && st.r0 + f < cf.F;
           const int pos = st.pos0 + tok;
           float v;
-          const float s = L::W4 ? __ldg(p.xs + ctl.tok_of[pos]) : 1.f;
+          const float s = L::W4 ? ctl.xs[ctl.tok_of[pos]] : 1.f;
           if (glu) {
             const int row = f / 8 * 16 + (f & 7);
             v = silu_f(sum(tok, row) * s) * (sum(tok, row + 8) * s);
@@ -950,7 +956,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) red_release(done + st.entry, 1);
       } else {
-        for (int i = rw * 32 + lane; i < items; i += 32 * L::NW) {
+        for (int i = rw * 32 + lane; i < items; i += 32 * writers) {
           const int tok = i / L::RT, row = i % L::RT;
           if (st.r0 + row < cf.h)
             __stcg(p.ypart + ((int64_t)st.ks * p.S + st.pos0 + tok) * cf.h + st.r0 + row, sum(tok, row));
@@ -984,7 +990,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           const int pr = t * cf.K + k;
           const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
           if (pos < 0) continue;  // dropped
-          const float w = shared ? 1.f : ctl.prob[pr];
+          const float w = shared ? 1.f : __ldcg(p.prob + at + pr);
           const float* src = p.ypart + (int64_t)pos * cf.h + r;
           float4 o[4];
 #pragma unroll
@@ -1150,7 +1156,7 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
     return many ? few_launch<FewTile<true, 8, 2, 2, 16, 512>>(p, xh, s)
                 : few_launch<FewTile<true, 8, 2, 1, 16, 512>>(p, xh, s);
   return many ? few_launch<FewTile<false, 4, 2, 2, 8, 256>>(p, xh, s)
-              : few_launch<FewTile<false, 4, 2, 1, 8, 512>>(p, xh, s);
+              : few_launch<FewTile<false, 4, 2, 1, 16, 256>>(p, xh, s);
 }
 
 }  // namespace moe
