@@ -564,19 +564,21 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 
   if (warp == L::NW) {
     // ================= weights =================
-    if (lane == 0) {
+    // (as for the tokens, one elected lane of the whole warp issues)
+    {
+      const bool elected = tc::elect_one();
       int stage = 0, j1 = 0, j2 = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
       const uint64_t policy = evict_first_policy();
       int next = first_claim;
       bool ok = true;
       while (ok) {
-        const int u = next;
-        if (u < total) next = atomicAdd(claim, 1);  // the next unit, while this one streams
+        const int u = __shfl_sync(0xffffffffu, next, 0);
+        if (u < total && lane == 0) next = atomicAdd(claim, 1);  // the next unit, while this one streams
         FewStage st{};
         int kbeg = 0, kend = 1, cols = 0, nrows = 0;
         const CUtensorMap* map = nullptr;
-        const uint8_t* sf = nullptr;
+        const uint8_t *sf0 = nullptr, *sf1 = nullptr;  // scales of the rows, of the up rows
         int half0 = 0;  // the map's third coordinate
         bool pairs_of_rows = false;
         if (u < total) {
@@ -616,8 +618,9 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           half0 = shared ? 0 : e * (pairs_of_rows ? 2 : 1);
           if (L::W4) {
             const FewWeights& W = st.kind == kFC1 ? p.a.w1 : p.a.w2;
-            sf = shared ? W.ws_sf
-                        : W.sf + (int64_t)e * (nrows / 128) * (cols / 128) * mx::ATOM;
+            const uint8_t* sf = shared ? W.ws_sf : W.sf + (int64_t)e * (nrows / 128) * (cols / 128) * mx::ATOM;
+            sf0 = sf + (int64_t)(st.r0 / 128) * (cols / 128) * mx::ATOM;
+            sf1 = sf + (int64_t)((st.r0 + cf.F) / 128) * (cols / 128) * mx::ATOM;
           }
         }
         for (int k0 = kbeg; k0 < kend; k0 += L::KC) {
@@ -626,29 +629,33 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           st.kc = min(L::KC, kend - k0);
           st.k0 = k0;
           st.last = k0 + L::KC >= kend;
-          ctl.st[stage] = st;
           const int nkb = (st.kc + L::KB - 1) / L::KB;
           const uint32_t sf_bytes = L::W4 ? st.kc / 128 * mx::ATOM : 0;
           const uint32_t tx = nkb * L::RT * L::A_ROW + sf_bytes * (pairs_of_rows ? 2 : 1);
-          tc::mbar_arrive_expect_tx(fb, st.kind == kEnd ? 0 : tx);
-          tc::mbar_arrive(tc::smem_u32(&ctl.told[stage]));
+          const uint32_t a_dst = ring0 + stage * L::STAGE;
+          if (elected) {
+            ctl.st[stage] = st;
+            tc::mbar_arrive_expect_tx(fb, st.kind == kEnd ? 0 : tx);
+            tc::mbar_arrive(tc::smem_u32(&ctl.told[stage]));
+            if (st.kind != kEnd) {
+#pragma unroll
+              for (int b = 0; b < L::NKB; ++b)
+                if (b < nkb)
+                  tma_load_3d(a_dst + b * L::RT * L::A_ROW, map, (k0 + b * L::KB) / (L::W4 ? 2 : 1),
+                              st.r0, half0, fb, policy);
+              if (L::W4) {  // the scales of the unit's rows: atoms of their 128-row tile
+                const uint32_t sf_dst = a_dst + L::A_BYTES + L::B_BYTES;
+                tc::bulk_load(sf_dst, sf0 + (int64_t)(k0 / 128) * mx::ATOM, sf_bytes, fb);
+                if (pairs_of_rows)
+                  tc::bulk_load(sf_dst + L::SF / 2, sf1 + (int64_t)(k0 / 128) * mx::ATOM, sf_bytes, fb);
+              }
+            }
+          }
+          __syncwarp();
           if (st.kind == kEnd) {
             issued &= ~(1u << stage);  // its copies are consumed, its barrier a phase further
             ok = false;
             break;
-          }
-          const uint32_t a_dst = ring0 + stage * L::STAGE;
-          for (int b = 0; b < nkb; ++b)
-            tma_load_3d(a_dst + b * L::RT * L::A_ROW, map, (k0 + b * L::KB) / (L::W4 ? 2 : 1),
-                        st.r0, half0, fb, policy);
-          if (L::W4) {  // the scales of the unit's rows: atoms of their 128-row tile
-            const uint32_t sf_dst = a_dst + L::A_BYTES + L::B_BYTES;
-            for (int i = 0; i < (pairs_of_rows ? 2 : 1); ++i) {
-              const int row = st.r0 + i * cf.F;
-              tc::bulk_load(sf_dst + i * (L::SF / 2),
-                            sf + ((int64_t)(row / 128) * (cols / 128) + k0 / 128) * mx::ATOM,
-                            sf_bytes, fb);
-            }
           }
           issued |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
