@@ -31,9 +31,10 @@
 // warps split a stage's columns and multiply with m16n8k16 tensor-core
 // instructions, weight rows as M, tokens as N: the weights are read once from
 // HBM however many tokens share them, and a product with up to 32 tokens costs
-// less than the loads.  (tcgen05 wants 128 weight rows a tile; that would
-// leave too few units to balance the SMs, and the mma rate is not what bounds
-// this kernel.)
+// less than the loads.  (Beside bf16 weights the mma rate is not what bounds
+// this kernel, and 64-row units balance the SMs better than tcgen05's 128.
+// Beside MXFP4 weights decoding the codes on the ALUs is: 34 instructions for
+// each 16 x 32 weights.)
 // At a unit's end the warps' sums meet in shared memory, in warp order.
 //
 // "Scalable Training of Mixture-of-Experts Models with Megatron Core" (review),
@@ -151,11 +152,13 @@ __device__ __noinline__ void few_select_exact(const float* logit, int t, RouterA
 }
 
 // Adds the partial logits and selects: a block a token, a thread an expert, with
-// select_and_write's choices.  A decoding step runs this code once, from a cold
-// instruction cache, and the fetches are what it waits for (select_and_write in
-// a warp took 13 us for one token of 256 experts): so each thread ranks its
-// expert by counting the keys above its own, in a short loop.  The results are
-// written kFewCopies times: each block of few_kernel reads one of the copies.
+// select_and_write's choices: each thread ranks its expert by counting the keys
+// above its own.  (A warp a token with the logits in registers, as the large
+// router has it, took 9.5 us for one token of 64 experts and 16 us of 256; this
+// 2.8 and 5.6, four threads an expert 4 and 5.5.)  The biases are read before the
+// partial logits are there: the router, a plain launch, runs, so what came before
+// it on the stream is done.  The results are written kFewCopies times: each block
+// of few_kernel reads one of the copies.
 __global__ void __launch_bounds__(256)
     few_select_kernel(const float* __restrict__ parts, int kparts, const float* gate_bias,
                       RouterArgs r, int pairs_pad, int32_t* idx_out, float* prob_out) {
@@ -167,14 +170,17 @@ __global__ void __launch_bounds__(256)
   const int e = threadIdx.x, t = blockIdx.x, lane = threadIdx.x & 31;
   const bool sig = r.score == MOE_SCORE_SIGMOID;
   pdl_trigger();
+  const float gb = gate_bias && e < r.E ? __ldg(gate_bias + e) : 0.f;
+  const float sb = r.sel_bias && e < r.E ? __ldg(r.sel_bias + e) : 0.f;
   pdl_wait();
   float l = 0.f;
   uint32_t key = 0u;  // order-preserving, 0 past E
   if (e < r.E) {
 #pragma unroll 4
     for (int p = 0; p < kparts; ++p) l += __ldcg(parts + ((int64_t)p * r.T + t) * r.E + e);
-    if (gate_bias) l += __ldg(gate_bias + e);
-    key = sortable_key(selection_key_fast(l, e, r));
+    l += gb;
+    const float fast = sig ? sigmoid_f(l) : l;  // selection_key_fast
+    key = sortable_key(r.sel_bias ? __fadd_rn(fast, sb) : fast);
   }
   s_logit[e] = l;
   s_key[e] = key;
@@ -254,6 +260,7 @@ struct alignas(16) FewStage {
 };
 
 constexpr uint16_t kNoExpert = 0xffff;
+constexpr int kMaxChunks = 9;  // of 32 experts, the shared one included
 constexpr int kMaxEntries = 257, kMaxPairs = kFewMaxT * 16, kMaxStages = 12;
 
 struct FewCtl {
@@ -269,6 +276,7 @@ struct FewCtl {
   int ent_n[kMaxEntries];        // pairs
   int cum1[kMaxEntries + 1], cum2[kMaxEntries + 1];  // units before entry j
   int start[kMaxEntries];                // first sorted pair of an expert
+  alignas(16) int4 part[kMaxChunks];     // busy experts, pairs, units and writers of 32 experts
   uint32_t mask[2][kMaxEntries];         // tokens of an expert: 0 .. 31, 32 .. 63
   uint16_t idx[kMaxPairs];       // expert of a pair (kNoExpert: out of range)
   int16_t pos_of[kMaxPairs];     // sorted position of pair p, -1: dropped
@@ -354,47 +362,51 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
     c.mask[threadIdx.x][cf.E] = n >= 32 ? ~0u : n > 0 ? (1u << n) - 1 : 0u;
   }
   __syncthreads();
-  // busy experts in order, 32 experts a step (the shared expert is one more);
-  // a loop of few instructions, as they are fetched once
-  if (warp == 0) {
-    const int last = cf.E + (cf.n_shared ? 1 : 0);
-    int ents = 0, pairs = 0, subs = 0, writers = 0;
-#pragma unroll 1
-    for (int e0 = 0; e0 < last; e0 += 32) {
-      const int e = e0 + lane;
-      int n = e < last ? __popc(c.mask[0][e]) + __popc(c.mask[1][e]) : 0;
-      if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
-      const uint32_t busy = __ballot_sync(0xffffffffu, n > 0);
-      if (busy == 0) continue;
-      const int sub = (n + L::NB - 1) / L::NB;
-      int ip = n, is = sub;
-      if (!__any_sync(0xffffffffu, n > 1)) {  // at most one token an expert: count the busy ones
-        ip = is = __popc(busy & (0xffffffffu >> (31 - lane)));
-      } else
+  // busy experts in order (the shared expert is one more): a warp takes 32 experts,
+  // counts, and continues after the warps before it
+  const int last = cf.E + (cf.n_shared ? 1 : 0), chunks = (last + 31) / 32;
+  static_assert(L::NW + 2 >= kMaxChunks, "a warp for every 32 experts");
+  {
+    const int e = warp * 32 + lane;
+    int n = warp < chunks && e < last ? __popc(c.mask[0][e]) + __popc(c.mask[1][e]) : 0;
+    if (e < cf.E && cf.capacity > 0) n = min(n, cf.capacity);
+    const uint32_t busy = __ballot_sync(0xffffffffu, n > 0);
+    const int sub = (n + L::NB - 1) / L::NB;
+    int ip = n, is = sub;
+    if (!__any_sync(0xffffffffu, n > 1)) {  // at most one token an expert: count the busy ones
+      ip = is = __popc(busy & (0xffffffffu >> (31 - lane)));
+    } else {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int a = __shfl_up_sync(0xffffffffu, ip, o), b = __shfl_up_sync(0xffffffffu, is, o);
         if (lane >= o) { ip += a; is += b; }
       }
-      if (n > 0) {
-        const int j = ents + __popc(busy & ((1u << lane) - 1));
-        c.start[e] = c.ent_start[j] = pairs + ip - n;
-        c.ent_e[j] = e;
-        c.ent_n[j] = n;
-        c.cum1[j] = (subs + is - sub) * nrb1;
-        c.cum2[j] = (subs + is - sub) * nrb2 * ksplit;
-        writers += few_writers_of(n, L::NB, L::RT, L::NW);
-      }
-      ents += __popc(busy);
-      pairs += __shfl_sync(0xffffffffu, ip, 31);
-      subs += __shfl_sync(0xffffffffu, is, 31);
     }
-    writers = __reduce_add_sync(0xffffffffu, writers);
-    if (lane == 0) {
-      c.pairs = pairs;
-      c.cum1[ents] = c.units1 = subs * nrb1;
-      c.cum2[ents] = c.units2 = subs * nrb2 * ksplit;
-      c.fc2_writers = writers * nrb2 * ksplit;
+    const int writers = __reduce_add_sync(0xffffffffu, few_writers_of(n, L::NB, L::RT, L::NW));
+    if (lane == 31 && warp < chunks) c.part[warp] = make_int4(__popc(busy), ip, is, writers);
+    __syncthreads();
+    int4 before = make_int4(0, 0, 0, 0);
+    for (int ch = 0; ch < min(warp, chunks); ++ch) {
+      const int4 v = c.part[ch];
+      before.x += v.x; before.y += v.y; before.z += v.z; before.w += v.w;
+    }
+    if (n > 0) {
+      const int j = before.x + __popc(busy & ((1u << lane) - 1)), u = before.z + is - sub;
+      c.start[e] = c.ent_start[j] = before.y + ip - n;
+      c.ent_e[j] = e;
+      c.ent_n[j] = n;
+      c.cum1[j] = u * nrb1;
+      c.cum2[j] = u * nrb2 * ksplit;
+    }
+    if (warp == L::NW + 1 && lane == 0) {  // past every chunk but perhaps its own
+      if (warp < chunks) {
+        const int4 v = c.part[warp];
+        before.x += v.x; before.y += v.y; before.z += v.z; before.w += v.w;
+      }
+      c.pairs = before.y;
+      c.cum1[before.x] = c.units1 = before.z * nrb1;
+      c.cum2[before.x] = c.units2 = before.z * nrb2 * ksplit;
+      c.fc2_writers = before.w * nrb2 * ksplit;
     }
   }
   __syncthreads();
