@@ -396,11 +396,11 @@ moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const void* x, const flo
 
 /* The same with the expert weights in MXFP4 (as moe_mxfp4_quantize writes them:
  * W1 [E*2F, h] in uniform groups of 2F rows, W2 [E*h, F] in uniform groups of
- * h rows, the shared expert's as one group).  The weights enter with their exact
- * values (a block of scale code 0, 2^-127, as zeros); tokens and hidden values
- * as fp16 with a power-of-two scale per token, or per token and 32 hidden
- * units: exact for bf16 tokens down to 2^-29 of the token's largest value.
- * SwiGLU, h and F multiples of 128 (else MOE_ERR_UNSUPPORTED). */
+ * h rows, the shared expert's as one group).  The products run as block-scaled
+ * tensor-core MMAs on the weights' exact values; tokens and hidden values enter
+ * as sums of four E2M1 blocks of 32 columns, which are within 2^-11 of the
+ * block's largest magnitude of them (bf16's own half step is 2^-9 of a value).
+ * A block of them that holds an infinity or a NaN counts as NaNs.  SwiGLU, h and F multiples of 128 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_layer_fwd_few_mxfp4(const moe_config_t* cfg, const void* x, const float* w_r,
                                      const float* gate_bias, const float* sel_bias,
                                      const uint8_t* w1_q, const uint8_t* w1_sf,

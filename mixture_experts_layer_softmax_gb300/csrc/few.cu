@@ -5,12 +5,11 @@
 //
 // The expert weights are the traffic: each busy expert's matrices are read
 // from HBM for a handful of rows.  bf16 weights, or MXFP4 weights (E2M1 codes
-// with one E8M0 scale per 32 columns; scale code 0, 2^-127, counts as zero: what
-// it scales is below fp32's normal numbers).
+// with one E8M0 scale per 32 columns).
 //
 // Three launches, each started while the one before drains (programmatic
 // dependent launch).  few_router_kernel writes partial logits (and, for MXFP4
-// weights, the tokens in fp16); few_select_kernel adds them and selects, a warp
+// weights, the tokens as E2M1 parts); few_select_kernel adds them and selects, a warp
 // a token.  few_kernel does the rest, one block per SM:
 //   every block sorts the (token, slot) pairs by expert (the same list
 //   everywhere), then takes units of work from one counter: first all of FC1's
@@ -33,14 +32,14 @@
 // HBM however many tokens share them, and a product with up to 32 tokens costs
 // less than the loads.  (Beside bf16 weights the mma rate is not what bounds
 // this kernel, and 64-row units balance the SMs better than tcgen05's 128.
-// Beside MXFP4 weights decoding the codes on the ALUs is: 34 instructions for
-// each 16 x 32 weights.)
+// MXFP4 weights have a kernel of their own, few_mx_kernel, below.)
 // At a unit's end the warps' sums meet in shared memory, in warp order.
 //
 // "Scalable Training of Mixture-of-Experts Models with Megatron Core" (review),
 // §2.1 (the four steps), §2.2 (router); the same formulas and options as
 // moe_layer_fwd.
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 
 #include <type_traits>
 
@@ -56,38 +55,53 @@ namespace {
 MOE_D void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MOE_D void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// The power of two that brings a largest magnitude (fp32 bits m) into
-// [2^14, 2^15) when the values are divided by it; 1 for a row with an infinity or
-// a NaN (they stay what they are), the smallest useful one below 2^-86.
-MOE_D float f16_block_scale(uint32_t m) {
-  const int e = (int)(m >> 23);
-  if (e == 255) return 1.f;
-  return __uint_as_float((uint32_t)(max(e, 41) - 14) << 23);
-}
-// Tokens in fp16: x = xh * xs with xs a power of two that puts the token's
-// largest magnitude into [2^14, 2^15).  Exact for values down to 2^-29 of the
-// largest; below, the error is at most 2^-40 of it, far under the fp32 sums'.
-__device__ void few_convert_token(const __nv_bfloat16* __restrict__ x, int h,
-                                  __half* __restrict__ xh, float* __restrict__ xs) {
-  __shared__ uint32_t s_max[8];
-  uint32_t m = 0;
-  for (int v = threadIdx.x; v < h / 8; v += blockDim.x) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(x) + v);
-    for (uint32_t w : {u.x, u.y, u.z, u.w}) m = max(m, max((w << 16) & 0x7fff0000u, w & 0x7fff0000u));
-  }
+// ---- E2M1 parts --------------------------------------------------------------------
+// A block of 32 values, one a lane, as a sum of kParts E2M1 blocks, each with a
+// scale of its own: part 0 rounds v / s, s the power of two that puts the largest
+// magnitude into [2, 4), and each further part what the ones before left.  There
+// E2M1's steps are at most 1, so part 0 leaves at most s / 2; at s / 4 that is at
+// most 2, steps of 1/2, and from then on every part takes three bits: the four
+// leave at most s / 1024, 2^-11 of the block's largest value (a bf16 number's own
+// half step is 2^-9 of it).  A block with an infinity or a NaN gets the NaN scale.
+constexpr int kParts = 4;
+MOE_D void e2m1_parts(float v, uint32_t (&code)[kParts], uint32_t (&scale)[kParts]) {
+  uint32_t m = __float_as_uint(v) & 0x7fffffffu;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
-  __syncthreads();
-  for (int w = 0; w < 8; ++w) m = max(m, s_max[w]);
-  const float scale = f16_block_scale(m), inv = 1.f / scale;
-  if (threadIdx.x == 0) *xs = scale;
-  for (int v = threadIdx.x; v < h / 8; v += blockDim.x) {
-    const Vec<__nv_bfloat16> u = ldg16(x + v * 8);
-    __half o[8];
+  const int e = (int)(m >> 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = __float2half_rn(to_f32(u.v[i]) * inv);
-    *reinterpret_cast<uint4*>(xh + v * 8) = *reinterpret_cast<const uint4*>(o);
+  for (int i = 0; i < kParts; ++i) {
+    const int x = max(e - 1 - (i == 0 ? 0 : 3 * i - 1), 0);
+    scale[i] = e == 255 ? (i == 0 ? 255u : 0u) : (uint32_t)x;
+    const uint32_t c = e == 255 ? 0u
+        : __nv_cvt_float2_to_fp4x2(make_float2(v * __uint_as_float((254u - x) << 23), 0.f), __NV_E2M1,
+                                   cudaRoundNearest) & 15u;
+    code[i] = c;
+    v -= __uint_as_float((c & 8u) << 28 | (c & 7u) << 22) * 0x1p126f * mx::e8m0_value((uint32_t)x);
+  }
+}
+// The 32 lanes' codes as words of eight, the first lane's lowest; valid on lanes
+// 0, 8, 16, 24.
+MOE_D uint32_t pack_codes(uint32_t code, int lane) {
+  uint32_t w = code << (4 * (lane & 7));
+#pragma unroll
+  for (int o = 1; o <= 4; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+  return w;
+}
+
+// A token's columns b0 .. b1 - 1 (blocks of 32) as parts: a warp a block.
+__device__ void few_split_token(const __nv_bfloat16* __restrict__ x, int h, int b0, int b1,
+                                uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int b = b0 + warp; b < b1; b += blockDim.x / 32) {
+    uint32_t code[kParts], scale[kParts];
+    e2m1_parts(to_f32(x[b * 32 + lane]), code, scale);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      const uint32_t w = pack_codes(code[i], lane);
+      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(q + (int64_t)i * (h / 2) + b * 16 + lane / 2) = w;
+      if (lane == 0) sf[(int64_t)i * (h / 32) + b] = (uint8_t)scale[i];
+    }
   }
 }
 
@@ -96,17 +110,19 @@ __device__ void few_convert_token(const __nv_bfloat16* __restrict__ x, int h,
 // x is exact in fp32 and the products and sums are fp32, each lane over its
 // own columns, the lanes added as a tree.  The blocks past the router's convert
 // one token each; block 0 clears the counters of few_kernel.
-constexpr int kRouteTok = 8;
+constexpr int kRouteTok = 8, kSplitCols = 1024;
 __global__ void __launch_bounds__(256)
     few_router_kernel(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w_r, int T,
                       int E, int h, int kparts, float* __restrict__ parts, int route_blocks,
-                      __half* xh, float* xs, int32_t* sync, int sync_words) {
+                      uint8_t* xq, uint8_t* xs, int32_t* sync, int sync_words) {
   pdl_trigger();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < sync_words; i += blockDim.x) sync[i] = 0;
   if ((int)blockIdx.x >= route_blocks) {
-    const int t = blockIdx.x - route_blocks;
-    few_convert_token(x + (int64_t)t * h, h, xh + (int64_t)t * h, xs + t);
+    const int per = (h + kSplitCols - 1) / kSplitCols, i = blockIdx.x - route_blocks;
+    const int t = i / per, b0 = i % per * (kSplitCols / 32);
+    few_split_token(x + (int64_t)t * h, h, b0, min(b0 + kSplitCols / 32, h / 32),
+                    xq + (int64_t)t * kParts * (h / 2), xs + (int64_t)t * kParts * (h / 32));
     return;
   }
   // one warp per (expert, slice, eight tokens)
@@ -280,22 +296,21 @@ struct FewCtl {
   uint32_t mask[2][kMaxEntries];         // tokens of an expert: 0 .. 31, 32 .. 63
   uint16_t idx[kMaxPairs];       // expert of a pair (kNoExpert: out of range)
   int16_t pos_of[kMaxPairs];     // sorted position of pair p, -1: dropped
-  float xs[kFewMaxT];            // scales of the fp16 tokens (MXFP4 weights)
   uint8_t tok_of[kMaxPairs + kFewMaxT];  // token of a sorted position
 };
 
 struct FewParams {
   // weights as (columns, rows of one half, halves of the experts); tokens, the
   // hidden values and their scales as (columns, rows)
-  CUtensorMap w1, w2, w1s, w2s, x, act, act_s;
+  CUtensorMap w1, w2, w1s, w2s, x, act;
   FewArgs a;
   const int32_t* idx;  // kFewCopies copies of the selection, pairs_pad apart
   const float* prob;
   int pairs_pad;
   int32_t* sync;
-  const float* xs;
-  void* hidden;      // bf16, or fp16 with hidden_s (MXFP4 weights)
-  float* hidden_s;
+  void* hidden;         // bf16, or E2M1 parts (MXFP4 weights) with
+  uint8_t* hidden_s;    // their block scales
+  const uint32_t* xs;   // block scales of the tokens' parts
   float* ypart;
   int S;            // rows of act and ypart: T K (+ T)
   int ksplit, stages;
@@ -304,40 +319,35 @@ struct FewParams {
 
 // RT = 16 MT weight rows of a unit, NB = 8 NT tokens, NW consumer warps of MPW
 // m-tiles each: MT / MPW of them share a slice of a stage's KC columns.
-template <bool W4_, int MT_, int MPW_, int NT_, int NW_, int KC_>
+template <int MT_, int MPW_, int NT_, int NW_, int KC_>
 struct FewTile {
-  static constexpr bool W4 = W4_;
   static constexpr int MT = MT_, MPW = MPW_, NT = NT_, NW = NW_, KC = KC_;
   static constexpr int RT = 16 * MT;  // weight rows of a unit
   static constexpr int NB = 8 * NT;   // tokens of a unit
   static constexpr int MG = MT / MPW, KG = NW / MG, KW = KC / KG;  // slices and their columns
   // A stage holds KC / 256 boxes of 256 columns, rows one after the other.
-  // bf16 rows are 512 bytes, unswizzled: two of a quarter-warp's eight 16-byte
+  // Rows are 512 bytes, unswizzled: two of a quarter-warp's eight 16-byte
   // loads meet in a bank, which the shared-memory bandwidth has room for.
-  // MXFP4 rows are 128 bytes with the 128-byte swizzle, without conflicts.
   static constexpr int KB = 256, NKB = KC / KB;
-  static constexpr int A_ROW = W4 ? 128 : 512, B_ROW = 512;
+  static constexpr int A_ROW = 512, B_ROW = 512;
   static constexpr int A_BYTES = NKB * RT * A_ROW, B_BYTES = NKB * NB * B_ROW;
-  static constexpr int SF = W4 ? 2 * (KC / 128) * mx::ATOM : 0;
-  static constexpr int BS_ROW = W4 ? KC / 32 * 4 : 0;
-  static constexpr int STAGE = (A_BYTES + B_BYTES + SF + NB * BS_ROW + 1023) / 1024 * 1024;
+  static constexpr int STAGE = (A_BYTES + B_BYTES + 1023) / 1024 * 1024;
   static constexpr int RED_TOK = RT + 4;  // padded token stride of the meeting buffer
   static constexpr int REDS = NT > 2 ? 1 : 2;  // meeting buffers (one of them fits beside more tokens)
   static constexpr int RED1 = KG * NB * RED_TOK * 4, RED = REDS * RED1;
   static constexpr int THREADS = 32 * (NW + 2);
-  static_assert(MT % MPW == 0 && NW % MG == 0 && NW >= 8 && KB % KW == 0 &&
-                    KW % (W4 ? 128 : 32) == 0,
-                "whole blocks per warp");
+  // warps that write the results of a unit of n tokens by `width` values
+  static MOE_HD int writers(int n, int width) {
+    const int w = (n * width + 31) / 32;
+    return w < NW ? w : NW;
+  }
+  static_assert(MT % MPW == 0 && NW % MG == 0 && NW >= 8 && KB % KW == 0 && KW % 32 == 0, "whole blocks per warp");
 };
 
-// Warps that write the results of a unit of n tokens by `width` values, and of
-// an expert's n tokens in units of nb.
-MOE_HD int few_writers(int n, int width, int warps) {
-  const int w = (n * width + 31) / 32;
-  return w < warps ? w : warps;
-}
-MOE_HD int few_writers_of(int n, int nb, int width, int warps) {
-  return n / nb * few_writers(nb, width, warps) + few_writers(n % nb, width, warps);
+// Warps that write the results of an expert's n tokens, in units of L::NB, by
+// `width` values.
+template <class L> MOE_HD int few_writers_of(int n, int width) {
+  return n / L::NB * L::writers(L::NB, width) + L::writers(n % L::NB, width);
 }
 
 // Sorts the pairs by expert (tokens ascending) and lays out the units; every
@@ -365,7 +375,7 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
   // busy experts in order (the shared expert is one more): a warp takes 32 experts,
   // counts, and continues after the warps before it
   const int last = cf.E + (cf.n_shared ? 1 : 0), chunks = (last + 31) / 32;
-  static_assert(L::NW + 2 >= kMaxChunks, "a warp for every 32 experts");
+  static_assert(L::THREADS / 32 >= kMaxChunks, "a warp for every 32 experts");
   {
     const int e = warp * 32 + lane;
     int n = warp < chunks && e < last ? __popc(c.mask[0][e]) + __popc(c.mask[1][e]) : 0;
@@ -382,7 +392,7 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
         if (lane >= o) { ip += a; is += b; }
       }
     }
-    const int writers = __reduce_add_sync(0xffffffffu, few_writers_of(n, L::NB, L::RT, L::NW));
+    const int writers = __reduce_add_sync(0xffffffffu, few_writers_of<L>(n, L::RT));
     if (lane == 31 && warp < chunks) c.part[warp] = make_int4(__popc(busy), ip, is, writers);
     __syncthreads();
     int4 before = make_int4(0, 0, 0, 0);
@@ -398,7 +408,7 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
       c.cum1[j] = u * nrb1;
       c.cum2[j] = u * nrb2 * ksplit;
     }
-    if (warp == L::NW + 1 && lane == 0) {  // past every chunk but perhaps its own
+    if (warp == L::THREADS / 32 - 1 && lane == 0) {  // past every chunk but perhaps its own
       if (warp < chunks) {
         const int4 v = c.part[warp];
         before.x += v.x; before.y += v.y; before.z += v.z; before.w += v.w;
@@ -458,40 +468,12 @@ MOE_D bool wait_count(const int32_t* p, int v, const tc::WaitCtl& w) {
   }
 }
 
-template <bool F16>
 MOE_D void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                     uint32_t b1) {
-  if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The fp16 product alone (a zero addend).
-MOE_D void mma16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                         uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-               "{%8,%9}, {%10,%10,%10,%10};"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// Eight E2M1 codes -> eight fp16 values (exact), in order.
-MOE_D void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // A box of a 3-D tensor map (as tc::tma_load_2d), first to leave the L2: weights
@@ -513,13 +495,83 @@ MOE_D void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t
 
 // Loads from the ring: ordinary loads, which the compiler may move among the
 // products but not across a barrier's wait.
-MOE_D uint32_t lds32(const uint8_t* a) { return *reinterpret_cast<const uint32_t*>(a); }
 MOE_D uint4 lds128(const uint8_t* a) { return *reinterpret_cast<const uint4*>(a); }
 
 // Rows of FC1's output of a unit: hidden units (a SwiGLU unit holds the gate
 // and up rows of RT / 2 of them, in groups of eight: each m-tile has eight
 // gate rows above the matching eight up rows).
 template <class L> MOE_HD int few_rows1(bool glu) { return glu ? L::RT / 2 : L::RT; }
+
+// The combine: a warp takes 64 columns of a token, eight slots at once: lanes
+// 4 s + c hold columns 16 i + 4 c .. + 3 of slot s, and a tree adds the slots (a
+// fixed order).  `at`: the block's copy of the selection.
+constexpr int kCols = 64;
+MOE_D int64_t few_combine_items(const moe_config_t& cf) {
+  return (int64_t)cf.T * ((cf.h + kCols - 1) / kCols);
+}
+__device__ __forceinline__ void few_combine(const FewParams& p, const FewCtl& ctl, int64_t at, int warp,
+                                            int warps, int lane) {
+  const moe_config_t& cf = p.a.c;
+  const int g = lane >> 2, q = lane & 3;
+  const int col_blocks = (cf.h + kCols - 1) / kCols;
+  const int64_t items = few_combine_items(cf);
+  const int slots = cf.K + (cf.n_shared ? 1 : 0);
+  for (int64_t i = (int64_t)warp * gridDim.x + blockIdx.x; i < items; i += (int64_t)gridDim.x * warps) {
+    const int t = (int)(i / col_blocks), r = (int)(i - (int64_t)t * col_blocks) * kCols + 4 * q;
+    float4 y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k = g; k < slots; k += 8) {
+      const bool shared = k == cf.K;
+      const int pr = t * cf.K + k;
+      const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
+      if (pos < 0) continue;  // dropped
+      const float w = shared ? 1.f : __ldcg(p.prob + at + pr);
+      const float* src = p.ypart + (int64_t)pos * cf.h + r;
+      float4 o[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (cf.has_bias && !shared) {
+        const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (r + 16 * c < cf.h)
+            o[c] = make_float4(to_f32(b[16 * c]), to_f32(b[16 * c + 1]), to_f32(b[16 * c + 2]), to_f32(b[16 * c + 3]));
+      }
+#pragma unroll 2
+      for (int s = 0; s < p.ksplit; ++s) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (r + 16 * c < cf.h) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)s * p.S * cf.h + 16 * c));
+            o[c].x += v.x; o[c].y += v.y; o[c].z += v.z; o[c].w += v.w;
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        y[c].x = fmaf(w, o[c].x, y[c].x); y[c].y = fmaf(w, o[c].y, y[c].y);
+        y[c].z = fmaf(w, o[c].z, y[c].z); y[c].w = fmaf(w, o[c].w, y[c].w);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) {
+        y[c].x += __shfl_xor_sync(0xffffffffu, y[c].x, o);
+        y[c].y += __shfl_xor_sync(0xffffffffu, y[c].y, o);
+        y[c].z += __shfl_xor_sync(0xffffffffu, y[c].z, o);
+        y[c].w += __shfl_xor_sync(0xffffffffu, y[c].w, o);
+      }
+      if (g == c && r + 16 * c < cf.h) {
+        __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r + 16 * c);
+        dst[0] = __floats2bfloat162_rn(y[c].x, y[c].y);
+        dst[1] = __floats2bfloat162_rn(y[c].z, y[c].w);
+      }
+    }
+  }
+}
 
 template <class L>
 __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constant__ FewParams p) {
@@ -559,9 +611,6 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const int e = __ldcg(p.idx + at + i);
       ctl.idx[i] = e >= 0 && e < cf.E ? (uint16_t)e : kNoExpert;
     }
-    if (L::W4 && threadIdx.x < cf.T) {
-      ctl.xs[threadIdx.x] = __ldcg(p.xs + threadIdx.x);
-    }
   }
   __syncthreads();
   const int nrb1 = ((glu ? 2 * cf.F : cf.F) + L::RT - 1) / L::RT;
@@ -588,9 +637,8 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
         const int u = __shfl_sync(0xffffffffu, next, 0);
         if (u < total && lane == 0) next = atomicAdd(claim, 1);  // the next unit, while this one streams
         FewStage st{};
-        int kbeg = 0, kend = 1, cols = 0, nrows = 0;
+        int kbeg = 0, kend = 1;
         const CUtensorMap* map = nullptr;
-        const uint8_t *sf0 = nullptr, *sf1 = nullptr;  // scales of the rows, of the up rows
         int half0 = 0;  // the map's third coordinate
         bool pairs_of_rows = false;
         if (u < total) {
@@ -602,8 +650,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
             st.kind = kFC1;
             st.r0 = loc / sub * few_rows1<L>(glu);
             st.pos0 = loc % sub * L::NB;
-            nrows = glu ? 2 * cf.F : cf.F;
-            kend = cols = cf.h;
+            kend = cf.h;
             pairs_of_rows = glu;
           } else {
             const int u2 = u - ctl.units1;
@@ -615,8 +662,6 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
             st.ks = rest % p.ksplit;
             st.r0 = rest / p.ksplit * L::RT;
             st.pos0 = loc % sub * L::NB;
-            nrows = cf.h;
-            cols = cf.F;
             const int nst = (cf.F + L::KC - 1) / L::KC;
             kbeg = nst * st.ks / p.ksplit * L::KC;
             kend = min(cf.F, nst * (st.ks + 1) / p.ksplit * L::KC);
@@ -628,12 +673,6 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           const bool shared = e == cf.E;
           map = st.kind == kFC1 ? (shared ? &p.w1s : &p.w1) : (shared ? &p.w2s : &p.w2);
           half0 = shared ? 0 : e * (pairs_of_rows ? 2 : 1);
-          if (L::W4) {
-            const FewWeights& W = st.kind == kFC1 ? p.a.w1 : p.a.w2;
-            const uint8_t* sf = shared ? W.ws_sf : W.sf + (int64_t)e * (nrows / 128) * (cols / 128) * mx::ATOM;
-            sf0 = sf + (int64_t)(st.r0 / 128) * (cols / 128) * mx::ATOM;
-            sf1 = sf + (int64_t)((st.r0 + cf.F) / 128) * (cols / 128) * mx::ATOM;
-          }
         }
         for (int k0 = kbeg; k0 < kend; k0 += L::KC) {
           if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
@@ -642,8 +681,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           st.k0 = k0;
           st.last = k0 + L::KC >= kend;
           const int nkb = (st.kc + L::KB - 1) / L::KB;
-          const uint32_t sf_bytes = L::W4 ? st.kc / 128 * mx::ATOM : 0;
-          const uint32_t tx = nkb * L::RT * L::A_ROW + sf_bytes * (pairs_of_rows ? 2 : 1);
+          const uint32_t tx = nkb * L::RT * L::A_ROW;
           const uint32_t a_dst = ring0 + stage * L::STAGE;
           if (elected) {
             ctl.st[stage] = st;
@@ -653,14 +691,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 #pragma unroll
               for (int b = 0; b < L::NKB; ++b)
                 if (b < nkb)
-                  tma_load_3d(a_dst + b * L::RT * L::A_ROW, map, (k0 + b * L::KB) / (L::W4 ? 2 : 1),
-                              st.r0, half0, fb, policy);
-              if (L::W4) {  // the scales of the unit's rows: atoms of their 128-row tile
-                const uint32_t sf_dst = a_dst + L::A_BYTES + L::B_BYTES;
-                tc::bulk_load(sf_dst, sf0 + (int64_t)(k0 / 128) * mx::ATOM, sf_bytes, fb);
-                if (pairs_of_rows)
-                  tc::bulk_load(sf_dst + L::SF / 2, sf1 + (int64_t)(k0 / 128) * mx::ATOM, sf_bytes, fb);
-              }
+                  tma_load_3d(a_dst + b * L::RT * L::A_ROW, map, k0 + b * L::KB, st.r0, half0, fb, policy);
             }
           }
           __syncwarp();
@@ -692,7 +723,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const FewStage st = ctl.st[stage];
       if (st.kind == kEnd) break;
       if (st.kind == kFC2 && ready != st.entry) {  // the expert's hidden values
-        const int writers = few_writers_of(ctl.ent_n[st.entry], L::NB, width1, L::NW);
+        const int writers = few_writers_of<L>(ctl.ent_n[st.entry], width1);
         int up = 0;
         if (lane == 0) up = wait_count(done + st.entry, nrb1 * writers, wc);
         if (!__shfl_sync(0xffffffffu, up, 0)) break;
@@ -723,15 +754,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
         }
       } else if (elected) {  // rows of the sorted list: boxes of eight
         const int n8 = (st.n + 7) / 8;
-        tc::mbar_arrive_expect_tx(fb, n8 * (nkb * 8 * L::B_ROW + 8 * L::BS_ROW));
-        for (int i = 0; i < n8; ++i) {
+        tc::mbar_arrive_expect_tx(fb, n8 * nkb * 8 * L::B_ROW);
+        for (int i = 0; i < n8; ++i)
           for (int b = 0; b < nkb; ++b)
             tc::tma_load_2d(b_dst + (b * L::NB + 8 * i) * L::B_ROW, &p.act, st.k0 + b * L::KB,
                             st.pos0 + 8 * i, fb);
-          if (L::W4)
-            tc::tma_load_2d(b_dst + L::B_BYTES + L::SF + 8 * i * L::BS_ROW, &p.act_s, st.k0 / 32,
-                            st.pos0 + 8 * i, fb);
-        }
       }
       __syncwarp();
       issued |= 1u << stage;
@@ -771,8 +798,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     bool finish = false;
     // The stages of one unit, the first of which is there (its weights).  TWO: a
     // SwiGLU FC1 unit, whose m-tiles' upper halves (up rows) lie in a block of
-    // their own.  What does not change from stage to stage is worked out once:
-    // with 4-bit weights the instructions are what bounds these loops.
+    // their own.  What does not change from stage to stage is worked out once.
     auto stages = [&](auto two_c, const FewStage& st) -> bool {
       constexpr bool TWO = decltype(two_c)::value;
       constexpr int M_STEP = TWO ? 8 : 16, HI = (TWO ? 8 * L::MT : 8) * L::A_ROW;
@@ -781,104 +807,34 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       // offsets within a stage: the lane's weight rows and token rows (past the
       // last token, the last)
       const uint32_t a_off = (k_w / L::KB * L::RT + m_row) * L::A_ROW +
-                             (L::W4 ? 4 * q : (k_w % L::KB + 8 * q) * 2);
-      uint32_t b_off[L::NT], sf_off[L::MPW][2], ts_off[L::NT][2];
+                             (k_w % L::KB + 8 * q) * 2;
+      uint32_t b_off[L::NT];
 #pragma unroll
-      for (int n = 0; n < L::NT; ++n) {
+      for (int n = 0; n < L::NT; ++n)
         b_off[n] = L::A_BYTES + (k_w / L::KB * L::NB + min(8 * n + g, st.n - 1)) * L::B_ROW +
                    (k_w % L::KB + 8 * q) * 2;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          ts_off[n][i] = L::A_BYTES + L::B_BYTES + L::SF +
-                         min(8 * n + 2 * q + i, st.n - 1) * L::BS_ROW + k_w / 32 * 4;
-      }
-#pragma unroll
-      for (int m = 0; m < L::MPW; ++m) {
-        const int i0 = (st.r0 + m_row + m * M_STEP) & 127, i1 = TWO ? i0 : i0 + 8;
-        const uint32_t at = L::A_BYTES + L::B_BYTES + k_w / 128 * mx::ATOM;
-        sf_off[m][0] = at + 16 * (i0 & 31) + 4 * (i0 >> 5);
-        sf_off[m][1] = at + (TWO ? L::SF / 2 : 0) + 16 * (i1 & 31) + 4 * (i1 >> 5);
-      }
-      // 16 bytes hold a 32-column block's codes of a row; the swizzle moves them by
-      // the row's place in its group of eight, which is g
-      [[maybe_unused]] const uint32_t sw16 = ((k_w % L::KB) / 32 ^ g) * 16;
       int kc = st.kc, last = st.last;
       for (;;) {
         if (!tc::mbar_wait(tc::smem_u32(&ctl.full_t[stage]), phase, wc)) return false;
         const uint8_t* base = ring + stage * L::STAGE;
         const uint8_t* a_at = base + a_off;
-        if constexpr (!L::W4) {
 #pragma unroll
-          for (int c = 0; c < L::KW / 32; ++c) {
-            if (k_w + c * 32 >= kc) break;  // (the boxes are zero past the matrix)
-            uint4 b[L::NT];
+        for (int c = 0; c < L::KW / 32; ++c) {
+          if (k_w + c * 32 >= kc) break;  // (the boxes are zero past the matrix)
+          uint4 b[L::NT];
+#pragma unroll
+          for (int n = 0; n < L::NT; ++n)
+            if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + c * 64);
+#pragma unroll
+          for (int m = 0; m < L::MPW; ++m) {
+            const uint4 lo = lds128(a_at + m * M_STEP * L::A_ROW + c * 64);
+            const uint4 hi = lds128(a_at + m * M_STEP * L::A_ROW + HI + c * 64);
 #pragma unroll
             for (int n = 0; n < L::NT; ++n)
-              if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + c * 64);
-#pragma unroll
-            for (int m = 0; m < L::MPW; ++m) {
-              const uint4 lo = lds128(a_at + m * M_STEP * L::A_ROW + c * 64);
-              const uint4 hi = lds128(a_at + m * M_STEP * L::A_ROW + HI + c * 64);
-#pragma unroll
-              for (int n = 0; n < L::NT; ++n)
-                if (L::NT == 1 || n < ntiles) {
-                  mma16816<false>(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n].x, b[n].y);
-                  mma16816<false>(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n].z, b[n].w);
-                }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int c4 = 0; c4 < L::KW / 128; ++c4) {  // 128 columns: one word of scales a row
-            if (k_w + c4 * 128 >= kc) break;
-            uint32_t sw[L::MPW][2];
-#pragma unroll
-            for (int m = 0; m < L::MPW; ++m) {
-              sw[m][0] = lds32(base + sf_off[m][0] + c4 * mx::ATOM);
-              sw[m][1] = lds32(base + sf_off[m][1] + c4 * mx::ATOM);
-            }
-            uint4 ts[L::NT][2];  // the tokens' own scales of these columns (FC2)
-            if constexpr (!TWO) {
-#pragma unroll
-              for (int n = 0; n < L::NT; ++n)
-                if (L::NT == 1 || n < ntiles) {
-                  ts[n][0] = lds128(base + ts_off[n][0] + c4 * 16);
-                  ts[n][1] = lds128(base + ts_off[n][1] + c4 * 16);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint4 b[L::NT];
-#pragma unroll
-              for (int n = 0; n < L::NT; ++n)
-                if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + (4 * c4 + c) * 64);
-              const uint8_t* at = a_at + (sw16 ^ (64 * c4 + 16 * c));
-#pragma unroll
-              for (int m = 0; m < L::MPW; ++m) {
-                uint32_t lo[4], hi[4];
-                e2m1x8_to_f16(lds32(at + m * M_STEP * L::A_ROW), lo);
-                e2m1x8_to_f16(lds32(at + m * M_STEP * L::A_ROW + HI), hi);
-                const float s0 = __uint_as_float((c < 3 ? sw[m][0] << (23 - 8 * c) : sw[m][0] >> 1) & 0x7f800000u);
-                const float s1 = __uint_as_float((c < 3 ? sw[m][1] << (23 - 8 * c) : sw[m][1] >> 1) & 0x7f800000u);
-#pragma unroll
-                for (int n = 0; n < L::NT; ++n)
-                  if (L::NT == 1 || n < ntiles) {
-                    // the fp16 products of one block, then its scales in fp32
-                    float d[4];
-                    mma16816_zero(d, lo[0], hi[0], lo[1], hi[1], b[n].x, b[n].y);
-                    mma16816<true>(d, lo[2], hi[2], lo[3], hi[3], b[n].z, b[n].w);
-                    if constexpr (!TWO) {
-                      const float t0 = __uint_as_float(c == 0 ? ts[n][0].x : c == 1 ? ts[n][0].y : c == 2 ? ts[n][0].z : ts[n][0].w);
-                      const float t1 = __uint_as_float(c == 0 ? ts[n][1].x : c == 1 ? ts[n][1].y : c == 2 ? ts[n][1].z : ts[n][1].w);
-                      d[0] *= t0; d[1] *= t1; d[2] *= t0; d[3] *= t1;
-                    }
-                    acc[m][n][0] = fmaf(d[0], s0, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(d[1], s0, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(d[2], s1, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(d[3], s1, acc[m][n][3]);
-                  }
+              if (L::NT == 1 || n < ntiles) {
+                mma16816(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n].x, b[n].y);
+                mma16816(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n].z, b[n].w);
               }
-            }
           }
         }
         __syncwarp();
@@ -933,7 +889,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const int rw = (warp + L::NW - unit % L::NW) % L::NW;  // place among the writers
       ++unit;
       const int width = st.kind == kFC1 ? width1 : L::RT;
-      const int writers = few_writers(st.n, width, L::NW);
+      const int writers = L::writers(st.n, width);
       if (rw >= writers) continue;
       const int items = st.n * width;
       if (st.kind == kFC1) {
@@ -944,32 +900,17 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           const bool valid = i < items && st.r0 + f < cf.F;
           const int pos = st.pos0 + tok;
           float v;
-          const float s = L::W4 ? ctl.xs[ctl.tok_of[pos]] : 1.f;
           if (glu) {
             const int row = f / 8 * 16 + (f & 7);
-            v = silu_f(sum(tok, row) * s) * (sum(tok, row + 8) * s);
+            v = silu_f(sum(tok, row)) * sum(tok, row + 8);
           } else {
             float z = sum(tok, f);
             if (cf.has_bias && e < cf.E && valid) z += to_f32(p.a.b1[(int64_t)e * cf.F + st.r0 + f]);
             v = gelu_f(z);
           }
           const int64_t at = (int64_t)pos * cf.F + st.r0 + f;
-          if constexpr (L::W4) {
-            // a warp has 32 hidden units of one token: fp16 with a power-of-two
-            // scale of their own (11 significant bits, half a step 2^-11 of
-            // values down to 2^-29 of the largest)
-            uint32_t m = __float_as_uint(v) & 0x7fffffffu;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float bsc = f16_block_scale(m);
-            if (valid) {
-              static_cast<__half*>(p.hidden)[at] = __float2half_rn(v * (1.f / bsc));
-              if (lane == 0) p.hidden_s[(int64_t)pos * (cf.F / 32) + (st.r0 + f) / 32] = bsc;
-            }
-          } else {
-            // bf16, as moe_layer_fwd keeps them: FC2's operand type
-            if (valid) static_cast<__nv_bfloat16*>(p.hidden)[at] = __float2bfloat16_rn(v);
-          }
+          // bf16, as moe_layer_fwd keeps them: FC2's operand type
+          if (valid) static_cast<__nv_bfloat16*>(p.hidden)[at] = __float2bfloat16_rn(v);
         }
         fence_proxy_async_global();
         __syncwarp();
@@ -985,77 +926,460 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       }
     }
     // ---- combine: every block's share ----
-    // A warp takes 64 columns of a token, eight slots at once: lanes 4 s + c hold
-    // columns 16 i + 4 c .. + 3 of slot s, and a tree adds the slots (a fixed order).
-    constexpr int kCols = 64;
-    const int col_blocks = (cf.h + kCols - 1) / kCols;
-    const int64_t items = (int64_t)cf.T * col_blocks;
-    const int slots = cf.K + (cf.n_shared ? 1 : 0);
-    finish = finish && (int64_t)blockIdx.x < items;
+    finish = finish && blockIdx.x < few_combine_items(cf);
     if (finish && warp == 0) {  // one warp of a block that has a share watches the count
       int all = 0;
       if (lane == 0) all = wait_count(done2, ctl.fc2_writers, wc);
       __shfl_sync(0xffffffffu, all, 0);
     }
     if (finish && meet() && ld_acquire(done2) >= ctl.fc2_writers) {
-      for (int64_t i = (int64_t)warp * gridDim.x + blockIdx.x; i < items; i += (int64_t)gridDim.x * L::NW) {
-        const int t = (int)(i / col_blocks), r = (int)(i - (int64_t)t * col_blocks) * kCols + 4 * q;
-        float4 y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int k = g; k < slots; k += 8) {
-          const bool shared = k == cf.K;
-          const int pr = t * cf.K + k;
-          const int pos = shared ? ctl.pairs - cf.T + t : ctl.pos_of[pr];
-          if (pos < 0) continue;  // dropped
-          const float w = shared ? 1.f : __ldcg(p.prob + at + pr);
-          const float* src = p.ypart + (int64_t)pos * cf.h + r;
-          float4 o[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (cf.has_bias && !shared) {
-            const __nv_bfloat16* b = p.a.b2 + (int64_t)ctl.idx[pr] * cf.h + r;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (r + 16 * c < cf.h)
-                o[c] = make_float4(to_f32(b[16 * c]), to_f32(b[16 * c + 1]), to_f32(b[16 * c + 2]), to_f32(b[16 * c + 3]));
-          }
-#pragma unroll 2
-          for (int s = 0; s < p.ksplit; ++s) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (r + 16 * c < cf.h) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)s * p.S * cf.h + 16 * c));
-                o[c].x += v.x; o[c].y += v.y; o[c].z += v.z; o[c].w += v.w;
-              }
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            y[c].x = fmaf(w, o[c].x, y[c].x); y[c].y = fmaf(w, o[c].y, y[c].y);
-            y[c].z = fmaf(w, o[c].z, y[c].z); y[c].w = fmaf(w, o[c].w, y[c].w);
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-#pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) {
-            y[c].x += __shfl_xor_sync(0xffffffffu, y[c].x, o);
-            y[c].y += __shfl_xor_sync(0xffffffffu, y[c].y, o);
-            y[c].z += __shfl_xor_sync(0xffffffffu, y[c].z, o);
-            y[c].w += __shfl_xor_sync(0xffffffffu, y[c].w, o);
-          }
-          if (g == c && r + 16 * c < cf.h) {
-            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.a.y + (int64_t)t * cf.h + r + 16 * c);
-            dst[0] = __floats2bfloat162_rn(y[c].x, y[c].y);
-            dst[1] = __floats2bfloat162_rn(y[c].z, y[c].w);
-          }
-        }
-      }
+      few_combine(p, ctl, at, warp, L::NW, lane);
     }
   }
   __syncthreads();
+}
+
+// ---- MXFP4 weights -----------------------------------------------------------------
+// The same units, list, counter and order as few_kernel, the products on the
+// 5th-generation tensor cores: tcgen05.mma kind::mxf4, 128 weight rows as M
+// (FC1: 64 gate rows and the matching 64 up rows), the tokens' E2M1 parts as N
+// (four rows a token), the block scales of both operands applied by the MMA, fp32
+// accumulators in TMEM (two, for two units in turn).  Decoding the codes on the
+// ALUs for m16n8k16 products (tokens in fp16) took 34 warp instructions for 16 x
+// 32 weights: T = 13, 2 of 8 experts / T = 64, 8 of 64 / T = 5, 8 of 256 ran in
+// 156 / 92 / 165 us; this takes 129 / 70 / 133.
+//   warp 0  weights: 128-row boxes of 256 codes and the rows' scale atoms;
+//   warp 1  TMEM owner and MMA issuer (one elected lane);
+//   warp 2  tokens: their parts (FC1: token by token; FC2: one box);
+//   warp 3  scales: an FC1 unit's atoms put together from the halves of two
+//           tiles, the tokens' scale words gathered into atoms;
+//   warps 4-7  epilogue, a TMEM lane quarter each: adds the parts, FC1: SwiGLU
+//           (gate and up meet in shared memory) and the hidden values' parts;
+//           FC2: partial results.
+// Warps 8 and 9 only help with the list and the combine.
+template <int NT_>
+struct FewMxTile {
+  static constexpr int NT = NT_, NB = 8 * NT, N = NB * kParts, RT = 128, KC = 512, KB = 256;
+  static constexpr int A_BOX = RT * 128, B_BOX = N * 128;  // bytes of 256 columns
+  static constexpr int A_BYTES = 2 * A_BOX, B_BYTES = 2 * B_BOX;
+  static constexpr int SF = KC / 128 * mx::ATOM;           // atoms of 128 rows
+  static constexpr int B_OFF = A_BYTES, RAW = B_OFF + B_BYTES, SFA = RAW + 2 * SF, SFB = SFA + SF;
+  static constexpr int STAGE = SFB + SF;
+  static constexpr int EX = NB * 64, EX_BYTES = 2 * 2 * EX * 4;  // gate and up, two units in turn
+  static constexpr int THREADS = 320;
+  static constexpr uint32_t ACC = 64, SF_COL0 = 128, SF_COLS = 32, TMEM = 256;  // TMEM columns
+  static constexpr int MAX_STAGES = (TMEM - SF_COL0) / SF_COLS;
+  static MOE_HD int writers(int n, int) { return n > 0 ? 4 : 0; }
+  static_assert(N <= (int)ACC && STAGE % 1024 == 0, "TMEM columns, swizzle alignment");
+};
+
+struct FewMxCtl {
+  FewCtl c;
+  uint64_t full_s[kMaxStages];                      // the stage's scales are there
+  uint64_t unit_told[2], tmem_full[2], tmem_empty[2], drain;
+  alignas(16) FewStage unit[2];
+  uint32_t tmem_base;
+};
+
+// A box of a 3-D tensor map without a cache hint.
+MOE_D void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                       uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// 32 lanes x NG groups of 16 columns, one wait.
+template <int NG>
+MOE_D void tmem_ld_x16(uint32_t taddr, float (&v)[16 * NG]) {
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    float* d = v + 16 * i;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]), "=f"(d[4]), "=f"(d[5]), "=f"(d[6]),
+          "=f"(d[7]), "=f"(d[8]), "=f"(d[9]), "=f"(d[10]), "=f"(d[11]), "=f"(d[12]), "=f"(d[13]),
+          "=f"(d[14]), "=f"(d[15])
+        : "r"(taddr + 16 * i)
+        : "memory");
+  }
+}
+
+template <class L>
+__global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_constant__ FewParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const moe_config_t& cf = p.a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* ex = reinterpret_cast<float*>(ring + (size_t)p.stages * L::STAGE);
+  FewMxCtl& mc = *reinterpret_cast<FewMxCtl*>(reinterpret_cast<uint8_t*>(ex) + L::EX_BYTES);
+  FewCtl& ctl = mc.c;
+  const uint32_t ring0 = tc::smem_u32(ring);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s)
+      for (uint64_t* b : {&ctl.full_w[s], &ctl.full_t[s], &ctl.told[s], &ctl.empty[s], &mc.full_s[s]})
+        tc::mbar_init(tc::smem_u32(b), 1);
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(tc::smem_u32(&mc.unit_told[b]), 1);
+      tc::mbar_init(tc::smem_u32(&mc.tmem_full[b]), 1);
+      tc::mbar_init(tc::smem_u32(&mc.tmem_empty[b]), 4);
+    }
+    tc::mbar_init(tc::smem_u32(&mc.drain), 1);
+    tc::mbar_init(tc::smem_u32(&ctl.meet), 4);
+    ctl.abort = 0;
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+    for (const CUtensorMap* m : {&p.w1, &p.w2, &p.x, &p.act}) tc::prefetch_tensormap(m);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(&mc.tmem_base), L::TMEM);
+    tc::tmem_relinquish();
+  }
+  for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[0][e] = ctl.mask[1][e] = 0u;
+  pdl_wait();  // the selection, and with it the cleared counters and the tokens' parts
+  int32_t* claim = p.sync;
+  const int first_claim = threadIdx.x == 0 ? atomicAdd(claim, 1) : 0;
+  const int64_t at = (int64_t)(blockIdx.x % kFewCopies) * p.pairs_pad;  // this block's copy
+  for (int i = threadIdx.x; i < cf.T * cf.K; i += L::THREADS) {
+    const int e = __ldcg(p.idx + at + i);
+    ctl.idx[i] = e >= 0 && e < cf.E ? (uint16_t)e : kNoExpert;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const int nrb1 = 2 * cf.F / L::RT;
+  few_build_list<L>(ctl, cf, nrb1, cf.h / L::RT, p.ksplit, p.a.status);
+
+  int32_t* done = p.sync + 2;   // warps that wrote FC1 results, per busy expert
+  int32_t* done2 = p.sync + 1;  // warps that wrote FC2 results
+  const int total = ctl.units1 + ctl.units2;
+  const uint32_t tmem = mc.tmem_base;
+  tc::WaitCtl wc{p.a.status, &ctl.abort, p.wait_limit_ns, 0};
+  tc::WaitCtl wdrain{p.a.status, nullptr, 1000000000ull, 0};
+  const bool elected = tc::elect_one();
+  int stage = 0;
+  uint32_t phase = 0, issued = 0, issued_par = 0;
+  // (each role's own copies of these)
+  auto next_stage = [&] { if (++stage == p.stages) { stage = 0; phase ^= 1; } };
+  auto note_issued = [&] {
+    issued |= 1u << stage;
+    issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+  };
+  // Waits until an FC2 unit's expert has all its hidden values.
+  auto hidden_ready = [&](int entry) -> bool {
+    int up = 0;
+    if (lane == 0) up = wait_count(done + entry, nrb1 * few_writers_of<L>(ctl.ent_n[entry], 0), wc);
+    if (!__shfl_sync(0xffffffffu, up, 0)) return false;
+    ld_acquire(done + entry);  // every lane's own
+    return true;
+  };
+
+  if (warp == 0) {
+    // ================= weights =================
+    int j1 = 0, j2 = 0, next = first_claim;
+    const uint64_t policy = evict_first_policy();
+    bool ok = true;
+    while (ok) {
+      const int u = __shfl_sync(0xffffffffu, next, 0);
+      if (u < total && lane == 0) next = atomicAdd(claim, 1);  // the next unit, while this one streams
+      FewStage st{};
+      int kbeg = 0, kend = 1, half0 = 0;
+      const CUtensorMap* map = nullptr;
+      const uint8_t *sf0 = nullptr, *sf1 = nullptr;  // scales of the rows, of the up rows
+      if (u < total) {
+        int j, cols;
+        if (u < ctl.units1) {
+          while (ctl.cum1[j1 + 1] <= u) ++j1;
+          j = j1;
+          const int sub = (ctl.ent_n[j] + L::NB - 1) / L::NB, loc = u - ctl.cum1[j];
+          st.kind = kFC1;
+          st.r0 = loc / sub * (L::RT / 2);
+          st.pos0 = loc % sub * L::NB;
+          kend = cols = cf.h;
+        } else {
+          const int u2 = u - ctl.units1;
+          while (ctl.cum2[j2 + 1] <= u2) ++j2;
+          j = j2;
+          const int sub = (ctl.ent_n[j] + L::NB - 1) / L::NB, loc = u2 - ctl.cum2[j];
+          const int rest = loc / sub;
+          st.kind = kFC2;
+          st.ks = rest % p.ksplit;
+          st.r0 = rest / p.ksplit * L::RT;
+          st.pos0 = loc % sub * L::NB;
+          cols = cf.F;
+          const int nst = (cf.F + L::KC - 1) / L::KC;
+          kbeg = nst * st.ks / p.ksplit * L::KC;
+          kend = min(cf.F, nst * (st.ks + 1) / p.ksplit * L::KC);
+        }
+        st.entry = j;
+        st.n = min(L::NB, ctl.ent_n[j] - st.pos0);
+        st.pos0 += ctl.ent_start[j];
+        const int e = ctl.ent_e[j];
+        const bool shared = e == cf.E, fc1 = st.kind == kFC1;
+        map = fc1 ? (shared ? &p.w1s : &p.w1) : (shared ? &p.w2s : &p.w2);
+        half0 = shared ? 0 : e * (fc1 ? 2 : 1);
+        const FewWeights& W = fc1 ? p.a.w1 : p.a.w2;
+        const int64_t row_atoms = cols / 128;
+        const uint8_t* sf = shared ? W.ws_sf
+                                   : W.sf + (int64_t)e * ((fc1 ? 2 * cf.F : cf.h) / 128) * row_atoms * mx::ATOM;
+        sf0 = sf + st.r0 / 128 * row_atoms * mx::ATOM;
+        sf1 = sf + (st.r0 + cf.F) / 128 * row_atoms * mx::ATOM;
+      }
+      for (int k0 = kbeg; k0 < kend; k0 += L::KC) {
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
+        const uint32_t fb = tc::smem_u32(&ctl.full_w[stage]);
+        st.kc = min(L::KC, kend - k0);
+        st.k0 = k0;
+        st.last = k0 + L::KC >= kend;
+        const int nkb = (st.kc + L::KB - 1) / L::KB;
+        const uint32_t sf_bytes = st.kc / 128 * mx::ATOM;
+        const bool fc1 = st.kind == kFC1;
+        const uint32_t dst = ring0 + stage * L::STAGE;
+        if (elected) {
+          ctl.st[stage] = st;
+          tc::mbar_arrive_expect_tx(fb, st.kind == kEnd ? 0 : nkb * L::A_BOX + sf_bytes * (fc1 ? 2 : 1));
+          tc::mbar_arrive(tc::smem_u32(&ctl.told[stage]));
+          if (st.kind != kEnd) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              if (b < nkb) tma_load_3d(dst + b * L::A_BOX, map, (k0 + b * L::KB) / 2, st.r0, half0, fb, policy);
+            const int64_t off = (int64_t)(k0 / 128) * mx::ATOM;
+            tc::bulk_load(dst + (fc1 ? L::RAW : L::SFA), sf0 + off, sf_bytes, fb);
+            if (fc1) tc::bulk_load(dst + L::RAW + L::SF, sf1 + off, sf_bytes, fb);
+          }
+        }
+        __syncwarp();
+        if (st.kind == kEnd) {
+          issued &= ~(1u << stage);  // its copies are consumed, its barrier a phase further
+          ok = false;
+          break;
+        }
+        note_issued();
+        next_stage();
+      }
+    }
+    for (int s = 0; s < p.stages; ++s)
+      if ((issued >> s) & 1u)
+        tc::mbar_wait(tc::smem_u32(&ctl.full_w[s]), (issued_par >> s) & 1u, wdrain);
+  } else if (warp == 1) {
+    // ================= MMA issuer =================
+    const uint64_t a_desc = tc::desc_kmajor_sw128(ring0), b_desc = tc::desc_kmajor_sw128(ring0 + L::B_OFF);
+    const uint64_t sfa_desc = tc::desc_sf_atom(ring0 + L::SFA), sfb_desc = tc::desc_sf_atom(ring0 + L::SFB);
+    int unit = 0;
+    bool first = true, ok = true;
+    while (ok) {
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.full_w[stage]), phase, wc)) break;
+      const FewStage st = ctl.st[stage];
+      const int buf = unit & 1;
+      if (first &&  // the epilogue is done with this buffer's last unit
+          !tc::mbar_wait(tc::smem_u32(&mc.tmem_empty[buf]), ((unit >> 1) & 1) ^ 1, wc)) break;
+      if (st.kind != kEnd) {
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.full_t[stage]), phase, wc)) break;
+        if (!tc::mbar_wait(tc::smem_u32(&mc.full_s[stage]), phase, wc)) break;
+        tc::fence_after_sync();
+        const uint32_t so = stage * (L::STAGE >> 4);  // descriptors count 16 bytes
+        const uint32_t d = tmem + buf * L::ACC;
+        const uint32_t sfa = tmem + L::SF_COL0 + stage * L::SF_COLS, sfb = sfa + 16;
+        const int nk = st.kc / 128;
+        if (elected) {
+#pragma unroll
+          for (int k = 0; k < L::KC / 128; ++k) {
+            if (k >= nk) break;
+            tc::tmem_cp_32x128b_warpx4(sfa + 4 * k, sfa_desc + so + k * (mx::ATOM >> 4));
+            tc::tmem_cp_32x128b_warpx4(sfb + 4 * k, sfb_desc + so + k * (mx::ATOM >> 4));
+            const uint64_t ad = a_desc + so + (k >> 1) * (L::A_BOX >> 4) + (k & 1) * 4;
+            const uint64_t bd = b_desc + so + (k >> 1) * (L::B_BOX >> 4) + (k & 1) * 4;
+            tc::mma_mxf4(d, ad, bd, tc::idesc_mxf4_e2m1(128, L::N, 0, 0), sfa + 4 * k, sfb + 4 * k,
+                         !first || k > 0);
+            tc::mma_mxf4(d, ad + 2, bd + 2, tc::idesc_mxf4_e2m1(128, L::N, 2, 2), sfa + 4 * k, sfb + 4 * k, 1);
+          }
+          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+        }
+        __syncwarp();
+        first = false;
+      }
+      if (st.kind == kEnd || st.last) {
+        if (elected) {
+          mc.unit[buf] = st;
+          tc::mbar_arrive(tc::smem_u32(&mc.unit_told[buf]));
+          if (st.kind != kEnd) tc::mma_commit(tc::smem_u32(&mc.tmem_full[buf]));
+        }
+        __syncwarp();
+        ++unit;
+        first = true;
+      }
+      ok = st.kind != kEnd;
+      if (ok) next_stage();
+    }
+    if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
+      if (elected) tc::mma_commit(tc::smem_u32(&mc.drain));
+      tc::mbar_wait(tc::smem_u32(&mc.drain), 0, wdrain);
+    }
+  } else if (warp == 2) {
+    // ================= tokens =================
+    int ready = -1, mine = 0;
+    for (;;) {
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.told[stage]), phase, wc)) break;
+      const FewStage st = ctl.st[stage];
+      if (st.kind == kEnd) break;
+      if (st.kind == kFC2 && ready != st.entry) {
+        if (!hidden_ready(st.entry)) break;
+        fence_proxy_async_global();
+        ready = st.entry;
+      }
+      const uint32_t fb = tc::smem_u32(&ctl.full_t[stage]);
+      const uint32_t dst = ring0 + stage * L::STAGE + L::B_OFF;
+      const int nkb = (st.kc + L::KB - 1) / L::KB;
+      if (st.kind == kFC1) {  // tokens anywhere: a token's parts a box
+        if (st.k0 == 0) mine = ctl.tok_of[st.pos0 + min(lane, st.n - 1)];
+        if (elected) tc::mbar_arrive_expect_tx(fb, nkb * st.n * kParts * 128);
+        for (int i = 0; i < st.n; ++i) {
+          const int t = __shfl_sync(0xffffffffu, mine, i);
+          if (elected)
+            for (int b = 0; b < nkb; ++b)
+              tma_load_3d(dst + b * L::B_BOX + i * kParts * 128, &p.x, (st.k0 + b * L::KB) / 2, 0, t, fb);
+        }
+      } else if (elected) {  // rows of the sorted list: one box
+        tc::mbar_arrive_expect_tx(fb, nkb * L::B_BOX);
+        for (int b = 0; b < nkb; ++b)
+          tma_load_3d(dst + b * L::B_BOX, &p.act, (st.k0 + b * L::KB) / 2, 0, st.pos0, fb);
+      }
+      __syncwarp();
+      note_issued();
+      next_stage();
+    }
+    for (int s = 0; s < p.stages; ++s)
+      if ((issued >> s) & 1u)
+        tc::mbar_wait(tc::smem_u32(&ctl.full_t[s]), (issued_par >> s) & 1u, wdrain);
+  } else if (warp == 3) {
+    // ================= scales =================
+    int ready = -1;
+    constexpr int NR = (L::N + 31) / 32;  // rows (token, part) a lane
+    for (;;) {
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.told[stage]), phase, wc)) break;
+      const FewStage st = ctl.st[stage];
+      if (st.kind == kEnd) break;
+      if (st.kind == kFC2 && ready != st.entry) {
+        if (!hidden_ready(st.entry)) break;
+        ready = st.entry;
+      }
+      const bool fc1 = st.kind == kFC1;
+      const int nk = st.kc / 128, words = (fc1 ? cf.h : cf.F) / 128;
+      uint32_t w[NR][4];
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const int r = lane + 32 * i, tok = r / kParts;
+        const int src = tok < st.n ? (fc1 ? ctl.tok_of[st.pos0 + tok] : st.pos0 + tok) : -1;
+        const uint32_t* base = fc1 ? p.xs : reinterpret_cast<const uint32_t*>(p.hidden_s);
+        base += ((int64_t)src * kParts + r % kParts) * words + st.k0 / 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][k] = src >= 0 && k < nk ? __ldcg(base + k) : 0u;
+      }
+      uint8_t* sp = ring + stage * L::STAGE;
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.full_w[stage]), phase, wc)) break;
+      if (fc1) {  // rows r0 .. r0 + 63 of the gate tile, then the same of the up tile
+        const int hb = (st.r0 & 127) >> 6;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < nk) {
+            const uint8_t* raw = sp + L::RAW + k * mx::ATOM + 16 * lane + 8 * hb;
+            const uint2 g = *reinterpret_cast<const uint2*>(raw);
+            const uint2 u = *reinterpret_cast<const uint2*>(raw + L::SF);
+            *reinterpret_cast<uint4*>(sp + L::SFA + k * mx::ATOM + 16 * lane) = make_uint4(g.x, g.y, u.x, u.y);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < nk)
+            *reinterpret_cast<uint32_t*>(sp + L::SFB + k * mx::ATOM + 16 * lane + 4 * i) = w[i][k];
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&mc.full_s[stage]));
+      next_stage();
+    }
+  } else if (warp < 8) {
+    // ================= epilogue =================
+    const int q = warp & 3;  // TMEM lane quarter
+    uint32_t meet_par = 0;
+    for (int unit = 0;; ++unit) {
+      const int buf = unit & 1;
+      const uint32_t par = (unit >> 1) & 1;
+      if (!tc::mbar_wait(tc::smem_u32(&mc.unit_told[buf]), par, wc)) break;
+      const FewStage st = mc.unit[buf];
+      if (st.kind == kEnd) break;
+      if (!tc::mbar_wait(tc::smem_u32(&mc.tmem_full[buf]), par, wc)) break;
+      tc::fence_after_sync();
+      float v[L::N];
+      tmem_ld_x16<L::N / 16>(tmem + ((uint32_t)(q * 32) << 16) + buf * L::ACC, v);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&mc.tmem_empty[buf]));
+      float y[L::NB];
+#pragma unroll
+      for (int t = 0; t < L::NB; ++t) {
+        y[t] = v[kParts * t + kParts - 1];  // the smallest part first
+#pragma unroll
+        for (int i = kParts - 2; i >= 0; --i) y[t] += v[kParts * t + i];
+      }
+      if (st.kind == kFC1) {
+        float* eb = ex + buf * 2 * L::EX;
+#pragma unroll
+        for (int t = 0; t < L::NB; ++t) eb[(q >> 1) * L::EX + t * 64 + (q & 1) * 32 + lane] = y[t];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.meet));
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.meet), meet_par, wc)) break;
+        meet_par ^= 1;
+        // a block of 32 hidden units of a token a warp
+        const int f = (q & 1) * 32;
+        for (int t = q >> 1; t < st.n; t += 2) {
+          const float z = eb[t * 64 + f + lane];
+          uint32_t code[kParts], scale[kParts];
+          e2m1_parts(silu_f(z) * eb[L::EX + t * 64 + f + lane], code, scale);
+          const int64_t row = (int64_t)(st.pos0 + t) * kParts;
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const uint32_t w = pack_codes(code[i], lane);
+            if ((lane & 7) == 0)
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.hidden) + (row + i) * (cf.F / 2) +
+                                           (st.r0 + f + lane) / 2) = w;
+            if (lane == 0) p.hidden_s[(row + i) * (cf.F / 32) + (st.r0 + f) / 32] = (uint8_t)scale[i];
+          }
+        }
+        fence_proxy_async_global();
+        __syncwarp();
+        if (lane == 0) red_release(done + st.entry, 1);
+      } else {
+        float* dst = p.ypart + ((int64_t)st.ks * p.S + st.pos0) * cf.h + st.r0 + q * 32 + lane;
+#pragma unroll
+        for (int t = 0; t < L::NB; ++t)
+          if (t < st.n) __stcg(dst + (int64_t)t * cf.h, y[t]);
+        __syncwarp();
+        if (lane == 0) red_release(done2, 1);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, L::TMEM);
+  }
+  // ---- combine: every block's share ----
+  const bool share = !ctl.abort && blockIdx.x < few_combine_items(cf);
+  if (share && threadIdx.x == 0) mc.tmem_base = wait_count(done2, ctl.fc2_writers, wc);  // (its address is read)
+  __syncthreads();
+  if (share && mc.tmem_base != 0) {
+    ld_acquire(done2);  // every thread's own
+    few_combine(p, ctl, at, warp, L::THREADS / 32, lane);
+  }
 }
 
 // Launches a kernel that may start while the one before it drains; it waits
@@ -1092,17 +1416,47 @@ bool few_encode(CUtensorMap* m, CUtensorMapDataType type, int elem, const void* 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches a kernel with a ring of as many stages as fit beside `fixed` bytes, at
+// most `most`.
+cudaError_t few_launch_ring(void (*kern)(const FewParams), int threads, int stage, int most, int fixed,
+                            FewParams& p, cudaStream_t s) {
+  fixed += 1024;  // the ring's alignment
+  p.stages = (227 * 1024 - fixed) / stage;
+  if (p.stages > most) p.stages = most;
+  const int smem = p.stages * stage + fixed;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return few_pdl_launch(kern, p.a.sms, threads, smem, s, p);
+}
+
+// The launch with MXFP4 weights.
 template <class L>
-cudaError_t few_launch(FewParams& p, const __half* xh, cudaStream_t s) {
+cudaError_t few_mx_launch(FewParams& p, const uint8_t* xq, cudaStream_t s) {
+  const moe_config_t& c = p.a.c;
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  auto weights = [&](CUtensorMap* m, const void* w, uint64_t cols, uint64_t rows, uint64_t halves,
+                     int pair) {
+    return few_encode(m, u8, 1, w, 3, cols / 2, rows, halves, 128, L::RT / pair, pair, true);
+  };
+  bool ok = weights(&p.w1, p.a.w1.w, c.h, c.F, (uint64_t)c.E * 2, 2) &&
+            weights(&p.w2, p.a.w2.w, c.F, c.h, c.E, 1);
+  if (c.n_shared)
+    ok = ok && weights(&p.w1s, p.a.w1.ws, c.h, c.F, 2, 2) && weights(&p.w2s, p.a.w2.ws, c.F, c.h, 1, 1);
+  ok = ok && few_encode(&p.x, u8, 1, xq, 3, c.h / 2, kParts, c.T, 128, kParts, 1, true) &&
+       few_encode(&p.act, u8, 1, p.hidden, 3, c.F / 2, kParts, p.S, 128, kParts, L::NB, true);
+  if (!ok) return cudaErrorInvalidValue;
+  return few_launch_ring(few_mx_kernel<L>, L::THREADS, L::STAGE, L::MAX_STAGES, L::EX_BYTES + (int)sizeof(FewMxCtl), p, s);
+}
+
+template <class L>
+cudaError_t few_launch(FewParams& p, cudaStream_t s) {
   const moe_config_t& c = p.a.c;
   const bool glu = c.act == MOE_ACT_SWIGLU;
-  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto u16 = CU_TENSOR_MAP_DATA_TYPE_UINT16;
   // weights: rows of F or h, the gate and up halves of an expert one after the other
   auto weights = [&](CUtensorMap* m, const void* w, uint64_t cols, uint64_t rows, uint64_t halves,
                      int pair) {
-    return L::W4 ? few_encode(m, u8, 1, w, 3, cols / 2, rows, halves, L::A_ROW, L::RT / pair, pair, true)
-                 : few_encode(m, u16, 2, w, 3, cols, rows, halves, L::KB, L::RT / pair, pair, false);
+    return few_encode(m, u16, 2, w, 3, cols, rows, halves, L::KB, L::RT / pair, pair, false);
   };
   const int pair = glu ? 2 : 1;
   bool ok = weights(&p.w1, p.a.w1.w, c.h, c.F, (uint64_t)c.E * pair, pair) &&
@@ -1110,22 +1464,10 @@ cudaError_t few_launch(FewParams& p, const __half* xh, cudaStream_t s) {
   if (c.n_shared)
     ok = ok && weights(&p.w1s, p.a.w1.ws, c.h, c.F, pair, pair) &&
          weights(&p.w2s, p.a.w2.ws, c.F, c.h, 1, 1);
-  const void* x = L::W4 ? static_cast<const void*>(xh) : p.a.x;
-  ok = ok && few_encode(&p.x, u16, 2, x, 2, c.h, c.T, 1, L::KB, 1, 1, false) &&
+  ok = ok && few_encode(&p.x, u16, 2, p.a.x, 2, c.h, c.T, 1, L::KB, 1, 1, false) &&
        few_encode(&p.act, u16, 2, p.hidden, 2, c.F, p.S, 1, L::KB, 8, 1, false);
-  if (L::W4)
-    ok = ok && few_encode(&p.act_s, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.hidden_s, 2, c.F / 32, p.S,
-                          1, L::KC / 32, 8, 1, false);
   if (!ok) return cudaErrorInvalidValue;
-  constexpr int kMost = 227 * 1024;
-  const int fixed = 1024 + L::RED + (int)sizeof(FewCtl);  // 1024: the ring's alignment
-  int stages = (kMost - fixed) / L::STAGE;
-  if (stages > kMaxStages) stages = kMaxStages;
-  p.stages = stages;
-  const int smem = stages * L::STAGE + fixed;
-  cudaError_t e = cudaFuncSetAttribute(few_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return few_pdl_launch(few_kernel<L>, p.a.sms, L::THREADS, smem, s, p);
+  return few_launch_ring(few_kernel<L>, L::THREADS, L::STAGE, kMaxStages, L::RED + (int)sizeof(FewCtl), p, s);
 }
 
 }  // namespace
@@ -1141,10 +1483,11 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   p.prob = reinterpret_cast<float*>(a.ws + L.prob);
   p.pairs_pad = few_pairs_pad(c);
   p.sync = reinterpret_cast<int32_t*>(a.ws + L.sync);
-  __half* xh = reinterpret_cast<__half*>(a.ws + L.xh);
-  p.xs = reinterpret_cast<float*>(a.ws + L.xs);
+  uint8_t* xq = reinterpret_cast<uint8_t*>(a.ws + L.xq);
+  uint8_t* xs = reinterpret_cast<uint8_t*>(a.ws + L.xs);
+  p.xs = reinterpret_cast<uint32_t*>(xs);
   p.hidden = a.ws + L.a;
-  p.hidden_s = reinterpret_cast<float*>(a.ws + L.as);
+  p.hidden_s = reinterpret_cast<uint8_t*>(a.ws + L.as);
   p.ypart = reinterpret_cast<float*>(a.ws + L.ypart);
   p.S = c.T * c.K + (c.n_shared ? c.T : 0);
   p.ksplit = few_ksplit(c);
@@ -1157,9 +1500,9 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   r.topk_idx = const_cast<int32_t*>(p.idx);
   r.topk_prob = const_cast<float*>(p.prob);
   const int route_blocks = (int)ceil_div((int64_t)c.E * kparts * ceil_div(c.T, kRouteTok), 8);
-  few_router_kernel<<<route_blocks + (mxfp4 ? c.T : 0), 256, 0, s>>>(
+  few_router_kernel<<<route_blocks + (mxfp4 ? c.T * (int)ceil_div(c.h, kSplitCols) : 0), 256, 0, s>>>(
       a.x, a.w_r, c.T, c.E, c.h, kparts, parts, route_blocks,
-      xh, const_cast<float*>(p.xs), p.sync, (int)few_sync_words(c));
+      xq, xs, p.sync, (int)few_sync_words(c));
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = few_pdl_launch(few_select_kernel, c.T, 256, 0, s,
@@ -1168,14 +1511,11 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Tokens a unit holds: 8 while experts have at most that many on average or
   // half of it (what is more becomes a second unit, whose weights come from the
-  // L2), 16 beyond.  us with 8 / 16: bf16 T = 32, 2 of 8: 513 / 455; MXFP4 T = 13, 2
-  // of 8 (3 tokens an expert): 166 / 234; T = 64, 8 of 64 (8): 103 / 99.
+  // L2), 16 beyond.  us with 8 / 16 beside bf16 weights, T = 32, 2 of 8: 513 / 455.
   const bool many = c.T > 8 && (int64_t)c.T * c.K > 4LL * c.E;
   if (mxfp4)
-    return many ? few_launch<FewTile<true, 8, 2, 2, 16, 512>>(p, xh, s)
-                : few_launch<FewTile<true, 8, 2, 1, 16, 512>>(p, xh, s);
-  return many ? few_launch<FewTile<false, 4, 2, 2, 8, 256>>(p, xh, s)
-              : few_launch<FewTile<false, 4, 2, 1, 16, 256>>(p, xh, s);
+    return many ? few_mx_launch<FewMxTile<2>>(p, xq, s) : few_mx_launch<FewMxTile<1>>(p, xq, s);
+  return many ? few_launch<FewTile<4, 2, 2, 8, 256>>(p, s) : few_launch<FewTile<4, 2, 1, 16, 256>>(p, s);
 }
 
 }  // namespace moe

@@ -38,7 +38,7 @@ inline bool few_counts_fit(const moe_config_t& c) {
 }
 
 struct FewLayout {
-  size_t sync, parts, idx, prob, xh, xs, a, as, ypart, total;
+  size_t sync, parts, idx, prob, xq, xs, a, as, ypart, total;
 };
 // int32 words at `sync`: the unit counter, the warps that finished FC2 results,
 // and those that finished FC1 results per busy expert (E + 1).
@@ -58,10 +58,10 @@ inline FewLayout few_layout(const moe_config_t& c) {
   w.parts = take((size_t)few_kparts(c) * T * c.E * 4);
   w.idx = take((size_t)kFewCopies * few_pairs_pad(c) * 4);
   w.prob = take((size_t)kFewCopies * few_pairs_pad(c) * 4);
-  w.xh = take(T * c.h * 2);              // tokens in fp16 (MXFP4 weights)
-  w.xs = take(T * 4);                    // and their power-of-two scales
-  w.a = take(S * c.F * 2);               // hidden values, 16 bits
-  w.as = take(S * ceil_div(c.F, 32) * 4);  // and their scales (MXFP4 weights)
+  w.xq = take(T * c.h * 2);        // tokens in four E2M1 parts (MXFP4 weights)
+  w.xs = take(T * ceil_div(c.h, 32) * 4);  // and their block scales
+  w.a = take(S * c.F * 2);         // hidden values: bf16, or parts
+  w.as = take(S * ceil_div(c.F, 32) * 4);  // and their block scales
   w.ypart = take((size_t)few_ksplit(c) * S * c.h * 4);
   w.total = off;
   return w;

@@ -3,10 +3,15 @@ few tokens) against the float64 oracle.
 
 Tolerance of y, from the roundings on the way (all sums fp32, u = 2^-23 an
 addition, of n terms n u sum|terms|): FC1's sums, carried through the
-activation (|phi'| <= 1.13; the expert's hidden values are then rounded to 16
-bits, at most half a bf16 step, 2^-8 |a|), FC2's sums, p (relative 2^-18, the
-router's logits included) and the bf16 y, 2^-8 |y|.  The bound is evaluated per
-element from the absolute values of the same products."""
+activation (|phi'| <= 1.13; the expert's hidden values are then rounded to bf16,
+at most half a step, 2^-8 |a|), FC2's sums, p (relative 2^-18, the router's logits
+included) and the bf16 y, 2^-8 |y|.  The bound is evaluated per element from the
+absolute values of the same products.  Beside MXFP4 weights tokens and hidden
+values are sums of four E2M1 blocks of 32 columns: part 0 rounds to steps of at
+most s (s the power of two with the block's largest value in [2 s, 4 s)) and leaves
+at most s / 2, which is 2 units of part 1's scale s / 4, where E2M1's steps are at
+most 1/2; so it leaves s / 16 = 2 units of s / 32, part 2 s / 128 = 2 units of
+s / 256, part 3 s / 1024, at most 2^-11 of the block's largest value."""
 
 import numpy as np
 import pytest
@@ -100,13 +105,21 @@ class Few:
         F, h = self.F, self.h
         z = x @ w1.T + (0 if b1 is None else b1)
         dz = h * U * (np.abs(x) @ np.abs(w1).T + (0 if b1 is None else np.abs(b1)))
+
+        def parts(v):  # what a block's four parts leave
+            m = np.abs(v).reshape(len(v), -1, 32).max(2)
+            return 2.0 ** -11 * np.repeat(m, 32, axis=1)
+
+        if self.mx:
+            dz = dz + parts(x) @ np.abs(w1).T
         if self.act == 1:
             g, u, dg, du = z[:, :F], z[:, F:], dz[:, :F], dz[:, F:]
             a = O.silu(g) * u
             da = 1.13 * dg * (np.abs(u) + du) + (np.abs(O.silu(g)) + 1.13 * dg) * du
         else:
             a, da = O.gelu(z), 1.13 * dz
-        da = da + (2.0 ** -8 + 2.0 ** -18) * (np.abs(a) + da)
+        da = da + 2.0 ** -18 * (np.abs(a) + da)
+        da = da + (parts(np.abs(a) + da) if self.mx else 2.0 ** -8 * (np.abs(a) + da))
         o = a @ w2.T + (0 if b2 is None else b2)
         S = np.abs(a) @ np.abs(w2).T
         return o, da @ np.abs(w2).T + F * U * S
@@ -216,8 +229,8 @@ def test_mxfp4_weights(c):
 @pytest.mark.parametrize("mx", [False, True])
 @pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** 40])
 def test_token_magnitudes(mx, scale):
-    """Tokens far from 1 (their 16-bit copies keep the exponent range), beside
-    ordinary ones; the activation's product must stay finite."""
+    """Tokens far from 1, beside ordinary ones, and an outlier in a row; the
+    activation's product must stay finite."""
     rng = np.random.default_rng(5)
     x = rng.standard_normal((4, 256))
     x[1] *= scale
