@@ -9,7 +9,7 @@
 //
 // Three launches, each started while the one before drains (programmatic
 // dependent launch).  few_router_kernel writes partial logits (and, for MXFP4
-// weights, the tokens as E2M1 parts); few_select_kernel adds them and selects, a warp
+// weights, the tokens as E2M1 parts); few_select_kernel adds them and selects, a block
 // a token.  few_kernel does the rest, one block per SM:
 //   every block sorts the (token, slot) pairs by expert (the same list
 //   everywhere), then takes units of work from one counter: first all of FC1's
@@ -21,7 +21,7 @@
 //   When all FC2 units are done every block adds its share of the slots'
 //   results, in a fixed order, and writes y.
 // Within a block: two producer warps stream the unit's weight rows and the
-// expert's token rows through a ring of shared-memory stages (512 columns a
+// expert's token rows through a ring of shared-memory stages (256 columns a
 // stage, TMA boxes of many rows: a copy per row costs its issuing warp about
 // 95 cycles whatever its size, which held an earlier form of this kernel at 10 bytes a
 // cycle and SM).  The weight producer runs ahead of the arithmetic, into the
@@ -29,7 +29,7 @@
 // phase borders; only the token producer waits for FC1's results.  NW consumer
 // warps split a stage's columns and multiply with m16n8k16 tensor-core
 // instructions, weight rows as M, tokens as N: the weights are read once from
-// HBM however many tokens share them, and a product with up to 32 tokens costs
+// HBM however many tokens share them, and a product with up to 16 tokens costs
 // less than the loads.  (Beside bf16 weights the mma rate is not what bounds
 // this kernel, and 64-row units balance the SMs better than tcgen05's 128.
 // MXFP4 weights have a kernel of their own, few_mx_kernel, below.)
@@ -38,7 +38,6 @@
 // "Scalable Training of Mixture-of-Experts Models with Megatron Core" (review),
 // §2.1 (the four steps), §2.2 (router); the same formulas and options as
 // moe_layer_fwd.
-#include <cuda_fp16.h>
 #include <cuda_fp4.h>
 
 #include <type_traits>
@@ -62,7 +61,7 @@ MOE_D void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: 
 // E2M1's steps are at most 1, so part 0 leaves at most s / 2; at s / 4 that is at
 // most 2, steps of 1/2, and from then on every part takes three bits: the four
 // leave at most s / 1024, 2^-11 of the block's largest value (a bf16 number's own
-// half step is 2^-9 of it).  A block with an infinity or a NaN gets the NaN scale.
+// half step is 2^-8 of it).  A block with an infinity or a NaN gets the NaN scale.
 constexpr int kParts = 4;
 MOE_D void e2m1_parts(float v, uint32_t (&code)[kParts], uint32_t (&scale)[kParts]) {
   uint32_t m = __float_as_uint(v) & 0x7fffffffu;
@@ -110,7 +109,9 @@ __device__ void few_split_token(const __nv_bfloat16* __restrict__ x, int h, int 
 // x is exact in fp32 and the products and sums are fp32, each lane over its
 // own columns, the lanes added as a tree.  The blocks past the router's convert
 // one token each; block 0 clears the counters of few_kernel.
-constexpr int kRouteTok = 8, kSplitCols = 1024;
+// (256 columns a block: one token of 256 experts 55.9 us, with 1024 57.0; 64 tokens of 64
+// 70.3 and 69.5.)
+constexpr int kRouteTok = 8, kSplitCols = 256;
 __global__ void __launch_bounds__(256)
     few_router_kernel(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w_r, int T,
                       int E, int h, int kparts, float* __restrict__ parts, int route_blocks,
@@ -950,13 +951,12 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 // 156 / 92 / 165 us; this takes 129 / 70 / 133.
 //   warp 0  weights: 128-row boxes of 256 codes and the rows' scale atoms;
 //   warp 1  TMEM owner and MMA issuer (one elected lane);
-//   warp 2  tokens: their parts (FC1: token by token; FC2: one box);
+//   warps 2, 8, 9  tokens: their parts (FC1: token by token; FC2: one box);
 //   warp 3  scales: an FC1 unit's atoms put together from the halves of two
 //           tiles, the tokens' scale words gathered into atoms;
 //   warps 4-7  epilogue, a TMEM lane quarter each: adds the parts, FC1: SwiGLU
 //           (gate and up meet in shared memory) and the hidden values' parts;
 //           FC2: partial results.
-// Warps 8 and 9 only help with the list and the combine.
 template <int NT_>
 struct FewMxTile {
   static constexpr int NT = NT_, NB = 8 * NT, N = NB * kParts, RT = 128, KC = 512, KB = 256;
@@ -966,6 +966,7 @@ struct FewMxTile {
   static constexpr int B_OFF = A_BYTES, RAW = B_OFF + B_BYTES, SFA = RAW + 2 * SF, SFB = SFA + SF;
   static constexpr int STAGE = SFB + SF;
   static constexpr int EX = NB * 64, EX_BYTES = 2 * 2 * EX * 4;  // gate and up, two units in turn
+  static constexpr int TOKEN_WARPS = 3;  // warps 2, 8 and 9
   static constexpr int THREADS = 320;
   static constexpr uint32_t ACC = 64, SF_COL0 = 128, SF_COLS = 32, TMEM = 256;  // TMEM columns
   static constexpr int MAX_STAGES = (TMEM - SF_COL0) / SF_COLS;
@@ -1021,9 +1022,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
   const uint32_t ring0 = tc::smem_u32(ring);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s)
-      for (uint64_t* b : {&ctl.full_w[s], &ctl.full_t[s], &ctl.told[s], &ctl.empty[s], &mc.full_s[s]})
+    for (int s = 0; s < p.stages; ++s) {
+      for (uint64_t* b : {&ctl.full_w[s], &ctl.told[s], &ctl.empty[s], &mc.full_s[s]})
         tc::mbar_init(tc::smem_u32(b), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.full_t[s]), L::TOKEN_WARPS);
+    }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(tc::smem_u32(&mc.unit_told[b]), 1);
       tc::mbar_init(tc::smem_u32(&mc.tmem_full[b]), 1);
@@ -1220,14 +1223,17 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
       if (elected) tc::mma_commit(tc::smem_u32(&mc.drain));
       tc::mbar_wait(tc::smem_u32(&mc.drain), 0, wdrain);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp >= 8) {
     // ================= tokens =================
+    // A token's parts are a box of their own (FC1): three warps share the issue (one
+    // token of 256 experts 55.8 us with one warp, 54.8 so; 13 tokens of 8 127.9, 127.3).
+    const int tw = warp == 2 ? 0 : warp - 7;
     int ready = -1, mine = 0;
     for (;;) {
       if (!tc::mbar_wait(tc::smem_u32(&ctl.told[stage]), phase, wc)) break;
       const FewStage st = ctl.st[stage];
       if (st.kind == kEnd) break;
-      if (st.kind == kFC2 && ready != st.entry) {
+      if (tw == 0 && st.kind == kFC2 && ready != st.entry) {
         if (!hidden_ready(st.entry)) break;
         fence_proxy_async_global();
         ready = st.entry;
@@ -1237,17 +1243,19 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
       const int nkb = (st.kc + L::KB - 1) / L::KB;
       if (st.kind == kFC1) {  // tokens anywhere: a token's parts a box
         if (st.k0 == 0) mine = ctl.tok_of[st.pos0 + min(lane, st.n - 1)];
-        if (elected) tc::mbar_arrive_expect_tx(fb, nkb * st.n * kParts * 128);
-        for (int i = 0; i < st.n; ++i) {
+        const int mine_n = (st.n - tw + L::TOKEN_WARPS - 1) / L::TOKEN_WARPS;  // tokens tw, tw + 3, ..
+        if (elected) tc::mbar_arrive_expect_tx(fb, nkb * mine_n * kParts * 128);
+        for (int i = tw; i < st.n; i += L::TOKEN_WARPS) {
           const int t = __shfl_sync(0xffffffffu, mine, i);
           if (elected)
             for (int b = 0; b < nkb; ++b)
               tma_load_3d(dst + b * L::B_BOX + i * kParts * 128, &p.x, (st.k0 + b * L::KB) / 2, 0, t, fb);
         }
       } else if (elected) {  // rows of the sorted list: one box
-        tc::mbar_arrive_expect_tx(fb, nkb * L::B_BOX);
-        for (int b = 0; b < nkb; ++b)
-          tma_load_3d(dst + b * L::B_BOX, &p.act, (st.k0 + b * L::KB) / 2, 0, st.pos0, fb);
+        tc::mbar_arrive_expect_tx(fb, tw == 0 ? nkb * L::B_BOX : 0);
+        if (tw == 0)
+          for (int b = 0; b < nkb; ++b)
+            tma_load_3d(dst + b * L::B_BOX, &p.act, (st.k0 + b * L::KB) / 2, 0, st.pos0, fb);
       }
       __syncwarp();
       note_issued();
