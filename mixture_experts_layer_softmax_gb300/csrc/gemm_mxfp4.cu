@@ -58,7 +58,7 @@ struct Mx4Params {
   __nv_bfloat16* out;      // [P, N] bf16 or null
   uint8_t* out_q;          // FC1: codes of a [P, N / 2] or null
   uint8_t* out_sf;         // FC1: scale atoms of a
-  int E, Kd, N, Nb;
+  int P, E, Kd, N, Nb;
   bool wide;               // out is 32-byte aligned (its rows are multiples of 256 bytes)
   int* status;
   uint64_t wait_limit_ns;
@@ -374,13 +374,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), TMEM_COLS);
     tc::tmem_relinquish();
   }
-  for (int e = threadIdx.x; e <= E; e += kThreads) ctl.off[e] = __ldg(p.offsets + e);
+  // (kept within the rows here, and ascending below: no offsets reach past a tensor)
+  for (int e = threadIdx.x; e <= E; e += kThreads) ctl.off[e] = min(max(__ldg(p.offsets + e), 0), p.P);
   __syncthreads();
   if (warp == 2) {  // tile_start and rtile: exclusive scans over the experts
-    int run_t = 0, run_r = 0;
+    int run_t = 0, run_r = 0, run_o = ctl.off[0];
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
-      const int mblk = e < E ? (ctl.off[e + 1] - ctl.off[e] + BM - 1) / BM : 0;
+      int end = max(run_o, e < E ? ctl.off[e + 1] : 0);  // expert e's end: the largest offset so far
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end = max(end, t);
+      }
+      const int prev = __shfl_up_sync(0xffffffffu, end, 1), beg = lane ? prev : run_o;
+      if (e < E) ctl.off[e + 1] = end;
+      run_o = __shfl_sync(0xffffffffu, end, 31);
+      const int mblk = (end - beg + BM - 1) / BM;
       int it = mblk * nblk, ir = mblk;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -568,8 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) a[j] *= inv;
           if (valid) {
+            const uint32_t keep = code == 255u ? 0u : ~0u;  // codes of a NaN block: 0, as the quantiser's
             *reinterpret_cast<uint4*>(p.out_q + (row * p.N + n) / 2) =
-                make_uint4(e2m1x8(a), e2m1x8(a + 8), e2m1x8(a + 16), e2m1x8(a + 24));
+                make_uint4(e2m1x8(a) & keep, e2m1x8(a + 8) & keep, e2m1x8(a + 16) & keep, e2m1x8(a + 24) & keep);
             // its scale: atom (rtile[e] + mb, kb = nb), row i, block qt
             p.out_sf[mx::atom_word(ctl.rtile[e] + mb, p.N / 128, nb, i) + qt] = (uint8_t)code;
           }
@@ -654,7 +665,7 @@ cudaError_t launch_grouped_gemm_mxfp4(bool swiglu, int P, const uint8_t* A, cons
   Mx4Params p{};
   p.offsets = offsets; p.prob = prob; p.a_sf = A_sf; p.b_sf = B_sf;
   p.out = static_cast<__nv_bfloat16*>(out); p.out_q = out_q; p.out_sf = out_sf;
-  p.E = E; p.Kd = Kd; p.N = N; p.Nb = Nb;
+  p.P = P; p.E = E; p.Kd = Kd; p.N = N; p.Nb = Nb;
   p.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;

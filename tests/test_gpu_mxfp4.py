@@ -357,3 +357,54 @@ def test_injected_failure_enqueues_nothing():
         M.moe_mxfp4_quantize(16, 128, 1, None, x, q, sf)
     torch.cuda.synchronize()
     assert (q == 0x77).all() and (sf == 0x77).all()
+
+
+def test_products_keep_broken_offsets_within_the_rows():
+    """Offsets past the last row end there; descending ones reach past no tensor."""
+    M = lib()
+    c = _case(seed=12, T=140, K=1, E=5, h=256, F=128)
+    P, E, h, F, offs = c["P"], c["E"], c["h"], c["F"], c["offsets"]
+    cfg = M.make_config(c["T"], h, E, c["K"], F)
+    xq, xsf = quantize_dev(M, c["x"], E, offs)
+    w1q, w1sf = quantize_dev(M, c["w1"], E)
+    w2q, w2sf = quantize_dev(M, c["w2"], E)
+    nsf, G = M.moe_mxfp8_scale_bytes(P, F, E), 4096
+    past = offs.astype(np.int64).copy()
+    past[-1] = 1 << 30
+    outs = []
+    for o in (offs, past, np.array([P, 0, P, -9, 1 << 30, 3]), np.array([-5, 1 << 30, 0, 17, 2, 1])):
+        od = torch.from_numpy(o.astype(np.int32)).cuda()
+        a = torch.full((P * F + 2 * G,), 5.0, dtype=torch.bfloat16, device="cuda")
+        y = torch.full((P * h + 2 * G,), 5.0, dtype=torch.bfloat16, device="cuda")
+        aq = torch.full((P * F // 2 + 2 * G,), 0x77, dtype=torch.uint8, device="cuda")
+        asf = torch.full((nsf + 2 * G,), 0x77, dtype=torch.uint8, device="cuda")
+        M.moe_expert_fc1_mxfp4(cfg, xq, xsf, od, None, w1q, w1sf, a[G:-G], aq[G:-G], asf[G:-G])
+        M.moe_expert_fc2_mxfp4(cfg, aq[G:-G], asf[G:-G], od, w2q, w2sf, y[G:-G])
+        torch.cuda.synchronize()
+        assert M.moe_get_error() == M.MOE_OK
+        for b, v in ((a, 5.0), (y, 5.0), (aq, 0x77), (asf, 0x77)):
+            assert (b[:G] == v).all() and (b[-G:] == v).all()
+        outs.append((a.clone(), y.clone()))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_fc1_quantised_output_of_non_finite_blocks():
+    """A block of a with a NaN: the NaN scale and zero codes, as the quantiser writes it."""
+    M = lib()
+    c = _case(seed=13, T=40, K=1, E=2, h=128, F=256)
+    P, E, h, F, offs = c["P"], c["E"], c["h"], c["F"], c["offsets"]
+    cfg = M.make_config(c["T"], h, E, c["K"], F)
+    x = c["x"].copy()
+    x[3, 7] = np.nan
+    xq, xsf = quantize_dev(M, x, E, offs)
+    w1q, w1sf = quantize_dev(M, c["w1"], E)
+    od = torch.from_numpy(offs.astype(np.int32)).cuda()
+    aq = torch.full((P, F // 2), 0x77, dtype=torch.uint8, device="cuda")
+    asf = torch.zeros(M.moe_mxfp8_scale_bytes(P, F, E), dtype=torch.uint8, device="cuda")
+    M.moe_expert_fc1_mxfp4(cfg, xq, xsf, od, None, w1q, w1sf, None, aq, asf)
+    torch.cuda.synchronize()
+    assert M.moe_get_error() == M.MOE_OK
+    sc = scales_of(asf, scale_index(P, F, offs))
+    assert (sc[3] == 255).all() and (aq[3] == 0).all()
+    rest = np.setdiff1d(np.arange(P), [3])
+    assert (sc[rest] != 255).all()
