@@ -55,51 +55,55 @@ MOE_D void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MOE_D void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---- E2M1 parts --------------------------------------------------------------------
-// A block of 32 values, one a lane, as a sum of kParts E2M1 blocks, each with a
-// scale of its own: part 0 rounds v / s, s the power of two that puts the largest
-// magnitude into [2, 4), and each further part what the ones before left.  There
-// E2M1's steps are at most 1, so part 0 leaves at most s / 2; at s / 4 that is at
-// most 2, steps of 1/2, and from then on every part takes three bits: the four
-// leave at most s / 1024, 2^-11 of the block's largest value (a bf16 number's own
-// half step is 2^-8 of it).  A block with an infinity or a NaN gets the NaN scale.
+// A block of 32 values, four a lane of eight lanes, as a sum of kParts E2M1 blocks,
+// each with a scale of its own: part 0 rounds v / s, s the power of two that puts
+// the largest magnitude into [2, 4), and each further part what the ones before
+// left.  There E2M1's steps are at most 1, so part 0 leaves at most s / 2; at s / 4
+// that is at most 2, steps of 1/2, and from then on every part takes three bits: the
+// four leave at most s / 1024, 2^-11 of the block's largest value (a bf16 number's
+// own half step is 2^-8 of it).  A block with an infinity or a NaN gets the NaN
+// scale.  code[i]: the lane's four codes of part i, the first lowest.
 constexpr int kParts = 4;
-MOE_D void e2m1_parts(float v, uint32_t (&code)[kParts], uint32_t (&scale)[kParts]) {
-  uint32_t m = __float_as_uint(v) & 0x7fffffffu;
+MOE_D void e2m1_parts(float (&v)[4], uint32_t (&code)[kParts], uint32_t (&scale)[kParts]) {
+  uint32_t m = 0u;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int e = (int)(m >> 23);
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
     const int x = max(e - 1 - (i == 0 ? 0 : 3 * i - 1), 0);
     scale[i] = e == 255 ? (i == 0 ? 255u : 0u) : (uint32_t)x;
-    const uint32_t c = e == 255 ? 0u
-        : __nv_cvt_float2_to_fp4x2(make_float2(v * __uint_as_float((254u - x) << 23), 0.f), __NV_E2M1,
-                                   cudaRoundNearest) & 15u;
-    code[i] = c;
-    v -= __uint_as_float((c & 8u) << 28 | (c & 7u) << 22) * 0x1p126f * mx::e8m0_value((uint32_t)x);
+    const float inv = __uint_as_float((254u - x) << 23), one = mx::e8m0_value((uint32_t)x);
+    uint32_t c = 0u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      c |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * j] * inv, v[2 * j + 1] * inv), __NV_E2M1,
+                                              cudaRoundNearest) << (8 * j);
+    code[i] = e == 255 ? 0u : c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = c >> (4 * j);
+      v[j] -= __uint_as_float((b & 8u) << 28 | (b & 7u) << 22) * 0x1p126f * one;
+    }
   }
 }
-// The 32 lanes' codes as words of eight, the first lane's lowest; valid on lanes
-// 0, 8, 16, 24.
-MOE_D uint32_t pack_codes(uint32_t code, int lane) {
-  uint32_t w = code << (4 * (lane & 7));
-#pragma unroll
-  for (int o = 1; o <= 4; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-  return w;
-}
 
-// A token's columns b0 .. b1 - 1 (blocks of 32) as parts: a warp a block.
+// A token's columns b0 .. b1 - 1 (blocks of 32) as parts: four blocks a warp.
 __device__ void few_split_token(const __nv_bfloat16* __restrict__ x, int h, int b0, int b1,
                                 uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int b = b0 + warp; b < b1; b += blockDim.x / 32) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 3, l = lane & 7;
+  for (int b = b0 + 4 * warp; b < b1; b += blockDim.x / 8) {  // (b1 - b0 is a multiple of four)
+    const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(x + (b + g) * 32 + 4 * l);
+    const float2 lo = __bfloat1622float2(src[0]), hi = __bfloat1622float2(src[1]);
+    float v[4] = {lo.x, lo.y, hi.x, hi.y};
     uint32_t code[kParts], scale[kParts];
-    e2m1_parts(to_f32(x[b * 32 + lane]), code, scale);
+    e2m1_parts(v, code, scale);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-      const uint32_t w = pack_codes(code[i], lane);
-      if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(q + (int64_t)i * (h / 2) + b * 16 + lane / 2) = w;
-      if (lane == 0) sf[(int64_t)i * (h / 32) + b] = (uint8_t)scale[i];
+      *reinterpret_cast<uint16_t*>(q + (int64_t)i * (h / 2) + (b + g) * 16 + 2 * l) = (uint16_t)code[i];
+      if (l == 0) sf[(int64_t)i * (h / 32) + b + g] = (uint8_t)scale[i];
     }
   }
 }
@@ -109,9 +113,7 @@ __device__ void few_split_token(const __nv_bfloat16* __restrict__ x, int h, int 
 // x is exact in fp32 and the products and sums are fp32, each lane over its
 // own columns, the lanes added as a tree.  The blocks past the router's convert
 // one token each; block 0 clears the counters of few_kernel.
-// (256 columns a block: one token of 256 experts 55.9 us, with 1024 57.0; 64 tokens of 64
-// 70.3 and 69.5.)
-constexpr int kRouteTok = 8, kSplitCols = 256;
+constexpr int kRouteTok = 8, kSplitCols = 1024;
 __global__ void __launch_bounds__(256)
     few_router_kernel(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w_r, int T,
                       int E, int h, int kparts, float* __restrict__ parts, int route_blocks,
@@ -948,8 +950,10 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 // accumulators in TMEM (two, for two units in turn).  Decoding the codes on the
 // ALUs for m16n8k16 products (tokens in fp16) took 34 warp instructions for 16 x
 // 32 weights: T = 13, 2 of 8 experts / T = 64, 8 of 64 / T = 5, 8 of 256 ran in
-// 156 / 92 / 165 us; this takes 129 / 70 / 133.
-//   warp 0  weights: 128-row boxes of 256 codes and the rows' scale atoms;
+// 156 / 92 / 165 us; this takes 122 / 54 / 129.
+//   warp 0  weights: 128-row boxes of 256 codes and the rows' scale atoms; 512
+//           columns a stage (256 a stage, seven or eight stages: the scale warp's
+//           work a stage bounds it, 161 / 68 / 171 us);
 //   warp 1  TMEM owner and MMA issuer (one elected lane);
 //   warps 2, 8, 9  tokens: their parts (FC1: token by token; FC2: one box);
 //   warp 3  scales: an FC1 unit's atoms put together from the halves of two
@@ -960,18 +964,19 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 template <int NT_>
 struct FewMxTile {
   static constexpr int NT = NT_, NB = 8 * NT, N = NB * kParts, RT = 128, KC = 512, KB = 256;
+  static constexpr int NKB = KC / KB, NKA = KC / 128;  // boxes and scale atoms along K (uint4 loads below)
   static constexpr int A_BOX = RT * 128, B_BOX = N * 128;  // bytes of 256 columns
-  static constexpr int A_BYTES = 2 * A_BOX, B_BYTES = 2 * B_BOX;
-  static constexpr int SF = KC / 128 * mx::ATOM;           // atoms of 128 rows
+  static constexpr int A_BYTES = NKB * A_BOX, B_BYTES = NKB * B_BOX;
+  static constexpr int SF = NKA * mx::ATOM;                // atoms of 128 rows
   static constexpr int B_OFF = A_BYTES, RAW = B_OFF + B_BYTES, SFA = RAW + 2 * SF, SFB = SFA + SF;
   static constexpr int STAGE = SFB + SF;
   static constexpr int EX = NB * 64, EX_BYTES = 2 * 2 * EX * 4;  // gate and up, two units in turn
   static constexpr int TOKEN_WARPS = 3;  // warps 2, 8 and 9
   static constexpr int THREADS = 320;
-  static constexpr uint32_t ACC = 64, SF_COL0 = 128, SF_COLS = 32, TMEM = 256;  // TMEM columns
+  static constexpr uint32_t ACC = 64, SF_COL0 = 128, SF_COLS = 8 * NKA, TMEM = 256;  // TMEM columns
   static constexpr int MAX_STAGES = (TMEM - SF_COL0) / SF_COLS;
   static MOE_HD int writers(int n, int) { return n > 0 ? 4 : 0; }
-  static_assert(N <= (int)ACC && STAGE % 1024 == 0, "TMEM columns, swizzle alignment");
+  static_assert(N <= (int)ACC && STAGE % 1024 == 0 && SFA % 128 == 0, "TMEM columns, swizzle alignment");
 };
 
 struct FewMxCtl {
@@ -1149,7 +1154,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
           tc::mbar_arrive(tc::smem_u32(&ctl.told[stage]));
           if (st.kind != kEnd) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < L::NKB; ++b)
               if (b < nkb) tma_load_3d(dst + b * L::A_BOX, map, (k0 + b * L::KB) / 2, st.r0, half0, fb, policy);
             const int64_t off = (int64_t)(k0 / 128) * mx::ATOM;
             tc::bulk_load(dst + (fc1 ? L::RAW : L::SFA), sf0 + off, sf_bytes, fb);
@@ -1187,11 +1192,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
         tc::fence_after_sync();
         const uint32_t so = stage * (L::STAGE >> 4);  // descriptors count 16 bytes
         const uint32_t d = tmem + buf * L::ACC;
-        const uint32_t sfa = tmem + L::SF_COL0 + stage * L::SF_COLS, sfb = sfa + 16;
+        const uint32_t sfa = tmem + L::SF_COL0 + stage * L::SF_COLS, sfb = sfa + 4 * L::NKA;
         const int nk = st.kc / 128;
         if (elected) {
 #pragma unroll
-          for (int k = 0; k < L::KC / 128; ++k) {
+          for (int k = 0; k < L::NKA; ++k) {
             if (k >= nk) break;
             tc::tmem_cp_32x128b_warpx4(sfa + 4 * k, sfa_desc + so + k * (mx::ATOM >> 4));
             tc::tmem_cp_32x128b_warpx4(sfb + 4 * k, sfb_desc + so + k * (mx::ATOM >> 4));
@@ -1266,6 +1271,10 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
         tc::mbar_wait(tc::smem_u32(&ctl.full_t[s]), (issued_par >> s) & 1u, wdrain);
   } else if (warp == 3) {
     // ================= scales =================
+    // The tokens' scale words come from the L2, asked for while the stage's weights
+    // are under way.  (Asked for a stage earlier, they are waited for by the stage's
+    // proxy fence all the same: 13 tokens of 8 experts 123.6 us, so 122.2; a word a
+    // load, not a stage's words in one: 127.5.)
     int ready = -1;
     constexpr int NR = (L::N + 31) / 32;  // rows (token, part) a lane
     for (;;) {
@@ -1278,7 +1287,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
       }
       const bool fc1 = st.kind == kFC1;
       const int nk = st.kc / 128, words = (fc1 ? cf.h : cf.F) / 128;
-      uint32_t w[NR][4];
+      alignas(16) uint32_t w[NR][L::NKA];
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
         const int r = lane + 32 * i, tok = r / kParts;
@@ -1286,14 +1295,22 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
         const uint32_t* base = fc1 ? p.xs : reinterpret_cast<const uint32_t*>(p.hidden_s);
         base += ((int64_t)src * kParts + r % kParts) * words + st.k0 / 128;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = src >= 0 && k < nk ? __ldcg(base + k) : 0u;
+        for (int k = 0; k < L::NKA; ++k) w[i][k] = 0u;
+        if (src < 0) continue;
+        if (nk == L::NKA && words % L::NKA == 0) {  // a stage's words, aligned
+          *reinterpret_cast<uint4*>(w[i]) = __ldcg(reinterpret_cast<const uint4*>(base));
+        } else {
+#pragma unroll
+          for (int k = 0; k < L::NKA; ++k)
+            if (k < nk) w[i][k] = __ldcg(base + k);
+        }
       }
       uint8_t* sp = ring + stage * L::STAGE;
       if (!tc::mbar_wait(tc::smem_u32(&ctl.full_w[stage]), phase, wc)) break;
       if (fc1) {  // rows r0 .. r0 + 63 of the gate tile, then the same of the up tile
         const int hb = (st.r0 & 127) >> 6;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < L::NKA; ++k)
           if (k < nk) {
             const uint8_t* raw = sp + L::RAW + k * mx::ATOM + 16 * lane + 8 * hb;
             const uint2 g = *reinterpret_cast<const uint2*>(raw);
@@ -1304,7 +1321,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < NR; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < L::NKA; ++k)
           if (k < nk)
             *reinterpret_cast<uint32_t*>(sp + L::SFB + k * mx::ATOM + 16 * lane + 4 * i) = w[i][k];
       tc::fence_proxy_async_smem();
@@ -1344,20 +1361,24 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
         if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.meet));
         if (!tc::mbar_wait(tc::smem_u32(&ctl.meet), meet_par, wc)) break;
         meet_par ^= 1;
-        // a block of 32 hidden units of a token a warp
-        const int f = (q & 1) * 32;
-        for (int t = q >> 1; t < st.n; t += 2) {
-          const float z = eb[t * 64 + f + lane];
+        // blocks of 32 hidden units of a token, eight lanes a block, four blocks a warp
+        // (a block a warp, a value a lane: 64 tokens of 64 experts 69.1 us, so 54.1)
+        const int l = lane & 7;
+        for (int i0 = 4 * q; i0 < 2 * st.n; i0 += 16) {  // whole warps (shuffles)
+          const int i = i0 + (lane >> 3), t = i >> 1, f = (i & 1) * 32;
+          const bool valid = t < st.n;
+          const int at4 = (valid ? t * 64 + f : 0) + 4 * l;
+          const float4 z = *reinterpret_cast<const float4*>(eb + at4), u = *reinterpret_cast<const float4*>(eb + L::EX + at4);
+          float v4[4] = {silu_f(z.x) * u.x, silu_f(z.y) * u.y, silu_f(z.z) * u.z, silu_f(z.w) * u.w};
           uint32_t code[kParts], scale[kParts];
-          e2m1_parts(silu_f(z) * eb[L::EX + t * 64 + f + lane], code, scale);
+          e2m1_parts(v4, code, scale);
+          if (!valid) continue;
           const int64_t row = (int64_t)(st.pos0 + t) * kParts;
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            const uint32_t w = pack_codes(code[i], lane);
-            if ((lane & 7) == 0)
-              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.hidden) + (row + i) * (cf.F / 2) +
-                                           (st.r0 + f + lane) / 2) = w;
-            if (lane == 0) p.hidden_s[(row + i) * (cf.F / 32) + (st.r0 + f) / 32] = (uint8_t)scale[i];
+          for (int k = 0; k < kParts; ++k) {
+            *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.hidden) + (row + k) * (cf.F / 2) +
+                                         (st.r0 + f) / 2 + 2 * l) = (uint16_t)code[k];
+            if (l == 0) p.hidden_s[(row + k) * (cf.F / 32) + (st.r0 + f) / 32] = (uint8_t)scale[k];
           }
         }
         fence_proxy_async_global();
