@@ -171,13 +171,11 @@ __device__ __noinline__ void few_select_exact(const float* logit, int t, RouterA
 }
 
 // Adds the partial logits and selects: a block a token, a thread an expert, with
-// select_and_write's choices: each thread ranks its expert by counting the keys
-// above its own.  (A warp a token with the logits in registers, as the large
-// router has it, took 9.5 us for one token of 64 experts and 16 us of 256; this
-// 2.8 and 5.6, four threads an expert 4 and 5.5.)  The biases are read before the
-// partial logits are there: the router, a plain launch, runs, so what came before
-// it on the stream is done.  The results are written kFewCopies times: each block
-// of few_kernel reads one of the copies.
+// select_and_write's choices.  (A warp a token with the logits in registers, as the
+// large router has it, took 9.5 us for one token of 64 experts and 16 us of 256.)
+// The biases are read before the partial logits are there: the router, a plain
+// launch, runs, so what came before it on the stream is done.  The results are
+// written kFewCopies times: each block of few_kernel reads one of the copies.
 __global__ void __launch_bounds__(256)
     few_select_kernel(const float* __restrict__ parts, int kparts, const float* gate_bias,
                       RouterArgs r, int pairs_pad, int32_t* idx_out, float* prob_out) {
@@ -193,36 +191,50 @@ __global__ void __launch_bounds__(256)
   const float sb = r.sel_bias && e < r.E ? __ldg(r.sel_bias + e) : 0.f;
   pdl_wait();
   float l = 0.f;
-  uint32_t key = 0u;  // order-preserving, 0 past E
+  uint32_t key = 0u;  // order-preserving; 0 past E and for what was picked
   if (e < r.E) {
 #pragma unroll 4
     for (int p = 0; p < kparts; ++p) l += __ldcg(parts + ((int64_t)p * r.T + t) * r.E + e);
     l += gb;
     const float fast = sig ? sigmoid_f(l) : l;  // selection_key_fast
-    key = sortable_key(r.sel_bias ? __fadd_rn(fast, sb) : fast);
+    key = max(sortable_key(r.sel_bias ? __fadd_rn(fast, sb) : fast), 1u);
   }
   s_logit[e] = l;
   s_key[e] = key;
-  if (e < 32) s_sel[e] = 0;
-  __syncthreads();
-  if (r.force_balance) {
-    if (e < r.K) s_sel[e] = (int)(((int64_t)t * r.K + e) % r.E);
-  } else if (e < r.E) {
-    int rank = 0;  // equal keys: the lower expert first
-#pragma unroll 2
-    for (int j = 0; j < r.E; j += 4) {
-      const uint4 k = *reinterpret_cast<const uint4*>(s_key + j);
-      rank += (k.x > key || (k.x == key && j < e)) + (k.y > key || (k.y == key && j + 1 < e)) +
-              (k.z > key || (k.z == key && j + 2 < e)) + (k.w > key || (k.w == key && j + 3 < e));
-    }
-    if (rank <= r.K) s_sel[rank] = e;  // the (K+1)-th too: its gap is looked at
-  }
   __syncthreads();
   if (e >= 32) return;
-  const int my = s_sel[lane];
+  // One warp picks: the largest key of its 256, the lowest expert among equals, and
+  // again without it.  (Each thread counting the keys above its own, bound by the
+  // shared-memory reads: 4.8 us for the kernel with 256 experts and one token; this
+  // 2.7.)  The (K+1)-th too: its gap is looked at below.
+  int my = 0;
+  if (r.force_balance) {
+    my = lane < r.K ? (int)(((int64_t)t * r.K + lane) % r.E) : 0;
+  } else {
+    uint32_t k[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = s_key[lane + 32 * j];
+#pragma unroll 1
+    for (int i = 0; i < min(r.K + 1, r.E); ++i) {
+      const uint32_t best = __reduce_max_sync(FULL, max(max(max(k[0], k[1]), max(k[2], k[3])),
+                                                        max(max(k[4], k[5]), max(k[6], k[7]))));
+      unsigned at = 256u;
+#pragma unroll
+      for (int j = 7; j >= 0; --j)
+        if (k[j] == best) at = lane + 32 * j;
+      at = __reduce_min_sync(FULL, at);
+      if (lane == i) my = (int)at;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at == lane + 32 * j) k[j] = 0u;
+    }
+  }
+  if (lane < r.K) s_sel[lane] = my;
+  __syncwarp();
+  const int before = __shfl_up_sync(FULL, my, 1);
   bool close = false;  // sigmoid: two of the best K + 1 keys within their error bound
   if (sig && !r.force_balance && lane >= 1 && lane < min(r.K + 1, r.E)) {
-    const float prev = from_sortable_key(s_key[s_sel[lane - 1]]), cur = from_sortable_key(s_key[my]);
+    const float prev = from_sortable_key(s_key[before]), cur = from_sortable_key(s_key[my]);
     close = !(prev - cur > 4e-6f * (1.f + fabsf(prev) + fabsf(cur)));
   }
   if (__any_sync(FULL, close)) {
@@ -576,6 +588,22 @@ __device__ __forceinline__ void few_combine(const FewParams& p, const FewCtl& ct
   }
 }
 
+// The shared expert's weights are known before the selection: the blocks ask for
+// them together (16 KB a request, one thread), up to about what HBM delivers until
+// the selection and the list are there (one token of 256 experts, MXFP4, 51.5 us
+// without, 51.1 so; five, bf16, 407.5 and 405.3, 409 with 40 MB).
+constexpr int64_t kPrefetchBytes = 20 << 20;
+constexpr int kPrefetchChunk = 16384;
+MOE_D void few_prefetch(const void* base, int64_t bytes, int64_t& room) {
+  bytes = min(bytes, room);
+  room -= bytes;
+  for (int64_t at = (int64_t)blockIdx.x * kPrefetchChunk; at + kPrefetchChunk <= bytes;
+       at += (int64_t)gridDim.x * kPrefetchChunk)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const uint8_t*>(base) + at),
+                 "r"(kPrefetchChunk)
+                 : "memory");
+}
+
 template <class L>
 __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constant__ FewParams p) {
   // (the ring's offset, not a rounded pointer: the compiler must see that its loads
@@ -604,7 +632,12 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     for (const CUtensorMap* m : {&p.w1, &p.w2, &p.x, &p.act}) tc::prefetch_tensormap(m);
   }
   for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[0][e] = ctl.mask[1][e] = 0u;
-  pdl_wait();  // the selection, and with it the cleared counters and the fp16 tokens
+  if (cf.n_shared && threadIdx.x == 32 * (L::NW + 1)) {
+    int64_t room = kPrefetchBytes;
+    few_prefetch(p.a.w1.ws, (int64_t)(glu ? 2 : 1) * cf.F * cf.h * 2, room);
+    few_prefetch(p.a.w2.ws, (int64_t)cf.F * cf.h * 2, room);
+  }
+  pdl_wait();  // the selection, and with it the cleared counters
   int32_t* claim = p.sync;
   // the first unit's number comes while the list is made
   const int first_claim = threadIdx.x == 32 * L::NW ? atomicAdd(claim, 1) : 0;
@@ -1049,6 +1082,13 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
     tc::tmem_relinquish();
   }
   for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[0][e] = ctl.mask[1][e] = 0u;
+  if (cf.n_shared && threadIdx.x == 32 * 3) {
+    int64_t room = kPrefetchBytes;
+    few_prefetch(p.a.w1.ws, (int64_t)cf.F * cf.h, room);
+    few_prefetch(p.a.w2.ws, (int64_t)cf.F * cf.h / 2, room);
+    few_prefetch(p.a.w1.ws_sf, (int64_t)cf.F * cf.h / 16, room);
+    few_prefetch(p.a.w2.ws_sf, (int64_t)cf.F * cf.h / 32, room);
+  }
   pdl_wait();  // the selection, and with it the cleared counters and the tokens' parts
   int32_t* claim = p.sync;
   const int first_claim = threadIdx.x == 0 ? atomicAdd(claim, 1) : 0;
