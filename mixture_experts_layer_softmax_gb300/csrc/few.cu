@@ -301,7 +301,7 @@ struct FewCtl {
   uint64_t empty[kMaxStages], meet;
   alignas(16) FewStage st[kMaxStages];
   int abort;
-  int pairs, units1, units2, fc2_writers;
+  int entries, pairs, units1, units2, fc2_writers;
   int ent_e[kMaxEntries];        // expert (E: the shared one)
   int ent_start[kMaxEntries];    // first sorted pair
   int ent_n[kMaxEntries];        // pairs
@@ -428,6 +428,7 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
         const int4 v = c.part[warp];
         before.x += v.x; before.y += v.y; before.z += v.z; before.w += v.w;
       }
+      c.entries = before.x;
       c.pairs = before.y;
       c.cum1[before.x] = c.units1 = before.z * nrb1;
       c.cum2[before.x] = c.units2 = before.z * nrb2 * ksplit;
@@ -452,6 +453,48 @@ __device__ void few_build_list(FewCtl& c, const moe_config_t& cf, int nrb1, int 
   if (cf.n_shared)
     for (int t = threadIdx.x; t < cf.T; t += L::THREADS) c.tok_of[c.start[cf.E] + t] = (uint8_t)t;
   __syncthreads();
+}
+
+// Unit u of the list (FC1's, then FC2's): all of its first stage but the columns,
+// which are kbeg .. kend - 1.  The whole warp calls it: the lanes look for the entry
+// together (one going on from the last unit's entry step by step, with divisions
+// that most lists do without: 64 tokens of 64 experts 54.7 us, so 54.3; one of 256
+// 50.7 and 50.2).  rows1: hidden units of an FC1 unit.
+template <class L>
+MOE_D FewStage few_unit(const FewCtl& c, const moe_config_t& cf, int u, int ksplit, int rows1, int lane,
+                        int& kbeg, int& kend) {
+  FewStage st{};
+  const bool fc1 = u < c.units1;
+  const int v = fc1 ? u : u - c.units1;
+  const int* cum = fc1 ? c.cum1 : c.cum2;
+  int j = -1;
+  for (int i = 0; i < c.entries; i += 32)
+    j += __popc(__ballot_sync(0xffffffffu, i + lane < c.entries && cum[i + lane] <= v));
+  const int n = c.ent_n[j], loc = v - cum[j];
+  int rest = loc, part = 0;  // the unit's rows, its tokens
+  if (n > L::NB) {
+    const int sub = (n + L::NB - 1) / L::NB;
+    rest = loc / sub;
+    part = loc - rest * sub;
+  }
+  st.kind = fc1 ? kFC1 : kFC2;
+  kbeg = 0;
+  kend = fc1 ? cf.h : cf.F;
+  if (fc1) {
+    st.r0 = rest * rows1;
+  } else if (ksplit == 1) {
+    st.r0 = rest * L::RT;
+  } else {
+    st.ks = rest % ksplit;
+    st.r0 = rest / ksplit * L::RT;
+    const int nst = (cf.F + L::KC - 1) / L::KC;
+    kbeg = nst * st.ks / ksplit * L::KC;
+    kend = min(cf.F, nst * (st.ks + 1) / ksplit * L::KC);
+  }
+  st.entry = j;
+  st.n = min(L::NB, n - part * L::NB);
+  st.pos0 = c.ent_start[j] + part * L::NB;
+  return st;
 }
 
 MOE_D int ld_acquire(const int32_t* p) {
@@ -588,12 +631,14 @@ __device__ __forceinline__ void few_combine(const FewParams& p, const FewCtl& ct
   }
 }
 
-// The shared expert's weights are known before the selection: the blocks ask for
-// them together (16 KB a request, one thread), up to about what HBM delivers until
-// the selection and the list are there (one token of 256 experts, MXFP4, 51.5 us
-// without, 51.1 so; five, bf16, 407.5 and 405.3, 409 with 40 MB).
+// Weights that are needed whatever the selection, or nearly so, are asked for before
+// it, by the blocks together (16 KB a request, one thread), up to about what HBM
+// delivers until the list is there: the first experts' when there are twice as many
+// pairs as experts or more (an expert then stays idle once in e^2 at most: 13 tokens,
+// 2 of 8, MXFP4, 122.0 us without, 119.2 so, 118.7 with 40 MB; 32 tokens, bf16, 422.3,
+// 417.0 and 419.2), then the shared one's (five tokens of 256, bf16, 407.5 and 405.3).
 constexpr int64_t kPrefetchBytes = 20 << 20;
-constexpr int kPrefetchChunk = 16384;
+constexpr int kPrefetchChunk = 16384, kPrefetchPairs = 2;
 MOE_D void few_prefetch(const void* base, int64_t bytes, int64_t& room) {
   bytes = min(bytes, room);
   room -= bytes;
@@ -632,8 +677,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     for (const CUtensorMap* m : {&p.w1, &p.w2, &p.x, &p.act}) tc::prefetch_tensormap(m);
   }
   for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[0][e] = ctl.mask[1][e] = 0u;
-  if (cf.n_shared && threadIdx.x == 32 * (L::NW + 1)) {
+  if (threadIdx.x == 32 * (L::NW + 1)) {
     int64_t room = kPrefetchBytes;
+    if (cf.T * cf.K >= kPrefetchPairs * cf.E)
+      few_prefetch(p.a.w1.w, (int64_t)cf.E * (glu ? 2 : 1) * cf.F * cf.h * 2, room);
+    if (!cf.n_shared) room = 0;
     few_prefetch(p.a.w1.ws, (int64_t)(glu ? 2 : 1) * cf.F * cf.h * 2, room);
     few_prefetch(p.a.w2.ws, (int64_t)cf.F * cf.h * 2, room);
   }
@@ -664,7 +712,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     // (as for the tokens, one elected lane of the whole warp issues)
     {
       const bool elected = tc::elect_one();
-      int stage = 0, j1 = 0, j2 = 0;
+      int stage = 0;
       uint32_t phase = 0, issued = 0, issued_par = 0;
       const uint64_t policy = evict_first_policy();
       int next = first_claim;
@@ -678,34 +726,9 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
         int half0 = 0;  // the map's third coordinate
         bool pairs_of_rows = false;
         if (u < total) {
-          int j;
-          if (u < ctl.units1) {
-            while (ctl.cum1[j1 + 1] <= u) ++j1;
-            j = j1;
-            const int sub = (ctl.ent_n[j] + L::NB - 1) / L::NB, loc = u - ctl.cum1[j];
-            st.kind = kFC1;
-            st.r0 = loc / sub * few_rows1<L>(glu);
-            st.pos0 = loc % sub * L::NB;
-            kend = cf.h;
-            pairs_of_rows = glu;
-          } else {
-            const int u2 = u - ctl.units1;
-            while (ctl.cum2[j2 + 1] <= u2) ++j2;
-            j = j2;
-            const int sub = (ctl.ent_n[j] + L::NB - 1) / L::NB, loc = u2 - ctl.cum2[j];
-            const int rest = loc / sub;
-            st.kind = kFC2;
-            st.ks = rest % p.ksplit;
-            st.r0 = rest / p.ksplit * L::RT;
-            st.pos0 = loc % sub * L::NB;
-            const int nst = (cf.F + L::KC - 1) / L::KC;
-            kbeg = nst * st.ks / p.ksplit * L::KC;
-            kend = min(cf.F, nst * (st.ks + 1) / p.ksplit * L::KC);
-          }
-          st.entry = j;
-          st.n = min(L::NB, ctl.ent_n[j] - st.pos0);
-          st.pos0 += ctl.ent_start[j];
-          const int e = ctl.ent_e[j];
+          st = few_unit<L>(ctl, cf, u, p.ksplit, few_rows1<L>(glu), lane, kbeg, kend);
+          pairs_of_rows = glu && st.kind == kFC1;
+          const int e = ctl.ent_e[st.entry];
           const bool shared = e == cf.E;
           map = st.kind == kFC1 ? (shared ? &p.w1s : &p.w1) : (shared ? &p.w2s : &p.w2);
           half0 = shared ? 0 : e * (pairs_of_rows ? 2 : 1);
@@ -1082,8 +1105,13 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
     tc::tmem_relinquish();
   }
   for (int e = threadIdx.x; e < kMaxEntries; e += L::THREADS) ctl.mask[0][e] = ctl.mask[1][e] = 0u;
-  if (cf.n_shared && threadIdx.x == 32 * 3) {
+  if (threadIdx.x == 32 * 3) {
     int64_t room = kPrefetchBytes;
+    if (cf.T * cf.K >= kPrefetchPairs * cf.E) {
+      few_prefetch(p.a.w1.sf, (int64_t)cf.E * cf.F * cf.h / 16, room);
+      few_prefetch(p.a.w1.w, (int64_t)cf.E * cf.F * cf.h, room);
+    }
+    if (!cf.n_shared) room = 0;
     few_prefetch(p.a.w1.ws, (int64_t)cf.F * cf.h, room);
     few_prefetch(p.a.w2.ws, (int64_t)cf.F * cf.h / 2, room);
     few_prefetch(p.a.w1.ws_sf, (int64_t)cf.F * cf.h / 16, room);
@@ -1129,7 +1157,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
 
   if (warp == 0) {
     // ================= weights =================
-    int j1 = 0, j2 = 0, next = first_claim;
+    int next = first_claim;
     const uint64_t policy = evict_first_policy();
     bool ok = true;
     while (ok) {
@@ -1140,39 +1168,13 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
       const CUtensorMap* map = nullptr;
       const uint8_t *sf0 = nullptr, *sf1 = nullptr;  // scales of the rows, of the up rows
       if (u < total) {
-        int j, cols;
-        if (u < ctl.units1) {
-          while (ctl.cum1[j1 + 1] <= u) ++j1;
-          j = j1;
-          const int sub = (ctl.ent_n[j] + L::NB - 1) / L::NB, loc = u - ctl.cum1[j];
-          st.kind = kFC1;
-          st.r0 = loc / sub * (L::RT / 2);
-          st.pos0 = loc % sub * L::NB;
-          kend = cols = cf.h;
-        } else {
-          const int u2 = u - ctl.units1;
-          while (ctl.cum2[j2 + 1] <= u2) ++j2;
-          j = j2;
-          const int sub = (ctl.ent_n[j] + L::NB - 1) / L::NB, loc = u2 - ctl.cum2[j];
-          const int rest = loc / sub;
-          st.kind = kFC2;
-          st.ks = rest % p.ksplit;
-          st.r0 = rest / p.ksplit * L::RT;
-          st.pos0 = loc % sub * L::NB;
-          cols = cf.F;
-          const int nst = (cf.F + L::KC - 1) / L::KC;
-          kbeg = nst * st.ks / p.ksplit * L::KC;
-          kend = min(cf.F, nst * (st.ks + 1) / p.ksplit * L::KC);
-        }
-        st.entry = j;
-        st.n = min(L::NB, ctl.ent_n[j] - st.pos0);
-        st.pos0 += ctl.ent_start[j];
-        const int e = ctl.ent_e[j];
+        st = few_unit<L>(ctl, cf, u, p.ksplit, L::RT / 2, lane, kbeg, kend);
+        const int e = ctl.ent_e[st.entry];
         const bool shared = e == cf.E, fc1 = st.kind == kFC1;
         map = fc1 ? (shared ? &p.w1s : &p.w1) : (shared ? &p.w2s : &p.w2);
         half0 = shared ? 0 : e * (fc1 ? 2 : 1);
         const FewWeights& W = fc1 ? p.a.w1 : p.a.w2;
-        const int64_t row_atoms = cols / 128;
+        const int64_t row_atoms = (fc1 ? cf.h : cf.F) / 128;
         const uint8_t* sf = shared ? W.ws_sf
                                    : W.sf + (int64_t)e * ((fc1 ? 2 * cf.F : cf.h) / 128) * row_atoms * mx::ATOM;
         sf0 = sf + st.r0 / 128 * row_atoms * mx::ATOM;
