@@ -109,11 +109,12 @@ __device__ void few_split_token(const __nv_bfloat16* __restrict__ x, int h, int 
 }
 
 // ---- route ----------------------------------------------------------------------
-// Partial logits: one warp per (expert, slice of h), eight tokens at a time.
-// x is exact in fp32 and the products and sums are fp32, each lane over its
-// own columns, the lanes added as a tree.  The blocks past the router's convert
-// one token each; block 0 clears the counters of few_kernel.
-constexpr int kRouteTok = 8, kSplitCols = 1024;
+// Partial logits: one warp per (expert, slice of h, TOK tokens).  x is exact in
+// fp32 and the products and sums are fp32, each lane over its own columns, the
+// lanes added as a tree.  The blocks past the router's split kSplitCols columns of
+// a token each; block 0 clears the counters of few_kernel.
+constexpr int kSplitCols = 1024;
+template <int TOK>
 __global__ void __launch_bounds__(256)
     few_router_kernel(const __nv_bfloat16* __restrict__ x, const float* __restrict__ w_r, int T,
                       int E, int h, int kparts, float* __restrict__ parts, int route_blocks,
@@ -128,21 +129,20 @@ __global__ void __launch_bounds__(256)
                     xq + (int64_t)t * kParts * (h / 2), xs + (int64_t)t * kParts * (h / 32));
     return;
   }
-  // one warp per (expert, slice, eight tokens)
   const int unit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (unit >= E * kparts * (int)ceil_div(T, kRouteTok)) return;
-  const int e = unit % E, part = unit / E % kparts, t0 = unit / (E * kparts) * kRouteTok;
+  if (unit >= E * kparts * (int)ceil_div(T, TOK)) return;
+  const int e = unit % E, part = unit / E % kparts, t0 = unit / (E * kparts) * TOK;
   const int vecs = h / 8;  // 16-byte vectors of x
   const int v0 = (int)((int64_t)vecs * part / kparts), v1 = (int)((int64_t)vecs * (part + 1) / kparts);
   const float* w = w_r + (int64_t)e * h;
   {
-    float acc[kRouteTok];
+    float acc[TOK];
 #pragma unroll
-    for (int j = 0; j < kRouteTok; ++j) acc[j] = 0.f;
+    for (int j = 0; j < TOK; ++j) acc[j] = 0.f;
     for (int v = v0 + lane; v < v1; v += 32) {
       const Vec<float> wa = ldg16(w + v * 8), wb = ldg16(w + v * 8 + 4);
 #pragma unroll
-      for (int j = 0; j < kRouteTok; ++j) {
+      for (int j = 0; j < TOK; ++j) {
         if (t0 + j >= T) break;
         const Vec<__nv_bfloat16> xv = ldg16(x + (int64_t)(t0 + j) * h + v * 8);
 #pragma unroll
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(256)
       }
     }
 #pragma unroll
-    for (int j = 0; j < kRouteTok; ++j) {
+    for (int j = 0; j < TOK; ++j) {
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
       if (lane == 0 && t0 + j < T) parts[((int64_t)part * T + t0 + j) * E + e] = acc[j];
@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(256)
   __shared__ float s_prob[16];
   const unsigned FULL = 0xffffffffu;
   const int e = threadIdx.x, t = blockIdx.x, lane = threadIdx.x & 31;
+  constexpr int kBatch = 8;
   const bool sig = r.score == MOE_SCORE_SIGMOID;
   pdl_trigger();
   const float gb = gate_bias && e < r.E ? __ldg(gate_bias + e) : 0.f;
@@ -193,8 +194,14 @@ __global__ void __launch_bounds__(256)
   float l = 0.f;
   uint32_t key = 0u;  // order-preserving; 0 past E and for what was picked
   if (e < r.E) {
-#pragma unroll 4
-    for (int p = 0; p < kparts; ++p) l += __ldcg(parts + ((int64_t)p * r.T + t) * r.E + e);
+    for (int p0 = 0; p0 < kparts; p0 += kBatch) {  // all of a batch under way, added in order
+      float v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        v[i] = p0 + i < kparts ? __ldcg(parts + ((int64_t)(p0 + i) * r.T + t) * r.E + e) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) l += v[i];
+    }
     l += gb;
     const float fast = sig ? sigmoid_f(l) : l;  // selection_key_fast
     key = max(sortable_key(r.sel_bias ? __fadd_rn(fast, sb) : fast), 1u);
@@ -1570,8 +1577,16 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   r.sel_bias = a.sel_bias;
   r.topk_idx = const_cast<int32_t*>(p.idx);
   r.topk_prob = const_cast<float*>(p.prob);
-  const int route_blocks = (int)ceil_div((int64_t)c.E * kparts * ceil_div(c.T, kRouteTok), 8);
-  few_router_kernel<<<route_blocks + (mxfp4 ? c.T * (int)ceil_div(c.h, kSplitCols) : 0), 256, 0, s>>>(
+  // Tokens a warp of the router takes: as many as leave 26 warps an SM.  us with 8 / 4 /
+  // 2 / 1 (MXFP4): 64 tokens of 64 experts 54.8 / 55.8 / 56.5 / 59.4, 24 tokens 48.1 /
+  // 46.7 / 46.5 / 47.9, 5 tokens of 256 129.3 / 126.3 / 124.9 / 123.0.
+  auto warps = [&](int tok) { return (int64_t)c.E * kparts * ceil_div(c.T, tok); };
+  int tok = 8;
+  while (tok > 1 && warps(tok) < 26 * 152) tok /= 2;
+  const int route_blocks = (int)ceil_div(warps(tok), 8);
+  auto* route = tok == 1 ? few_router_kernel<1> : tok == 2 ? few_router_kernel<2>
+                : tok == 4 ? few_router_kernel<4> : few_router_kernel<8>;
+  route<<<route_blocks + (mxfp4 ? c.T * (int)ceil_div(c.h, kSplitCols) : 0), 256, 0, s>>>(
       a.x, a.w_r, c.T, c.E, c.h, kparts, parts, route_blocks,
       xq, xs, p.sync, (int)few_sync_words(c));
   cudaError_t e = cudaGetLastError();
