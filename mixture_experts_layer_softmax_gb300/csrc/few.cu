@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 // accumulators in TMEM (two, for two units in turn).  Decoding the codes on the
 // ALUs for m16n8k16 products (tokens in fp16) took 34 warp instructions for 16 x
 // 32 weights: T = 13, 2 of 8 experts / T = 64, 8 of 64 / T = 5, 8 of 256 ran in
-// 156 / 92 / 165 us; this takes 122 / 54 / 129.
+// 156 / 92 / 165 us; this takes 118 / 54 / 124.
 //   warp 0  weights: 128-row boxes of 256 codes and the rows' scale atoms; 512
 //           columns a stage (256 a stage, seven or eight stages: the scale warp's
 //           work a stage bounds it, 161 / 68 / 171 us);

@@ -196,6 +196,9 @@ BF16 = [
     dict(T=12, h=256, E=8, K=2, F=128, force=True),
     dict(T=40, h=256, E=4, K=2, F=128, capacity=7, shared=1),        # drops
     dict(T=50, h=128, E=8, K=2, F=136, capacity=1),
+    dict(T=64, h=1032, E=256, K=8, F=16),                            # a router warp with 8 tokens,
+    dict(T=37, h=1024, E=120, K=4, F=24, score=1),                   # 4
+    dict(T=23, h=2048, E=64, K=8, F=40, sel=True),                   # and 2
 ]
 MX = [
     dict(T=1, h=128, E=8, K=2, F=128),
@@ -304,6 +307,49 @@ def test_side_stream_graphs_and_two_at_once(mx):
     torch.cuda.synchronize()
     assert torch.equal(f.y, want)
     assert M.moe_get_error() == M.MOE_OK
+
+
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E", [8, 64, 256])
+def test_equal_logits_pick_the_lowest_experts(E, score):
+    """Experts with the same router row have the same logit to the bit."""
+    M = lib()
+    f = Few(T=6, h=256, E=E, K=4, F=64, score=score, seed=4)
+    f.w_r[:] = f.w_r[0]
+    f.device(M).call(M)
+    torch.cuda.synchronize()
+    assert (f.idx.cpu() == torch.arange(4, dtype=torch.int32)).all()
+    assert (f.prob == 0.25).all()
+    f = Few(T=6, h=256, E=E, K=4, F=64, score=score, seed=4)
+    f.w_r[E // 2:] = f.w_r[:E - E // 2]              # every expert of the lower half again
+    f.device(M).call(M)
+    torch.cuda.synchronize()
+    idx, half = to_np(f.idx).astype(int), E // 2
+    for row in idx:                                  # a pair's lower one is next to its upper one
+        for k in (0, 2):
+            if row[k] < half:
+                assert row[k + 1] == row[k] + half
+    assert M.moe_get_error() == M.MOE_OK
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_routed_non_finite_tokens(mx):
+    """Tokens whose logits are NaN take some K different experts and stay NaN; the
+    others are as without them."""
+    M = lib()
+    kw = dict(T=9, h=256, E=40, K=5, F=128, mx=mx, seed=3)
+    clean = run(**kw)
+    x = clean.x.copy()
+    x[2, 5], x[6, 100] = np.nan, np.inf
+    f = Few(**dict(kw, x=x)).device(M)
+    f.call(M)
+    torch.cuda.synchronize()
+    assert M.moe_get_error() == M.MOE_OK
+    idx = to_np(f.idx).astype(int)
+    assert all(len(set(r)) == 5 and min(r) >= 0 and max(r) < 40 for r in idx)
+    rest = [0, 1, 3, 4, 5, 7, 8]
+    assert torch.equal(f.y[rest], clean.y[rest]) and torch.equal(f.idx[rest], clean.idx[rest])
+    assert torch.isnan(f.y[2].float()).all()
 
 
 def test_agrees_with_the_layer_pass():
