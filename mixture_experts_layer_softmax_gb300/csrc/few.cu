@@ -330,7 +330,7 @@ struct FewParams {
   const float* prob;
   int pairs_pad;
   int32_t* sync;
-  void* hidden;         // bf16, or E2M1 parts (MXFP4 weights) with
+  void* hidden;         // bf16, HR rows a pair, or E2M1 parts (MXFP4 weights) with
   uint8_t* hidden_s;    // their block scales
   const uint32_t* xs;   // block scales of the tokens' parts
   float* ypart;
@@ -352,7 +352,13 @@ struct FewTile {
   // loads meet in a bank, which the shared-memory bandwidth has room for.
   static constexpr int KB = 256, NKB = KC / KB;
   static constexpr int A_ROW = 512, B_ROW = 512;
-  static constexpr int A_BYTES = NKB * RT * A_ROW, B_BYTES = NKB * NB * B_ROW;
+  // Rows of FC2's hidden values a token: two bf16 numbers a value, the second what the
+  // first left, within 2^-16 of it (with one the result's error is 1.4 times the output
+  // rounding's), where that costs 1 to 2 percent; with 16 tokens a unit it costs 6 (32
+  // tokens, 2 of 8: 414 us, 438 with two), and they keep one, as moe_layer_fwd does.
+  static constexpr int HR = NT == 1 ? 2 : 1;
+  static constexpr int NBR = HR * NB;
+  static constexpr int A_BYTES = NKB * RT * A_ROW, B_BYTES = NKB * NBR * B_ROW;
   static constexpr int STAGE = (A_BYTES + B_BYTES + 1023) / 1024 * 1024;
   static constexpr int RED_TOK = RT + 4;  // padded token stride of the meeting buffer
   static constexpr int REDS = NT > 2 ? 1 : 2;  // meeting buffers (one of them fits beside more tokens)
@@ -815,16 +821,16 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
           for (int i = 0; i < 2 * L::NT; ++i)
             if (i < n4)
               for (int b = 0; b < nkb; ++b)
-                tc::tma_gather4(b_dst + (b * L::NB + 4 * i) * L::B_ROW, &p.x, st.k0 + b * L::KB,
+                tc::tma_gather4(b_dst + (b * L::NBR + 4 * i) * L::B_ROW, &p.x, st.k0 + b * L::KB,
                                 row[i][0], row[i][1], row[i][2], row[i][3], fb);
         }
       } else if (elected) {  // rows of the sorted list: boxes of eight
-        const int n8 = (st.n + 7) / 8;
+        const int n8 = (L::HR * st.n + 7) / 8;
         tc::mbar_arrive_expect_tx(fb, n8 * nkb * 8 * L::B_ROW);
         for (int i = 0; i < n8; ++i)
           for (int b = 0; b < nkb; ++b)
-            tc::tma_load_2d(b_dst + (b * L::NB + 8 * i) * L::B_ROW, &p.act, st.k0 + b * L::KB,
-                            st.pos0 + 8 * i, fb);
+            tc::tma_load_2d(b_dst + (b * L::NBR + 8 * i) * L::B_ROW, &p.act, st.k0 + b * L::KB,
+                            L::HR * st.pos0 + 8 * i, fb);
       }
       __syncwarp();
       issued |= 1u << stage;
@@ -864,9 +870,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     bool finish = false;
     // The stages of one unit, the first of which is there (its weights).  TWO: a
     // SwiGLU FC1 unit, whose m-tiles' upper halves (up rows) lie in a block of
-    // their own.  What does not change from stage to stage is worked out once.
-    auto stages = [&](auto two_c, const FewStage& st) -> bool {
+    // their own.  ROWS: rows a token, which add up in the same sums.
+    // What does not change from stage to stage is worked out once.
+    auto stages = [&](auto two_c, auto rows_c, const FewStage& st) -> bool {
       constexpr bool TWO = decltype(two_c)::value;
+      constexpr int ROWS = decltype(rows_c)::value;
       constexpr int M_STEP = TWO ? 8 : 16, HI = (TWO ? 8 * L::MT : 8) * L::A_ROW;
       const int ntiles = (st.n + 7) >> 3;
       const int m_row = M_STEP * mi + g;
@@ -877,7 +885,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       uint32_t b_off[L::NT];
 #pragma unroll
       for (int n = 0; n < L::NT; ++n)
-        b_off[n] = L::A_BYTES + (k_w / L::KB * L::NB + min(8 * n + g, st.n - 1)) * L::B_ROW +
+        b_off[n] = L::A_BYTES + (k_w / L::KB * L::NBR + ROWS * min(8 * n + g, st.n - 1)) * L::B_ROW +
                    (k_w % L::KB + 8 * q) * 2;
       int kc = st.kc, last = st.last;
       for (;;) {
@@ -887,10 +895,13 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 #pragma unroll
         for (int c = 0; c < L::KW / 32; ++c) {
           if (k_w + c * 32 >= kc) break;  // (the boxes are zero past the matrix)
-          uint4 b[L::NT];
+          uint4 b[ROWS][L::NT];
 #pragma unroll
           for (int n = 0; n < L::NT; ++n)
-            if (L::NT == 1 || n < ntiles) b[n] = lds128(base + b_off[n] + c * 64);
+            if (L::NT == 1 || n < ntiles) {
+#pragma unroll
+              for (int r = 0; r < ROWS; ++r) b[r][n] = lds128(base + b_off[n] + r * L::B_ROW + c * 64);
+            }
 #pragma unroll
           for (int m = 0; m < L::MPW; ++m) {
             const uint4 lo = lds128(a_at + m * M_STEP * L::A_ROW + c * 64);
@@ -898,8 +909,11 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 #pragma unroll
             for (int n = 0; n < L::NT; ++n)
               if (L::NT == 1 || n < ntiles) {
-                mma16816(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[n].x, b[n].y);
-                mma16816(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[n].z, b[n].w);
+#pragma unroll
+                for (int r = ROWS - 1; r >= 0; --r) {
+                  mma16816(acc[m][n], lo.x, hi.x, lo.y, hi.y, b[r][n].x, b[r][n].y);
+                  mma16816(acc[m][n], lo.z, hi.z, lo.w, hi.w, b[r][n].z, b[r][n].w);
+                }
               }
           }
         }
@@ -918,8 +932,10 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       const FewStage st = ctl.st[stage];
       if (st.kind == kEnd) { finish = true; break; }
       bool done_all;
-      if (glu && st.kind == kFC1) done_all = stages(std::true_type{}, st);
-      else done_all = stages(std::false_type{}, st);
+      using One = std::integral_constant<int, 1>;
+      if (st.kind == kFC2) done_all = stages(std::false_type{}, std::integral_constant<int, L::HR>{}, st);
+      else if (glu) done_all = stages(std::true_type{}, One{}, st);
+      else done_all = stages(std::false_type{}, One{}, st);
       if (!done_all) break;
       const int ntiles = (st.n + 7) >> 3;
 
@@ -974,9 +990,15 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
             if (cf.has_bias && e < cf.E && valid) z += to_f32(p.a.b1[(int64_t)e * cf.F + st.r0 + f]);
             v = gelu_f(z);
           }
-          const int64_t at = (int64_t)pos * cf.F + st.r0 + f;
-          // bf16, as moe_layer_fwd keeps them: FC2's operand type
-          if (valid) static_cast<__nv_bfloat16*>(p.hidden)[at] = __float2bfloat16_rn(v);
+          if (valid) {
+            __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.hidden) + (int64_t)pos * L::HR * cf.F + st.r0 + f;
+            const __nv_bfloat16 first = __float2bfloat16_rn(v);
+            at[0] = first;
+            if (L::HR == 2) {
+              const float left = v - to_f32(first);
+              at[cf.F] = __float2bfloat16_rn(isfinite(left) ? left : 0.f);
+            }
+          }
         }
         fence_proxy_async_global();
         __syncwarp();
@@ -1543,7 +1565,7 @@ cudaError_t few_launch(FewParams& p, cudaStream_t s) {
     ok = ok && weights(&p.w1s, p.a.w1.ws, c.h, c.F, pair, pair) &&
          weights(&p.w2s, p.a.w2.ws, c.F, c.h, 1, 1);
   ok = ok && few_encode(&p.x, u16, 2, p.a.x, 2, c.h, c.T, 1, L::KB, 1, 1, false) &&
-       few_encode(&p.act, u16, 2, p.hidden, 2, c.F, p.S, 1, L::KB, 8, 1, false);
+       few_encode(&p.act, u16, 2, p.hidden, 2, c.F, (uint64_t)L::HR * p.S, 1, L::KB, 8, 1, false);
   if (!ok) return cudaErrorInvalidValue;
   return few_launch_ring(few_kernel<L>, L::THREADS, L::STAGE, kMaxStages, L::RED + (int)sizeof(FewCtl), p, s);
 }

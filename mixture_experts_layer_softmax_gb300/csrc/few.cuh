@@ -62,7 +62,7 @@ inline FewLayout few_layout(const moe_config_t& c) {
   w.prob = take((size_t)kFewCopies * few_pairs_pad(c) * 4);
   w.xq = take(T * c.h * 2);        // tokens in four E2M1 parts (MXFP4 weights)
   w.xs = take(T * ceil_div(c.h, 32) * 4);  // and their block scales
-  w.a = take(S * c.F * 2);         // hidden values: bf16, or parts
+  w.a = take(S * c.F * 4);         // hidden values: one or two bf16 numbers each, or parts
   w.as = take(S * ceil_div(c.F, 32) * 4);  // and their block scales
   w.ypart = take((size_t)few_ksplit(c) * S * c.h * 4);
   w.total = off;

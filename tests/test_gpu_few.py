@@ -3,8 +3,9 @@ few tokens) against the float64 oracle.
 
 Tolerance of y, from the roundings on the way (all sums fp32, u = 2^-23 an
 addition, of n terms n u sum|terms|): FC1's sums, carried through the
-activation (|phi'| <= 1.13; the expert's hidden values are then rounded to bf16,
-at most half a step, 2^-8 |a|), FC2's sums, p (relative 2^-18, the router's logits
+activation (|phi'| <= 1.13; the expert's hidden values are then two bf16 numbers,
+the second what the first left: at most 2^-8 2^-8 |a|; with many tokens an expert
+one number, 2^-8 |a|), FC2's sums, p (relative 2^-18, the router's logits
 included) and the bf16 y, 2^-8 |y|.  The bound is evaluated per element from the
 absolute values of the same products.  Beside MXFP4 weights tokens and hidden
 values are sums of four E2M1 blocks of 32 columns: part 0 rounds to steps of at
@@ -119,7 +120,8 @@ class Few:
         else:
             a, da = O.gelu(z), 1.13 * dz
         da = da + 2.0 ** -18 * (np.abs(a) + da)
-        da = da + (parts(np.abs(a) + da) if self.mx else 2.0 ** -8 * (np.abs(a) + da))
+        many = self.T > 8 and self.T * self.K > 4 * self.E
+        da = da + (parts(np.abs(a) + da) if self.mx else 2.0 ** (-8 if many else -16) * (np.abs(a) + da))
         o = a @ w2.T + (0 if b2 is None else b2)
         S = np.abs(a) @ np.abs(w2).T
         return o, da @ np.abs(w2).T + F * U * S
