@@ -61,8 +61,10 @@ MOE_D void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: 
 // left.  There E2M1's steps are at most 1, so part 0 leaves at most s / 2; at s / 4
 // that is at most 2, steps of 1/2, and from then on every part takes three bits: the
 // four leave at most s / 1024, 2^-11 of the block's largest value (a bf16 number's
-// own half step is 2^-8 of it).  A block with an infinity or a NaN gets the NaN
-// scale.  code[i]: the lane's four codes of part i, the first lowest.
+// own half step is 2^-8 of it), or 2^-129 where the scales end at 2^-127.  What a part
+// leaves is kept in units of that part's scale, where every difference is exact and none
+// overflows (4 s is infinite for a block above 3.5 2^126).  A block with an infinity or
+// a NaN gets the NaN scale.  code[i]: the lane's four codes of part i, the first lowest.
 constexpr int kParts = 4;
 MOE_D void e2m1_parts(float (&v)[4], uint32_t (&code)[kParts], uint32_t (&scale)[kParts]) {
   uint32_t m = 0u;
@@ -71,22 +73,27 @@ MOE_D void e2m1_parts(float (&v)[4], uint32_t (&code)[kParts], uint32_t (&scale)
 #pragma unroll
   for (int o = 4; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const int e = (int)(m >> 23);
+  int x = max(e - 1, 0);
+  const float inv = __uint_as_float((uint32_t)(254 - x) << 23);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] *= inv;
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
-    const int x = max(e - 1 - (i == 0 ? 0 : 3 * i - 1), 0);
     scale[i] = e == 255 ? (i == 0 ? 255u : 0u) : (uint32_t)x;
-    const float inv = __uint_as_float((254u - x) << 23), one = mx::e8m0_value((uint32_t)x);
     uint32_t c = 0u;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      c |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * j] * inv, v[2 * j + 1] * inv), __NV_E2M1,
+      c |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * j], v[2 * j + 1]), __NV_E2M1,
                                               cudaRoundNearest) << (8 * j);
     code[i] = e == 255 ? 0u : c;
+    const int next = max(e - 1 - (3 * i + 2), 0);
+    const float up = __uint_as_float((uint32_t)(127 + x - next) << 23);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t b = c >> (4 * j);
-      v[j] -= __uint_as_float((b & 8u) << 28 | (b & 7u) << 22) * 0x1p126f * one;
+      v[j] = (v[j] - __uint_as_float((b & 8u) << 28 | (b & 7u) << 22) * 0x1p126f) * up;
     }
+    x = next;
   }
 }
 
