@@ -381,8 +381,7 @@ moe_status_t moe_layer_fwd(const moe_config_t* cfg, const void* x, const float* 
  * bf16 configurations without SAVE_FOR_BWD and without loss weights (else
  * MOE_ERR_UNSUPPORTED, as for T > 64 and for sizes whose units of work do not
  * fit 31 bits).  p is applied to the expert's output in fp32; the expert's
- * hidden values are kept as sums of two bf16 numbers, within 2^-16 of them, or
- * (T > 8 and T K > 4 E: many tokens an expert) in bf16, as in moe_layer_fwd.
+ * hidden values are kept as sums of two bf16 numbers, within 2^-16 of them.
  * Results may differ from moe_layer_fwd's in the last bits (the fp32 sums have
  * other orders).  Bitwise
  * reproducible.  MOE_FLAG_GEMM_* and MOE_FLAG_HIST_FROM_ROUTER have no effect.

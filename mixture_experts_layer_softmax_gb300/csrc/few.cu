@@ -337,7 +337,7 @@ struct FewParams {
   const float* prob;
   int pairs_pad;
   int32_t* sync;
-  void* hidden;         // bf16, HR rows a pair, or E2M1 parts (MXFP4 weights) with
+  void* hidden;         // bf16, two rows a pair, or E2M1 parts (MXFP4 weights) with
   uint8_t* hidden_s;    // their block scales
   const uint32_t* xs;   // block scales of the tokens' parts
   float* ypart;
@@ -361,14 +361,16 @@ struct FewTile {
   static constexpr int A_ROW = 512, B_ROW = 512;
   // Rows of FC2's hidden values a token: two bf16 numbers a value, the second what the
   // first left, within 2^-16 of it (with one the result's error is 1.4 times the output
-  // rounding's), where that costs 1 to 2 percent; with 16 tokens a unit it costs 6 (32
-  // tokens, 2 of 8: 414 us, 438 with two), and they keep one, as moe_layer_fwd does.
-  static constexpr int HR = NT == 1 ? 2 : 1;
+  // rounding's).  They cost 1 to 2 percent with 8 tokens a unit and 4 with 16 (32 tokens,
+  // 2 of 8: 425 us with one number, 444 with two).
+  static constexpr int HR = 2;
   static constexpr int NBR = HR * NB;
   static constexpr int A_BYTES = NKB * RT * A_ROW, B_BYTES = NKB * NBR * B_ROW;
   static constexpr int STAGE = (A_BYTES + B_BYTES + 1023) / 1024 * 1024;
   static constexpr int RED_TOK = RT + 4;  // padded token stride of the meeting buffer
-  static constexpr int REDS = NT > 2 ? 1 : 2;  // meeting buffers (one of them fits beside more tokens)
+  // Meeting buffers: with 16 tokens the second one's place holds a fourth stage
+  // (456 us with two buffers and three stages, 444 so).
+  static constexpr int REDS = NT > 1 ? 1 : 2;
   static constexpr int RED1 = KG * NB * RED_TOK * 4, RED = REDS * RED1;
   static constexpr int THREADS = 32 * (NW + 2);
   // warps that write the results of a unit of n tokens by `width` values
@@ -1001,10 +1003,8 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
             __nv_bfloat16* at = static_cast<__nv_bfloat16*>(p.hidden) + (int64_t)pos * L::HR * cf.F + st.r0 + f;
             const __nv_bfloat16 first = __float2bfloat16_rn(v);
             at[0] = first;
-            if (L::HR == 2) {
-              const float left = v - to_f32(first);
-              at[cf.F] = __float2bfloat16_rn(isfinite(left) ? left : 0.f);
-            }
+            const float left = v - to_f32(first);
+            at[cf.F] = __float2bfloat16_rn(isfinite(left) ? left : 0.f);
           }
         }
         fence_proxy_async_global();

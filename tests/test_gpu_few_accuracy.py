@@ -2,15 +2,17 @@
 oracle where the ordinary tokens of test_gpu_few.py cannot tell.
 
 The bound of an element is that of test_gpu_few.py, from the absolute values of
-the same products, with what E2M1 parts leave as PARTS of a block's largest value
-or 2^-129, whichever is more: the scales end at 2^-127, and a last part there
-rounds to steps of 1/2."""
+the same products: the hidden values beside bf16 weights are two bf16 numbers, the
+second what the first (half a step, 2^-8) left, so within 2^-16, however many tokens
+an expert has; what E2M1 parts leave is PARTS of a block's largest value or 2^-129,
+whichever is more: the scales end at 2^-127, and a last part there rounds to steps of
+1/2."""
 
 import numpy as np
 import pytest
 import torch
 
-from gpu_util import lib, needs_gpu
+from gpu_util import lib, needs_gpu, to_np
 from oracle import moe_oracle as O
 from oracle import mxfp4_oracle as X4
 from test_gpu_few import U, Few, bf16
@@ -27,21 +29,35 @@ def left(v):
 
 
 class Case(Few):
-    """SwiGLU experts without biases."""
-
     def expert(self, x, w1, w2, b1, b2):
         F, h = self.F, self.h
-        z = x @ w1.T
-        dz = h * U * (np.abs(x) @ np.abs(w1).T)
+        z = x @ w1.T + (0 if b1 is None else b1)
+        dz = h * U * (np.abs(x) @ np.abs(w1).T + (0 if b1 is None else np.abs(b1)))
         if self.mx:
             dz = dz + left(x) @ np.abs(w1).T
-        g, u, dg, du = z[:, :F], z[:, F:], dz[:, :F], dz[:, F:]
-        a = O.silu(g) * u
-        da = 1.13 * dg * (np.abs(u) + du) + (np.abs(O.silu(g)) + 1.13 * dg) * du
+        if self.act == 1:
+            g, u, dg, du = z[:, :F], z[:, F:], dz[:, :F], dz[:, F:]
+            a = O.silu(g) * u
+            da = 1.13 * dg * (np.abs(u) + du) + (np.abs(O.silu(g)) + 1.13 * dg) * du
+        else:
+            a, da = O.gelu(z), 1.13 * dz
         da = da + 2.0 ** -18 * (np.abs(a) + da)
-        many = self.T > 8 and self.T * self.K > 4 * self.E
-        da = da + (left(np.abs(a) + da) if self.mx else 2.0 ** (-8 if many else -16) * (np.abs(a) + da))
-        return a @ w2.T, da @ np.abs(w2).T + F * U * (np.abs(a) @ np.abs(w2).T)
+        da = da + (left(np.abs(a) + da) if self.mx else 2.0 ** -16 * (np.abs(a) + da))
+        o = a @ w2.T + (0 if b2 is None else b2)
+        return o, da @ np.abs(w2).T + F * U * (np.abs(a) @ np.abs(w2).T)
+
+    def exact(self):
+        """y in 64 bits for the routing and the weights of it that the call returned."""
+        x, y = self.x.astype(np.float64), np.zeros((self.T, self.h))
+        idx, prob = to_np(self.idx).astype(int), to_np(self.prob).astype(np.float64)
+        m = lambda w, e: None if w is None else w[e].astype(np.float64)  # noqa: E731
+        for e in np.unique(idx):
+            t, k = np.nonzero(idx == e)
+            o = self.expert(x[t], m(self.w1, e), m(self.w2, e), m(self.b1, e), m(self.b2, e))[0]
+            y[t] += prob[t, k][:, None] * o
+        if self.shared:
+            y += self.expert(x, self.w1s.astype(np.float64), self.w2s.astype(np.float64), None, None)[0]
+        return y
 
     def set_w1(self, w1):
         """First projections with these values (to bf16, then to MXFP4 where that is used)."""
@@ -58,6 +74,23 @@ def checked(f):
     torch.cuda.synchronize()
     assert M.moe_get_error() == M.MOE_OK
     f.check(M)
+    return f
+
+
+def only_the_output_rounding(f):
+    """The error as a whole is that of rounding y to bf16.  Steps are 2^-7 of y's power
+    of two, and rounding errors spread evenly over a step, so their squares' mean is
+    step^2 / 12; over n elements the norm scatters by 0.45 / sqrt(n / 2) of itself (n of
+    thousands here, the steps differing in size), and 1.05 is several times that.  The
+    fp32 sums and the tokens' and hidden values' representation have to vanish beside it:
+    2^-16 of the hidden values is 1/150 of the bf16 rounding, hidden values of one bf16
+    number make the ratio 1.4."""
+    y = f.exact()
+    step = np.exp2(np.floor(np.log2(np.abs(y) + 1e-300)) - 7)
+    err = to_np(f.y).astype(np.float64) - y
+    assert y.size >= 4096
+    assert np.linalg.norm(err) <= 1.05 * np.sqrt((step ** 2).sum() / 12), \
+        np.linalg.norm(err) / np.sqrt((step ** 2).sum() / 12)
 
 
 def ends(x_exp, w_exp, mx):
@@ -90,3 +123,39 @@ def test_tokens_near_the_smallest_numbers(mx):
     f.x[2] = 0.0
     f.x[3, 1::2] = bf16(2.0 ** -133)
     checked(f)
+
+
+FEW = [
+    dict(T=8, h=1032, E=8, K=2, F=512, shared=1),
+    dict(T=5, h=1024, E=256, K=8, F=136, score=1, sel=True, shared=1),
+]
+MANY = [  # more than four tokens an expert: units of 16 tokens
+    dict(T=9, h=512, E=1, K=1, F=520),
+    dict(T=16, h=1024, E=4, K=2, F=512, shared=1),
+    dict(T=33, h=640, E=2, K=1, F=384),
+    dict(T=64, h=512, E=1, K=1, F=256, shared=1),
+    dict(T=40, h=264, E=5, K=3, F=1000, act=0, bias=True),
+    dict(T=47, h=136, E=9, K=4, F=5008),
+]
+
+
+def _id(c):
+    return f"T{c['T']}_E{c['E']}_F{c['F']}"
+
+
+@pytest.mark.parametrize("c", FEW + MANY, ids=_id)
+def test_bf16_weights_leave_the_output_rounding(c):
+    only_the_output_rounding(checked(Case(**c)))
+
+
+def test_a_token_has_one_error_whatever_the_batch():
+    """Eight tokens of one expert in a unit of 8, and with a ninth in a unit of 16: the
+    rows differ by their fp32 sums' orders alone, some 2^-20 of the result, and that moves
+    an element to the next bf16 number in about one case in 2^12 (2^-20 beside a step of
+    2^-8); rounding the hidden values otherwise, by 2^-9, would move every third one."""
+    nine = Case(T=9, h=512, E=1, K=1, F=384)
+    checked(nine)
+    eight = Case(T=8, h=512, E=1, K=1, F=384, x=nine.x[:8])
+    eight.w_r, eight.w1, eight.w2 = nine.w_r, nine.w1, nine.w2
+    checked(eight)
+    assert (eight.y != nine.y[:8]).float().mean() < 0.02
