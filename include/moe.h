@@ -399,7 +399,7 @@ moe_status_t moe_layer_fwd_few(const moe_config_t* cfg, const void* x, const flo
  * W1 [E*2F, h] in uniform groups of 2F rows, W2 [E*h, F] in uniform groups of
  * h rows, the shared expert's as one group).  The products run as block-scaled
  * tensor-core MMAs on the weights' exact values; tokens and hidden values enter
- * as sums of four E2M1 blocks of 32 columns, which are within 2^-11 of the
+ * as sums of six E2M1 blocks of 32 columns, which are within 2^-17 of the
  * block's largest magnitude of them (bf16's own half step is 2^-8 of a value),
  * or within 2^-129 where that is more.
  * A block of them that holds an infinity or a NaN counts as NaNs.  SwiGLU experts

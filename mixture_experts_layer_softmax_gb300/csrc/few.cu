@@ -59,13 +59,12 @@ MOE_D void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: 
 // each with a scale of its own: part 0 rounds v / s, s the power of two that puts
 // the largest magnitude into [2, 4), and each further part what the ones before
 // left.  There E2M1's steps are at most 1, so part 0 leaves at most s / 2; at s / 4
-// that is at most 2, steps of 1/2, and from then on every part takes three bits: the
-// four leave at most s / 1024, 2^-11 of the block's largest value (a bf16 number's
-// own half step is 2^-8 of it), or 2^-129 where the scales end at 2^-127.  What a part
-// leaves is kept in units of that part's scale, where every difference is exact and none
-// overflows (4 s is infinite for a block above 3.5 2^126).  A block with an infinity or
-// a NaN gets the NaN scale.  code[i]: the lane's four codes of part i, the first lowest.
-constexpr int kParts = 4;
+// that is at most 2, steps of 1/2, and from then on every part takes three bits: six
+// leave at most s / 65536, 2^-17 of the block's largest value (a bf16 number's own half
+// step is 2^-8 of it), or 2^-129 where the scales end at 2^-127.  What a part leaves is
+// kept in units of that part's scale, where every difference is exact and none overflows
+// (4 s is infinite for a block above 3.5 2^126).  A block with an infinity or a NaN gets
+// the NaN scale.  code[i]: the lane's four codes of part i, the first lowest.
 MOE_D void e2m1_parts(float (&v)[4], uint32_t (&code)[kParts], uint32_t (&scale)[kParts]) {
   uint32_t m = 0u;
 #pragma unroll
@@ -1038,7 +1037,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 // The same units, list, counter and order as few_kernel, the products on the
 // 5th-generation tensor cores: tcgen05.mma kind::mxf4, 128 weight rows as M
 // (FC1: 64 gate rows and the matching 64 up rows), the tokens' E2M1 parts as N
-// (four rows a token), the block scales of both operands applied by the MMA, fp32
+// (six rows a token), the block scales of both operands applied by the MMA, fp32
 // accumulators in TMEM (two, for two units in turn).  Decoding the codes on the
 // ALUs for m16n8k16 products (tokens in fp16) took 34 warp instructions for 16 x
 // 32 weights: T = 13, 2 of 8 experts / T = 64, 8 of 64 / T = 5, 8 of 256 ran in
@@ -1065,7 +1064,7 @@ struct FewMxTile {
   static constexpr int EX = NB * 64, EX_BYTES = 2 * 2 * EX * 4;  // gate and up, two units in turn
   static constexpr int TOKEN_WARPS = 3;  // warps 2, 8 and 9
   static constexpr int THREADS = 320;
-  static constexpr uint32_t ACC = 64, SF_COL0 = 128, SF_COLS = 8 * NKA, TMEM = 256;  // TMEM columns
+  static constexpr uint32_t ACC = 128, SF_COL0 = 256, SF_COLS = 8 * NKA, TMEM = 512;  // TMEM columns
   static constexpr int MAX_STAGES = (TMEM - SF_COL0) / SF_COLS;
   static MOE_HD int writers(int n, int) { return n > 0 ? 4 : 0; }
   static_assert(N <= (int)ACC && STAGE % 1024 == 0 && SFA % 128 == 0, "TMEM columns, swizzle alignment");

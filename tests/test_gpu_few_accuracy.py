@@ -19,7 +19,7 @@ from test_gpu_few import U, Few, bf16
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
 
-PARTS = 2.0 ** -11   # four parts
+PARTS = 2.0 ** -17   # six parts, three bits each
 
 
 def left(v):
@@ -84,7 +84,8 @@ def only_the_output_rounding(f):
     thousands here, the steps differing in size), and 1.05 is several times that.  The
     fp32 sums and the tokens' and hidden values' representation have to vanish beside it:
     2^-16 of the hidden values is 1/150 of the bf16 rounding, hidden values of one bf16
-    number make the ratio 1.4."""
+    number make the ratio 1.4; four E2M1 parts of tokens and hidden values make it 1.15,
+    six leave an error 64 times smaller."""
     y = f.exact()
     step = np.exp2(np.floor(np.log2(np.abs(y) + 1e-300)) - 7)
     err = to_np(f.y).astype(np.float64) - y
@@ -146,6 +147,35 @@ def _id(c):
 @pytest.mark.parametrize("c", FEW + MANY, ids=_id)
 def test_bf16_weights_leave_the_output_rounding(c):
     only_the_output_rounding(checked(Case(**c)))
+
+
+MX = [
+    dict(T=1, h=4096, E=4, K=2, F=256),
+    dict(T=5, h=1152, E=256, K=8, F=128, score=1, sel=True, shared=1),
+    dict(T=8, h=1024, E=1, K=1, F=640),
+    dict(T=13, h=512, E=8, K=2, F=1024, gate=True),
+    dict(T=33, h=384, E=3, K=2, F=256, renorm=False),
+    dict(T=64, h=256, E=2, K=2, F=512, shared=1),
+]
+
+
+@pytest.mark.parametrize("c", MX, ids=_id)
+def test_mxfp4_weights_leave_the_output_rounding(c):
+    only_the_output_rounding(checked(Case(mx=True, **c)))
+
+
+@pytest.mark.parametrize("T", [6, 30])
+def test_what_stands_beside_an_outlier_in_a_block(T):
+    """A value of 100 in one of a token's 32 blocks, which meets zero weights: the
+    result is that of the other values, and what six parts leave of those 31
+    (2^-17 100 = 1/1300 at most, in a 32nd of the products) is a thirtieth of the
+    output rounding; 2^-11 100 would be twice that rounding."""
+    f = Case(T=T, h=1024, E=2, K=1, F=256, mx=True)
+    f.x[:, 40] = 100.0
+    w1 = f.w1_bf16.copy()
+    w1[:, :, 40] = 0.0
+    f.set_w1(w1)
+    only_the_output_rounding(checked(f))
 
 
 def test_a_token_has_one_error_whatever_the_batch():
