@@ -130,7 +130,9 @@ int32_t moe_expert_capacity(int32_t T, int32_t K, int32_t E, float capacity_fact
                             int32_t min_capacity);
 
 /* Bytes of workspace every call below needs for `cfg` (the same figure for
- * all of them; it grows with MOE_FLAG_SAVE_FOR_BWD).  0 if cfg is invalid. */
+ * all of them; it grows with MOE_FLAG_SAVE_FOR_BWD).  It does not shrink as T
+ * grows: a workspace sized for the largest batch serves every smaller one, the
+ * few-token calls among them.  0 if cfg is invalid. */
 size_t moe_workspace_size(const moe_config_t* cfg);
 
 /* Route (review §2.2 "Gating" and "Top-k selection"; §5.1 keeps the router

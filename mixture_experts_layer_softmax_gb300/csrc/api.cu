@@ -178,14 +178,19 @@ moe_status_t check_config(const moe_config_t* c) {
 }
 
 // Workspace bytes of a valid config, the same for every entry point: the
-// layer's layout, or the few-token call's (laid over it) where that is larger.
+// layer's layout, or the few-token call's (laid over it) where that is larger;
+// beyond kFewMaxT tokens that of a call of kFewMaxT, so that a workspace sized
+// for the largest batch serves every smaller one.
 size_t workspace_bytes(const moe_config_t& c) {
-  const size_t layer = workspace_layout(c).total, few = few_layout(c).total;
+  moe_config_t f = c;
+  if (f.T > kFewMaxT) f.T = kFewMaxT;
+  const size_t layer = workspace_layout(c).total, few = few_layout(f).total;
   return few > layer ? few : layer;
 }
 
+// (A config of more than kFewMaxT tokens has only calls that use the layer's layout.)
 moe_status_t check_ws(const moe_config_t* c, const void* ws, size_t ws_bytes) {
-  const size_t need = workspace_bytes(*c);
+  const size_t need = c->T > kFewMaxT ? workspace_layout(*c).total : workspace_bytes(*c);
   if (need == 0) return MOE_OK;
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return MOE_ERR_INVALID_ARG;
@@ -732,10 +737,7 @@ moe_status_t check_few(const moe_config_t* cfg, const void* x, const float* w_r,
   moe_status_t st = check_config(cfg);
   if (st != MOE_OK) return st;
   const moe_config_t& c = *cfg;
-  if (c.dtype != MOE_BF16 || c.T > kFewMaxT || (c.flags & MOE_FLAG_SAVE_FOR_BWD) ||
-      c.aux_loss_coeff != 0.f || c.z_loss_coeff != 0.f)
-    return MOE_ERR_UNSUPPORTED;
-  if (!few_counts_fit(c)) return MOE_ERR_UNSUPPORTED;
+  if (c.T > kFewMaxT || !few_takes(c)) return MOE_ERR_UNSUPPORTED;
   if (c.T > 0 && (!x || !w_r || !y)) return MOE_ERR_INVALID_ARG;
   if (!al16(x) || !al16(w_r) || !al16(y)) return MOE_ERR_INVALID_ARG;
   return check_ws(cfg, ws, ws_bytes);

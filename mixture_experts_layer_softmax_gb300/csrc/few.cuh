@@ -46,6 +46,12 @@ inline bool few_counts_fit(const moe_config_t& c) {
   return subs * ceil_div(r1, 64) < most && subs * ceil_div(c.h, 64) * few_ksplit(c) < most;
 }
 
+// Whether the few-token calls take the config, but for the number of its tokens.
+inline bool few_takes(const moe_config_t& c) {
+  return c.dtype == MOE_BF16 && !(c.flags & MOE_FLAG_SAVE_FOR_BWD) && c.aux_loss_coeff == 0.f &&
+         c.z_loss_coeff == 0.f && few_counts_fit(c);
+}
+
 struct FewLayout {
   size_t sync, parts, idx, prob, xq, xs, a, as, ypart, total;
 };
@@ -55,7 +61,7 @@ inline size_t few_sync_words(const moe_config_t& c) { return 2 + c.E + 1; }
 
 inline FewLayout few_layout(const moe_config_t& c) {
   FewLayout w{};
-  if (c.T < 1 || c.T > kFewMaxT || c.dtype != MOE_BF16) return w;
+  if (c.T < 1 || c.T > kFewMaxT || !few_takes(c)) return w;
   const size_t T = (size_t)c.T, S = T * c.K + (c.n_shared ? T : 0);
   size_t off = 0;
   auto take = [&](size_t bytes) {
