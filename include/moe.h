@@ -533,6 +533,14 @@ moe_status_t moe_set_stage_events(int32_t pass, void* const* events, int32_t n);
  * moe_get_error.  Never faults or hangs the device. */
 moe_status_t moe_test_bounded_wait(int64_t max_polls, moe_stream_t stream);
 
+/* Test hook for the few-token calls' waits on counts: the next such call that
+ * enqueues work expects one finished result of the first (which = 1) or second
+ * (which = 2) projections more than there are, and its waits give up after 20 ms:
+ * it records MOE_ERR_TIMEOUT and writes no y.  Returns what was pending (-1 if
+ * `which` is out of range); which = 0 clears it.  Never faults or hangs the
+ * device. */
+int32_t moe_test_few_wait_runs_out(int32_t which);
+
 /* Test hook (host-side fault injection, no device involvement): the next n
  * calls that would enqueue GPU work fail as if their first CUDA runtime call
  * had failed -- they return MOE_ERR_CUDA after validating their arguments and

@@ -90,6 +90,8 @@ std::mutex g_dev_mu;
 // Test hook (moe_test_inject_cuda_failure): calls left that must fail as if
 // their first CUDA runtime call had failed.
 std::atomic<int> g_inject_failures{0};
+// Test hook (moe_test_few_wait_runs_out): what the next few-token call waits for in vain.
+std::atomic<int> g_starve_few{0};
 
 // Stage timing (moe_set_stage_events): per host thread and pass, the caller's
 // CUDA events that the layer calls record at their stage boundaries.
@@ -757,6 +759,7 @@ moe_status_t run_few(FewArgs& a, const moe_config_t* cfg, const void* x, const f
   a.idx_out = idx_out; a.prob_out = prob_out;
   a.ws = static_cast<char*>(ws);
   a.status = d->status; a.sms = d->sms;
+  a.starve = g_starve_few.exchange(0);
   return cuda_status(launch_few(a, mxfp4, static_cast<cudaStream_t>(stream)));
 }
 }  // namespace
@@ -1063,6 +1066,11 @@ moe_status_t moe_test_bounded_wait(int64_t max_polls, moe_stream_t stream) {
   if (!d) return MOE_ERR_CUDA;
   return cuda_status(
       launch_bounded_wait_probe(max_polls, d->status, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t moe_test_few_wait_runs_out(int32_t which) {
+  if (which < 0 || which > 2) return -1;
+  return g_starve_few.exchange(which);
 }
 
 }  // extern "C"

@@ -342,6 +342,7 @@ struct FewParams {
   float* ypart;
   int S;            // rows of act and ypart: T K (+ T)
   int ksplit, stages;
+  int more1, more2;  // added to the awaited counts of FC1's and FC2's results: 0 but for a test
   uint64_t wait_limit_ns;
 };
 
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
   int32_t* done = p.sync + 2;   // warps that wrote FC1 results, per busy expert
   int32_t* done2 = p.sync + 1;  // warps that wrote FC2 results
   const int width1 = few_rows1<L>(glu);
-  const int total = ctl.units1 + ctl.units2;
+  const int total = ctl.units1 + ctl.units2, all2 = ctl.fc2_writers + p.more2;
   tc::WaitCtl wc{p.a.status, &ctl.abort, p.wait_limit_ns, 0};
   tc::WaitCtl wdrain{p.a.status, nullptr, 1000000000ull, 0};
 
@@ -805,7 +806,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
       if (st.kind == kFC2 && ready != st.entry) {  // the expert's hidden values
         const int writers = few_writers_of<L>(ctl.ent_n[st.entry], width1);
         int up = 0;
-        if (lane == 0) up = wait_count(done + st.entry, nrb1 * writers, wc);
+        if (lane == 0) up = wait_count(done + st.entry, nrb1 * writers + p.more1, wc);
         if (!__shfl_sync(0xffffffffu, up, 0)) break;
         ld_acquire(done + st.entry);  // every lane's own
         fence_proxy_async_global();
@@ -1023,10 +1024,10 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
     finish = finish && blockIdx.x < few_combine_items(cf);
     if (finish && warp == 0) {  // one warp of a block that has a share watches the count
       int all = 0;
-      if (lane == 0) all = wait_count(done2, ctl.fc2_writers, wc);
+      if (lane == 0) all = wait_count(done2, all2, wc);
       __shfl_sync(0xffffffffu, all, 0);
     }
-    if (finish && meet() && ld_acquire(done2) >= ctl.fc2_writers) {
+    if (finish && meet() && ld_acquire(done2) >= all2) {
       few_combine(p, ctl, at, warp, L::NW, lane);
     }
   }
@@ -1184,7 +1185,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
   // Waits until an FC2 unit's expert has all its hidden values.
   auto hidden_ready = [&](int entry) -> bool {
     int up = 0;
-    if (lane == 0) up = wait_count(done + entry, nrb1 * few_writers_of<L>(ctl.ent_n[entry], 0), wc);
+    if (lane == 0) up = wait_count(done + entry, nrb1 * few_writers_of<L>(ctl.ent_n[entry], 0) + p.more1, wc);
     if (!__shfl_sync(0xffffffffu, up, 0)) return false;
     ld_acquire(done + entry);  // every lane's own
     return true;
@@ -1340,7 +1341,8 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
             tma_load_3d(dst + b * L::B_BOX, &p.act, (st.k0 + b * L::KB) / 2, 0, st.pos0, fb);
       }
       __syncwarp();
-      note_issued();
+      if (st.kind == kFC1 || tw == 0) note_issued();
+      else issued &= ~(1u << stage);  // no copies of its own; the stage's last ones are consumed
       next_stage();
     }
     for (int s = 0; s < p.stages; ++s)
@@ -1480,7 +1482,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_mx_kernel(const __grid_cons
   }
   // ---- combine: every block's share ----
   const bool share = !ctl.abort && blockIdx.x < few_combine_items(cf);
-  if (share && threadIdx.x == 0) mc.tmem_base = wait_count(done2, ctl.fc2_writers, wc);  // (its address is read)
+  if (share && threadIdx.x == 0) mc.tmem_base = wait_count(done2, ctl.fc2_writers + p.more2, wc);  // (its address is read)
   __syncthreads();
   if (share && mc.tmem_base != 0) {
     ld_acquire(done2);  // every thread's own
@@ -1597,7 +1599,9 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   p.ypart = reinterpret_cast<float*>(a.ws + L.ypart);
   p.S = c.T * c.K + (c.n_shared ? c.T : 0);
   p.ksplit = few_ksplit(c);
-  p.wait_limit_ns = 2000000000ull;
+  p.more1 = a.starve == 1;
+  p.more2 = a.starve == 2;
+  p.wait_limit_ns = a.starve ? 20000000ull : 2000000000ull;
   RouterArgs r{};
   r.T = c.T; r.E = c.E; r.K = c.K; r.h = c.h; r.score = c.score;
   r.renorm = (c.flags & MOE_FLAG_RENORM) != 0;

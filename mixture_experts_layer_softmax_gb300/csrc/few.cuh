@@ -106,6 +106,7 @@ struct FewArgs {
   char* ws;           // few_layout
   int* status;
   int sms;
+  int starve;         // 0, or the wait on counts that is to run out: 1 FC1's results, 2 FC2's
 };
 
 cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s);

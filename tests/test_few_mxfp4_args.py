@@ -124,3 +124,14 @@ def test_workspace_covers_both_calls(M):
             n = M.moe_workspace_size(_cfg(M, T=T, **kw))
             assert n >= last and n % 256 == 0
             last = n
+
+
+def test_wait_hook(M):
+    """What is pending is handed back, and calls that enqueue nothing leave it."""
+    assert M.moe_test_few_wait_runs_out(3) == -1 and M.moe_test_few_wait_runs_out(-1) == -1
+    assert M.moe_test_few_wait_runs_out(2) == 0
+    assert _few(M, _cfg(M)) == M.MOE_OK                            # validates only
+    assert _few(M, _cfg(M, T=0, flags=0), x=None, y=None) == M.MOE_OK
+    assert M.moe_test_few_wait_runs_out(1) == 2
+    assert M.moe_test_few_wait_runs_out(0) == 1
+    assert M.moe_test_few_wait_runs_out(0) == 0
