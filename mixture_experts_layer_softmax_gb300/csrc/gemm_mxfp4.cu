@@ -103,10 +103,12 @@ MOE_D uint32_t pack_bf16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// SiLU with the approximate exponential and reciprocal (each within 2 units in
-// the last place of fp32 or so, far inside the output's bf16 or E2M1 step): the
-// exact ones kept the epilogue warps busy for longer than the tile's MMAs.
-// (exp(-z) overflowing gives -0, SiLU's limit; NaN stays.)
+// SiLU with the approximate exponential and reciprocal: the exact ones kept the
+// epilogue warps busy for longer than the tile's MMAs.  CUDA bounds __expf(-z) by
+// 2 + |1.173 z| units in the last place and __fdividef by 2, so the value is off by
+// 2^-23 (5 + 1.2 |z|) of itself: below 2^-16 for every z whose SiLU is a normal number
+// (z > -92), beside half steps of 2^-8 (bf16) and 2^-2 (E2M1).  A reciprocal below
+// 2^-126 is 0, and exp(-z) overflowing gives -0, SiLU's limit; NaN stays.
 MOE_D float silu_fast(float z) { return z * __fdividef(1.f, 1.f + __expf(-z)); }
 
 // 32 lanes x two groups of 32 columns: both loads in flight, then one wait, in one
