@@ -43,6 +43,7 @@
 // every role leaves its loop as in the bf16 kernels.
 #include <cuda_fp8.h>
 
+#include "mx.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -52,7 +53,8 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = 128;  // BK: K elements (= bytes) per stage
 constexpr int A_BYTES = BM * BK;             // 16 KB
 constexpr int B_BYTES = BN * BK;             // 32 KB
-constexpr int ATOM = 512;                    // one scale atom
+using mx::ATOM;
+using mx::atom_word;
 constexpr int SF_BYTES = 3 * ATOM;           // A atom + two B atoms
 constexpr int STAGES = 4;
 constexpr int kThreads = 320;  // producer, MMA, 8 epilogue warps
@@ -110,11 +112,6 @@ MOE_D uint2 e4m3x8(const float* v) {
 MOE_D uint32_t pack_bf16x2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Byte offset of row i's scale word (blocks j = 0..3) in atom (tile, kb).
-MOE_HD int64_t atom_word(int64_t tile, int KB, int kb, int i) {
-  return (tile * KB + kb) * ATOM + 16 * (i & 31) + 4 * (i >> 5);
 }
 
 // ---- quantiser ------------------------------------------------------------------
