@@ -385,7 +385,9 @@ moe_status_t moe_layer_fwd(const moe_config_t* cfg, const void* x, const float* 
  * fit 31 bits).  p is applied to the expert's output in fp32; the expert's
  * hidden values are kept as sums of two bf16 numbers, within 2^-16 of them.
  * Results may differ from moe_layer_fwd's in the last bits (the fp32 sums have
- * other orders).  Bitwise
+ * other orders), and two experts whose keys are that close may be chosen the
+ * other way round.  Weights are finite: beside an infinite one in W2 the two
+ * numbers may give NaN where the formula has an infinity.  Bitwise
  * reproducible.  MOE_FLAG_GEMM_* and MOE_FLAG_HIST_FROM_ROUTER have no effect.
  * ws: moe_workspace_size(cfg) bytes; no state of an earlier call is read, what
  * a moe_layer_fwd left there for a backward is overwritten, and calls that can

@@ -656,9 +656,11 @@ __device__ __forceinline__ void few_combine(const FewParams& p, const FewCtl& ct
 // Weights that are needed whatever the selection, or nearly so, are asked for before
 // it, by the blocks together (16 KB a request, one thread), up to about what HBM
 // delivers until the list is there: the first experts' when there are twice as many
-// pairs as experts or more (an expert then stays idle once in e^2 at most: 13 tokens,
-// 2 of 8, MXFP4, 122.0 us without, 119.2 so, 118.7 with 40 MB; 32 tokens, bf16, 422.3,
-// 417.0 and 419.2), then the shared one's (five tokens of 256, bf16, 407.5 and 405.3).
+// pairs as experts or more, then the shared one's (five tokens of 256, bf16, 407.5 us
+// without and 405.3).  Where tokens choose alike and independently an expert then stays
+// idle once in e^2 at most (13 tokens, 2 of 8, MXFP4, 122.0 us without, 119.2 so, 118.7
+// with 40 MB; 32 tokens, bf16, 422.3, 417.0 and 419.2); where they all choose experts
+// past the first ones, the requests are 3 us of HBM for nothing.
 constexpr int64_t kPrefetchBytes = 20 << 20;
 constexpr int kPrefetchChunk = 16384, kPrefetchPairs = 2;
 MOE_D void few_prefetch(const void* base, int64_t bytes, int64_t& room) {
@@ -1042,7 +1044,7 @@ __global__ void __launch_bounds__(L::THREADS, 1) few_kernel(const __grid_constan
 // accumulators in TMEM (two, for two units in turn).  Decoding the codes on the
 // ALUs for m16n8k16 products (tokens in fp16) took 34 warp instructions for 16 x
 // 32 weights: T = 13, 2 of 8 experts / T = 64, 8 of 64 / T = 5, 8 of 256 ran in
-// 156 / 92 / 165 us; this takes 118 / 54 / 124.
+// 156 / 92 / 165 us; this takes 121 / 58 / 124.
 //   warp 0  weights: 128-row boxes of 256 codes and the rows' scale atoms; 512
 //           columns a stage (256 a stage, seven or eight stages: the scale warp's
 //           work a stage bounds it, 161 / 68 / 171 us);
@@ -1614,7 +1616,7 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   // 46.7 / 46.5 / 47.9, 5 tokens of 256 129.3 / 126.3 / 124.9 / 123.0.
   auto warps = [&](int tok) { return (int64_t)c.E * kparts * ceil_div(c.T, tok); };
   int tok = 8;
-  while (tok > 1 && warps(tok) < 26 * 152) tok /= 2;
+  while (tok > 1 && warps(tok) < 26 * a.sms) tok /= 2;
   const int route_blocks = (int)ceil_div(warps(tok), 8);
   auto* route = tok == 1 ? few_router_kernel<1> : tok == 2 ? few_router_kernel<2>
                 : tok == 4 ? few_router_kernel<4> : few_router_kernel<8>;
@@ -1629,7 +1631,8 @@ cudaError_t launch_few(const FewArgs& a, bool mxfp4, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Tokens a unit holds: 8 while experts have at most that many on average or
   // half of it (what is more becomes a second unit, whose weights come from the
-  // L2), 16 beyond.  us with 8 / 16 beside bf16 weights, T = 32, 2 of 8: 513 / 455.
+  // L2), 16 beyond.  us with 8 / 16: T = 32, 2 of 8, bf16, 485 / 439; T = 64, 8 of 64,
+  // MXFP4, 63.5 / 58.1; T = 13, 2 of 8, MXFP4 (3.25 tokens an expert), 118 to 125 / 129.
   const bool many = c.T > 8 && (int64_t)c.T * c.K > 4LL * c.E;
   if (mxfp4)
     return many ? few_mx_launch<FewMxTile<2>>(p, xq, s) : few_mx_launch<FewMxTile<1>>(p, xq, s);

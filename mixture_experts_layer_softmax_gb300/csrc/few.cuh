@@ -18,7 +18,9 @@ constexpr int kParts = 6;
 // Slices of the router's h reduction: enough (expert, slice) pairs to give
 // every SM 16 warps, slices of at least 256 columns, at most 32 of them.  (us for 5
 // tokens of 256 experts, MXFP4, with 4 / 8 / 16 / 32 warps: 129.4 / 125.0 / 122.1 /
-// 126.0; slices of 128 columns: 64 tokens of 64 59.9 against 54.4.)
+// 126.0; slices of 128 columns: 64 tokens of 64 59.9 against 54.4.)  152 is the GB300's
+// SM count, not the device's own: the workspace's size, which this sets, and the sums'
+// order are the config's alone.
 inline int few_kparts(const moe_config_t& c) {
   const int64_t most = ceil_div(c.h, 256);
   int64_t p = ceil_div(16 * 152, c.E);
