@@ -167,9 +167,10 @@ def test_mxfp4_weights_leave_the_output_rounding(c):
 @pytest.mark.parametrize("T", [6, 30])
 def test_what_stands_beside_an_outlier_in_a_block(T):
     """A value of 100 in one of a token's 32 blocks, which meets zero weights: the
-    result is that of the other values, and what six parts leave of those 31
-    (2^-17 100 = 1/1300 at most, in a 32nd of the products) is a thirtieth of the
-    output rounding; 2^-11 100 would be twice that rounding."""
+    result is that of the other values.  Six parts leave at most 2^-17 100 = 1/1300 of
+    those beside it, 1/2300 in the mean, and as these are a 32nd of the products some
+    1/10000 of a result, a fifteenth of the output rounding; four parts (2^-11 100) would
+    leave four times that rounding."""
     f = Case(T=T, h=1024, E=2, K=1, F=256, mx=True)
     f.x[:, 40] = 100.0
     w1 = f.w1_bf16.copy()
