@@ -352,6 +352,93 @@ moe_status_t moe_expert_fc2_mxfp4(const moe_config_t* cfg, const uint8_t* a_q,
                                   const uint8_t* w2_q, const uint8_t* w2_sf, void* y_perm,
                                   moe_stream_t stream);
 
+/* ---- FP8 with a scale for each block of 128 (review §5.3, the blockwise recipe) ----
+ * E4M3 codes (uint8, row-major) with fp32 scales: activations one for each 128
+ * columns of a row (x_sf [rows, K/128]), expert weights one for each 128 x 128
+ * block (w_sf [N/128, K/128] per expert).  A block whose largest magnitude is m
+ * has a = max(m, 448 2^-125), the scale a / 448 (fp32) and the codes
+ * E4M3(448 x / a), to nearest even: of an infinity or a NaN, a NaN scale and NaN
+ * codes.  A code stands for its E4M3 value times the block's scale.
+ *
+ * Errors: NULL or 16-byte-misaligned tensors -> MOE_ERR_INVALID_ARG; K, N or the
+ * config's h / F not multiples of 128, act not SwiGLU, has_bias, fp32 dtype ->
+ * MOE_ERR_UNSUPPORTED; bounded-wait timeouts on the device -> moe_get_error. */
+
+/* Quantise activations (or their gradients) x [rows, K] bf16: q [rows, K], sf
+ * [rows, K/128].  Exact: the codes depend on the bf16 values alone. */
+moe_status_t moe_fp8_quantize(int64_t rows, int32_t K, const void* x, uint8_t* q, float* sf,
+                              moe_stream_t stream);
+
+/* Quantise `groups` weight matrices w [groups][N][K] bf16 in 128 x 128 blocks: q
+ * [groups][N][K], sf [groups][N/128][K/128], and with q_t and sf_t (both or
+ * neither) the transposed tensors [groups][K][N], [groups][K/128][N/128]: the same
+ * codes and scales, as the data gradients' products read them. */
+moe_status_t moe_fp8_quantize_weights(int32_t groups, int32_t N, int32_t K, const void* w,
+                                      uint8_t* q, float* sf, uint8_t* q_t, float* sf_t,
+                                      moe_stream_t stream);
+
+/* Dispatch of rows that are in FP8 already (moe_rmsnorm_fwd or moe_fp8_quantize
+ * wrote them): the maps of moe_permute (same rules, capacity included) and, instead
+ * of x_perm, its codes xp_q [P,h] and scales xp_sf [P,h/128], copied from the token
+ * rows x_q [T,h] and x_sf [T,h/128].  Rows of no slot (dropped slots leave some
+ * behind the last expert's) are left as they were.  bf16 configurations with
+ * h % 128 == 0; ws as for moe_permute. */
+moe_status_t moe_permute_fp8(const moe_config_t* cfg, const uint8_t* x_q, const float* x_sf,
+                             const int32_t* topk_idx, const float* topk_prob, uint8_t* xp_q,
+                             float* xp_sf, int32_t* counts, int32_t* offsets, int32_t* dst_row,
+                             int32_t* src_token, float* perm_prob, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/* FP8 FC1 with the SwiGLU epilogue: H = x_perm W1_e^T over the values that the codes
+ * stand for (tensor-core products of 128 columns, joined in fp32), a[r] = p_r
+ * silu(H[r, :F]) H[r, F:] (p_r = perm_prob[r], 1 when NULL).  Outputs, each optional
+ * but one of a and a_q:  act_save [P,2F] bf16 (H: what moe_grouped_mlp_bwd reads),
+ * a [P,F] bf16, a_q [P,F] + a_sf [P,F/128] (a in FP8, from fp32).
+ *   x_q [P,h], x_sf [P,h/128]; offsets [E+1] as from moe_permute;
+ *   w1_q [E][2F][h], w1_sf [E][2F/128][h/128]. */
+moe_status_t moe_expert_fc1_fp8(const moe_config_t* cfg, const uint8_t* x_q, const float* x_sf,
+                                const int32_t* offsets, const float* perm_prob,
+                                const uint8_t* w1_q, const float* w1_sf, void* act_save, void* a,
+                                uint8_t* a_q, float* a_sf, moe_stream_t stream);
+
+/* FP8 FC2: y_perm[r] = a[r] W2_e^T, bf16 out.  a_q [P,F], a_sf [P,F/128];
+ * w2_q [E][h][F], w2_sf [E][h/128][F/128]; y_perm [P,h].
+ * The data gradients are the same product on transposed weights: dy_perm W2 with a
+ * config of h and F exchanged and w2's q_t, and dH W1 with one of F = 2F and w1's. */
+moe_status_t moe_expert_fc2_fp8(const moe_config_t* cfg, const uint8_t* a_q, const float* a_sf,
+                                const int32_t* offsets, const uint8_t* w2_q, const float* w2_sf,
+                                void* y_perm, moe_stream_t stream);
+
+/* RMS norm with the residual's addition, in front of the layer (the pages take the
+ * layer's input as given: this is the usual pre-norm of the models they train):
+ *   v = x + res,  r = (mean(v^2) + eps)^(-1/2),  y = v r w
+ *   x [rows,h] and res [rows,h] (or NULL) of `dtype` (moe_dtype_t); w [h] f32;
+ *   outputs: sum [rows,h] dtype or NULL (v, the residual stream's new value); y
+ *   [rows,h] dtype and / or q [rows,h] + sf [rows,h/128] (y in FP8, from fp32), one of
+ *   them at least; rstd [rows] f32 or NULL (r, for the gradient).
+ * Sums in fp32 and a fixed order.  sum and y may be x's or res's own buffers.
+ * h: multiples of 4 (fp32) or 8 (bf16), of 128 for q, at most 65536, else
+ * MOE_ERR_UNSUPPORTED; eps finite and >= 0. */
+moe_status_t moe_rmsnorm_fwd(int64_t rows, int32_t h, int32_t dtype, const void* x,
+                             const void* res, const float* w, float eps, void* sum, void* y,
+                             uint8_t* q, float* sf, float* rstd, moe_stream_t stream);
+
+/* Its gradient, with n = v r and g = dy w:
+ *   dx = r (g - n mean(g n)) + dsum,   dw = sum over rows of dy n
+ *   dy, sum (v) [rows,h] dtype; rstd [rows]; w [h]; dsum [rows,h] dtype or NULL (the
+ *   gradient that reaches v by the residual stream); outputs dx [rows,h] (the
+ *   gradient of x and of res; may be dy's, sum's or dsum's own buffer), dw [h] f32 or
+ *   NULL.  ws: moe_rmsnorm_bwd_workspace_size(rows, h) bytes, needed for dw only.
+ * Bitwise reproducible on one kind of device. */
+moe_status_t moe_rmsnorm_bwd(int64_t rows, int32_t h, int32_t dtype, const void* dy,
+                             const void* sum, const float* rstd, const float* w,
+                             const void* dsum, void* dx, float* dw, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
+/* Workspace bytes of moe_rmsnorm_bwd (0 on bad arguments); it does not shrink as rows
+ * grows. */
+size_t moe_rmsnorm_bwd_workspace_size(int64_t rows, int32_t h);
+
 /* Combine (review §2.1 "Combine"; the skill page's index_add_):
  *   y[t] = sum_{k=0}^{K-1} w[t,k] * y_perm[dst_row[t,k]]  (+ shared_y[t])
  * with w = topk_prob, or 1 when topk_prob is NULL (probabilities already
@@ -362,6 +449,19 @@ moe_status_t moe_expert_fc2_mxfp4(const moe_config_t* cfg, const uint8_t* a_q,
 moe_status_t moe_unpermute_combine(const moe_config_t* cfg, const void* y_perm,
                                    const int32_t* dst_row, const float* topk_prob,
                                    const void* shared_y, void* y, moe_stream_t stream);
+
+/* Gradient of the combine (the weights' and the rows'; dshared_y is dy itself):
+ *   dy_perm[dst_row[t,k]] = w[t,k] dy[t],  dprob[t,k] = <dy[t], y_perm[dst_row[t,k]]>
+ * with w = topk_prob, or 1 when it is NULL; slots with dst_row -1 get dprob 0, rows
+ * of y_perm that no slot names are left as they were in dy_perm.
+ *   dy [T,h]; y_perm [P,h] and dprob [T,K] f32 (both or neither); dst_row [T,K];
+ *   dy_perm [P,h] out (not y_perm's buffer).
+ * The gradient of the dispatch, dx[t] = sum_k dx_perm[dst_row[t,k]], is
+ * moe_unpermute_combine without weights. */
+moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,
+                                       const void* y_perm, const int32_t* dst_row,
+                                       const float* topk_prob, void* dy_perm, float* dprob,
+                                       moe_stream_t stream);
 
 /* The whole forward layer pass: Route, Dispatch, grouped expert GEMMs (plus
  * the shared expert when n_shared = 1, weight 1, not routed), Combine.

@@ -68,6 +68,22 @@ cudaError_t launch_grouped_gemm_mxfp4(bool, int, const uint8_t*, const uint8_t*,
                                       const uint8_t*, const uint8_t*, int, int, int,
                                       const int32_t*, const float*, void*, uint8_t*, uint8_t*,
                                       int, int*, cudaStream_t);
+cudaError_t launch_fp8_quantize(int64_t, int, const void*, uint8_t*, float*, int, cudaStream_t);
+cudaError_t launch_fp8_quantize_weights(int, int, int, const void*, uint8_t*, float*, uint8_t*,
+                                        float*, cudaStream_t);
+cudaError_t launch_fp8_scatter(const moe_config_t&, const uint8_t*, const float*, const int32_t*,
+                               uint8_t*, float*, int*, cudaStream_t);
+cudaError_t launch_fp8_product(bool, int, const uint8_t*, const float*, int, const uint8_t*,
+                               const float*, int, int, const int32_t*, const float*, void*, void*,
+                               uint8_t*, float*, int, int*, cudaStream_t);
+size_t rmsnorm_bwd_workspace(int64_t rows, int h);
+cudaError_t launch_rmsnorm_fwd(int64_t, int, int, const void*, const void*, const float*, float,
+                               void*, void*, uint8_t*, float*, float*, cudaStream_t);
+cudaError_t launch_rmsnorm_bwd(int64_t, int, int, const void*, const void*, const float*,
+                               const float*, const void*, void*, float*, float*, int,
+                               cudaStream_t);
+cudaError_t launch_combine_bwd(const moe_config_t&, const void*, const void*, const int32_t*,
+                               const float*, void*, float*, int*, cudaStream_t);
 }  // namespace moe
 
 using namespace moe;
@@ -624,6 +640,164 @@ moe_status_t moe_expert_fc2_mxfp4(const moe_config_t* cfg, const uint8_t* a_q,
                                                c.E, c.h, offsets, nullptr, y_perm, nullptr,
                                                nullptr, d->sms, d->status,
                                                static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_quantize(int64_t rows, int32_t K, const void* x, uint8_t* q, float* sf,
+                              moe_stream_t stream) {
+  if (rows < 0 || rows > INT32_MAX || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (K % 128) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !sf || !al16(x) || !al16(q) || !al16(sf)) return MOE_ERR_INVALID_ARG;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  return cuda_status(
+      launch_fp8_quantize(rows, K, x, q, sf, d->sms, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_quantize_weights(int32_t groups, int32_t N, int32_t K, const void* w,
+                                      uint8_t* q, float* sf, uint8_t* q_t, float* sf_t,
+                                      moe_stream_t stream) {
+  if (groups < 1 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (N % 128 || K % 128) return MOE_ERR_UNSUPPORTED;
+  if (((int64_t)N / 128) * (K / 128) > INT32_MAX / groups) return MOE_ERR_UNSUPPORTED;
+  if (!w || !q || !sf || !q_t != !sf_t) return MOE_ERR_INVALID_ARG;
+  if (!al16(w) || !al16(q) || !al16(sf) || !al16(q_t) || !al16(sf_t)) return MOE_ERR_INVALID_ARG;
+  if (!device_info()) return MOE_ERR_CUDA;
+  return cuda_status(launch_fp8_quantize_weights(groups, N, K, w, q, sf, q_t, sf_t,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_permute_fp8(const moe_config_t* cfg, const uint8_t* x_q, const float* x_sf,
+                             const int32_t* topk_idx, const float* topk_prob, uint8_t* xp_q,
+                             float* xp_sf, int32_t* counts, int32_t* offsets, int32_t* dst_row,
+                             int32_t* src_token, float* perm_prob, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->dtype != MOE_BF16 || cfg->h % 128) return MOE_ERR_UNSUPPORTED;
+  if (!counts || !offsets) return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && (!x_q || !x_sf || !topk_idx || !dst_row || !src_token || !xp_q || !xp_sf))
+    return MOE_ERR_INVALID_ARG;
+  if (!al16(x_q) || !al16(x_sf) || !al16(xp_q) || !al16(xp_sf)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(cfg, ws, ws_bytes)) != MOE_OK) return st;
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const Workspace w = workspace_layout(*cfg);
+  cudaError_t e = launch_permute_maps(*cfg, topk_idx, topk_prob, at<int32_t>(ws, w.hist),
+                                      at<int32_t>(ws, w.chunk_base), counts, offsets, dst_row,
+                                      src_token, perm_prob, d->status, s,
+                                      (cfg->flags & MOE_FLAG_HIST_FROM_ROUTER) != 0);
+  if (e == cudaSuccess)
+    e = launch_fp8_scatter(*cfg, x_q, x_sf, dst_row, xp_q, xp_sf, d->status, s);
+  return cuda_status(e);
+}
+
+moe_status_t moe_expert_fc1_fp8(const moe_config_t* cfg, const uint8_t* x_q, const float* x_sf,
+                                const int32_t* offsets, const float* perm_prob,
+                                const uint8_t* w1_q, const float* w1_sf, void* act_save, void* a,
+                                uint8_t* a_q, float* a_sf, moe_stream_t stream) {
+  moe_status_t st = check_mxfp8(cfg);
+  if (st != MOE_OK) return st;
+  if (!x_q || !x_sf || !offsets || !w1_q || !w1_sf) return MOE_ERR_INVALID_ARG;
+  if ((!a && !a_q) || !a_q != !a_sf) return MOE_ERR_INVALID_ARG;
+  if (!al16(x_q) || !al16(x_sf) || !al16(w1_q) || !al16(w1_sf) || !al16(act_save) || !al16(a) ||
+      !al16(a_q) || !al16(a_sf))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  const moe_config_t& c = *cfg;
+  return cuda_status(launch_fp8_product(true, c.T * c.K, x_q, x_sf, c.h, w1_q, w1_sf, c.E, c.F,
+                                        offsets, perm_prob, act_save, a, a_q, a_sf, d->sms,
+                                        d->status, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_expert_fc2_fp8(const moe_config_t* cfg, const uint8_t* a_q, const float* a_sf,
+                                const int32_t* offsets, const uint8_t* w2_q, const float* w2_sf,
+                                void* y_perm, moe_stream_t stream) {
+  moe_status_t st = check_mxfp8(cfg);
+  if (st != MOE_OK) return st;
+  if (!a_q || !a_sf || !offsets || !w2_q || !w2_sf || !y_perm) return MOE_ERR_INVALID_ARG;
+  if (!al16(a_q) || !al16(a_sf) || !al16(w2_q) || !al16(w2_sf) || !al16(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  const moe_config_t& c = *cfg;
+  return cuda_status(launch_fp8_product(false, c.T * c.K, a_q, a_sf, c.F, w2_q, w2_sf, c.E, c.h,
+                                        offsets, nullptr, nullptr, y_perm, nullptr, nullptr,
+                                        d->sms, d->status, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+moe_status_t check_rmsnorm(int64_t rows, int32_t h, int32_t dtype) {
+  if (rows < 0 || rows > INT32_MAX || h <= 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (h % (dtype == MOE_BF16 ? 8 : 4) || h > 65536) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status_t moe_rmsnorm_fwd(int64_t rows, int32_t h, int32_t dtype, const void* x,
+                             const void* res, const float* w, float eps, void* sum, void* y,
+                             uint8_t* q, float* sf, float* rstd, moe_stream_t stream) {
+  const moe_status_t st = check_rmsnorm(rows, h, dtype);
+  if (st != MOE_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.f) return MOE_ERR_INVALID_ARG;
+  if (!q != !sf || (rows > 0 && (!x || !w || (!y && !q)))) return MOE_ERR_INVALID_ARG;
+  if (q && h % 128) return MOE_ERR_UNSUPPORTED;
+  if (!al16(x) || !al16(res) || !al16(w) || !al16(sum) || !al16(y) || !al16(q) || !al16(sf) ||
+      !al16(rstd))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!device_info()) return MOE_ERR_CUDA;
+  return cuda_status(launch_rmsnorm_fwd(rows, h, dtype, x, res, w, eps, sum, y, q, sf, rstd,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_rmsnorm_bwd_workspace_size(int64_t rows, int32_t h) {
+  if (check_rmsnorm(rows, h, MOE_F32) != MOE_OK) return 0;
+  return rmsnorm_bwd_workspace(rows, h);
+}
+
+moe_status_t moe_rmsnorm_bwd(int64_t rows, int32_t h, int32_t dtype, const void* dy,
+                             const void* sum, const float* rstd, const float* w,
+                             const void* dsum, void* dx, float* dw, void* ws, size_t ws_bytes,
+                             moe_stream_t stream) {
+  const moe_status_t st = check_rmsnorm(rows, h, dtype);
+  if (st != MOE_OK) return st;
+  if (rows > 0 && (!dy || !sum || !rstd || !w || !dx)) return MOE_ERR_INVALID_ARG;
+  if (!al16(dy) || !al16(sum) || !al16(rstd) || !al16(w) || !al16(dsum) || !al16(dx) || !al16(dw))
+    return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && dw) {
+    if (!ws || ws_bytes < rmsnorm_bwd_workspace(rows, h)) return MOE_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return MOE_ERR_INVALID_ARG;
+  }
+  if (rows == 0 && !dw) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, (size_t)h * 4, s));
+  return cuda_status(launch_rmsnorm_bwd(rows, h, dtype, dy, sum, rstd, w, dsum, dx, dw,
+                                        static_cast<float*>(ws), d->sms, s));
+}
+
+moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,
+                                       const void* y_perm, const int32_t* dst_row,
+                                       const float* topk_prob, void* dy_perm, float* dprob,
+                                       moe_stream_t stream) {
+  const moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->T > 0 && (!dy || !dst_row || !dy_perm)) return MOE_ERR_INVALID_ARG;
+  if (!y_perm != !dprob || (y_perm && y_perm == dy_perm)) return MOE_ERR_INVALID_ARG;
+  if (!al16(dy) || !al16(y_perm) || !al16(dy_perm)) return MOE_ERR_INVALID_ARG;
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  return cuda_status(launch_combine_bwd(*cfg, dy, y_perm, dst_row, topk_prob, dy_perm, dprob,
+                                        d->status, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_unpermute_combine(const moe_config_t* cfg, const void* y_perm,

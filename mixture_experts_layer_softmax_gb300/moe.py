@@ -75,7 +75,18 @@ _SIG = {
     "moe_expert_fc2_mxfp4": (ctypes.c_int, [_CFG] + [_P] * 7),
     "moe_layer_fwd_few": (ctypes.c_int, [_CFG] + [_P] * 14 + [ctypes.c_size_t, _P]),
     "moe_layer_fwd_few_mxfp4": (ctypes.c_int, [_CFG] + [_P] * 16 + [ctypes.c_size_t, _P]),
+    "moe_fp8_quantize": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P]),
+    "moe_fp8_quantize_weights": (ctypes.c_int, [ctypes.c_int32] * 3 + [_P] * 6),
+    "moe_permute_fp8": (ctypes.c_int, [_CFG] + [_P] * 12 + [ctypes.c_size_t, _P]),
+    "moe_expert_fc1_fp8": (ctypes.c_int, [_CFG] + [_P] * 11),
+    "moe_expert_fc2_fp8": (ctypes.c_int, [_CFG] + [_P] * 7),
+    "moe_rmsnorm_fwd": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
+                                       ctypes.c_float] + [_P] * 6),
+    "moe_rmsnorm_bwd_workspace_size": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int32]),
+    "moe_rmsnorm_bwd": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32] + [_P] * 8 +
+                        [ctypes.c_size_t, _P]),
     "moe_unpermute_combine": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P]),
+    "moe_unpermute_combine_bwd": (ctypes.c_int, [_CFG] + [_P] * 7),
     "moe_layer_fwd": (ctypes.c_int, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                      ctypes.c_size_t, _P]),
     "moe_grouped_mlp_bwd": (ctypes.c_int, [_CFG] + [_P] * 13 + [ctypes.c_size_t, _P]),
@@ -293,10 +304,73 @@ def moe_expert_fc2_mxfp4(cfg, a_q, a_sf, offsets, w2_q, w2_sf, y_perm, stream=No
         _ptr(y_perm), _stream(stream)))
 
 
+def moe_fp8_quantize(rows, K, x, q, sf, stream=None):
+    """x [rows, K] bf16 -> E4M3 codes q [rows, K] and scales sf [rows, K/128]."""
+    _check("moe_fp8_quantize", _lib.moe_fp8_quantize(
+        int(rows), int(K), _ptr(x), _ptr(q), _ptr(sf), _stream(stream)))
+
+
+def moe_fp8_quantize_weights(groups, N, K, w, q, sf, q_t=None, sf_t=None, stream=None):
+    """w [groups, N, K] bf16 -> codes q and scales sf [groups, N/128, K/128] of its
+    128 x 128 blocks and, if given, the transposed tensors q_t, sf_t."""
+    _check("moe_fp8_quantize_weights", _lib.moe_fp8_quantize_weights(
+        int(groups), int(N), int(K), _ptr(w), _ptr(q), _ptr(sf), _ptr(q_t), _ptr(sf_t),
+        _stream(stream)))
+
+
+def moe_permute_fp8(cfg, x_q, x_sf, topk_idx, topk_prob, xp_q, xp_sf, counts, offsets, dst_row,
+                    src_token, perm_prob, ws, stream=None):
+    """moe_permute of rows that are in FP8 already."""
+    wp, wb = _ws(ws)
+    _check("moe_permute_fp8", _lib.moe_permute_fp8(
+        ctypes.byref(cfg), _ptr(x_q), _ptr(x_sf), _ptr(topk_idx), _ptr(topk_prob), _ptr(xp_q),
+        _ptr(xp_sf), _ptr(counts), _ptr(offsets), _ptr(dst_row), _ptr(src_token), _ptr(perm_prob),
+        wp, wb, _stream(stream)))
+
+
+def moe_expert_fc1_fp8(cfg, x_q, x_sf, offsets, perm_prob, w1_q, w1_sf, act_save, a, a_q, a_sf,
+                       stream=None):
+    _check("moe_expert_fc1_fp8", _lib.moe_expert_fc1_fp8(
+        ctypes.byref(cfg), _ptr(x_q), _ptr(x_sf), _ptr(offsets), _ptr(perm_prob), _ptr(w1_q),
+        _ptr(w1_sf), _ptr(act_save), _ptr(a), _ptr(a_q), _ptr(a_sf), _stream(stream)))
+
+
+def moe_expert_fc2_fp8(cfg, a_q, a_sf, offsets, w2_q, w2_sf, y_perm, stream=None):
+    _check("moe_expert_fc2_fp8", _lib.moe_expert_fc2_fp8(
+        ctypes.byref(cfg), _ptr(a_q), _ptr(a_sf), _ptr(offsets), _ptr(w2_q), _ptr(w2_sf),
+        _ptr(y_perm), _stream(stream)))
+
+
+def moe_rmsnorm_fwd(rows, h, dtype, x, res, w, eps, sum=None, y=None, q=None, sf=None, rstd=None,
+                    stream=None):
+    """y = RMS norm of x + res, in `dtype` and / or FP8; sum = x + res."""
+    _check("moe_rmsnorm_fwd", _lib.moe_rmsnorm_fwd(
+        int(rows), int(h), int(dtype), _ptr(x), _ptr(res), _ptr(w), float(eps), _ptr(sum), _ptr(y),
+        _ptr(q), _ptr(sf), _ptr(rstd), _stream(stream)))
+
+
+def moe_rmsnorm_bwd_workspace_size(rows, h) -> int:
+    return int(_lib.moe_rmsnorm_bwd_workspace_size(int(rows), int(h)))
+
+
+def moe_rmsnorm_bwd(rows, h, dtype, dy, sum, rstd, w, dsum, dx, dw=None, ws=None, stream=None):
+    wp, wb = _ws(ws)
+    _check("moe_rmsnorm_bwd", _lib.moe_rmsnorm_bwd(
+        int(rows), int(h), int(dtype), _ptr(dy), _ptr(sum), _ptr(rstd), _ptr(w), _ptr(dsum),
+        _ptr(dx), _ptr(dw), wp, wb, _stream(stream)))
+
+
 def moe_unpermute_combine(cfg, y_perm, dst_row, topk_prob, shared_y, y, stream=None):
     _check("moe_unpermute_combine", _lib.moe_unpermute_combine(
         ctypes.byref(cfg), _ptr(y_perm), _ptr(dst_row), _ptr(topk_prob), _ptr(shared_y), _ptr(y),
         _stream(stream)))
+
+
+def moe_unpermute_combine_bwd(cfg, dy, y_perm, dst_row, topk_prob, dy_perm, dprob=None,
+                              stream=None):
+    _check("moe_unpermute_combine_bwd", _lib.moe_unpermute_combine_bwd(
+        ctypes.byref(cfg), _ptr(dy), _ptr(y_perm), _ptr(dst_row), _ptr(topk_prob), _ptr(dy_perm),
+        _ptr(dprob), _stream(stream)))
 
 
 def moe_layer_fwd(cfg, x, w_r, gate_bias, sel_bias, w1, b1, w2, b2, w1_shared, w2_shared, y,
