@@ -1,7 +1,24 @@
 // FP8 expert products with a scale for each block of 128 (fp8.cuh):
 //   z[r, n] = sum_b sa[r, b] sw[n / 128, b] sum_{k in block b} a[r, k] w[n, k]
 // for the rows r of each expert, and FC1's epilogue a = p silu(gate) up.
+//
+// The scales are fp32 numbers, which the tensor cores do not apply: the products
+// of one block of 128 columns (4 MMAs of K = 32, kind::f8f6f4) are summed in TMEM
+// and joined in registers, acc += (sa sw) t, an FMA a value and block.
+//
+// Persistent kernel, one CTA an SM, tiles of 128 rows x 256 weight rows (FC1: 128
+// gate and the matching 128 up rows):
+//   warp 0     TMA producer: 4 stages of {A 128 x 128 B, W 256 x 128 B}.
+//   warp 1     TMEM owner and MMA issuer: a stage's products go to one of two
+//              256-column accumulators, each given back once a block.
+//   warps 4-11 two warps a TMEM lane quarter (32 rows), each one half of the
+//              columns: a thread keeps 128 fp32 sums of one row.
+// While they evaluate and store a tile the MMAs run at most two blocks ahead.
+// Every wait is bounded; one that gives up records MOE_ERR_TIMEOUT and every role
+// leaves its loop.
 #include "fp8.cuh"
+#include "mx.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -9,124 +26,340 @@ namespace {
 
 using fp8::BLOCK;
 
-struct Fp8Params {
+constexpr int TM = 128, TN = 256;
+constexpr int A_BYTES = TM * BLOCK, W_BYTES = TN * BLOCK;
+constexpr int STAGES = 4;
+constexpr int kThreads = 384;
+// Registers a thread: 384 x 168 at launch; the first warpgroup gives some back and
+// the joining ones take them.
+constexpr int kRegsIssue = 56, kRegsJoin = 224;
+static_assert(kRegsIssue + 2 * kRegsJoin <= 3 * 168, "more registers than the launch brings");
+
+struct Ctl {
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], meet[4], drain;
+  uint32_t tmem_base;
+  int abort;
+  int off[257], tile_start[257];
+  uint32_t top[2][2][TM];  // tile parity, half of the columns, row
+};
+constexpr size_t kSmem = 1024 + (size_t)STAGES * (A_BYTES + W_BYTES) + sizeof(Ctl);
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+struct TcParams {
   const int32_t* offsets;  // [E+1]
   const float* prob;       // FC1: [P] or null
-  const uint8_t* a;        // [P, Kd]
-  const float* a_sf;       // [P, Kd/128]
-  const uint8_t* w;        // [E * Nw, Kd]
-  const float* w_sf;       // [E * Nw/128, Kd/128]
+  const float* a_sf;       // [P, KB]
+  const float* w_sf;       // [E * Nw/128, KB]
   __nv_bfloat16* save;     // FC1: [P, 2N] pre-activation or null
   __nv_bfloat16* out;      // [P, N] or null
   uint8_t* out_q;          // FC1: [P, N] or null
   float* out_sf;           // FC1: [P, N/128]
-  int P, E, Kd, N, Nw;     // Nw: weight rows an expert (2N or N)
+  int P, E, KB, N, Nw;     // KB: blocks of K; Nw: weight rows an expert (2N or N)
+  int* status;
+  uint64_t wait_limit_ns;
 };
 
-constexpr int BM = 16;
+// acc += s t for N values, two in one packed FMA.
+template <int N> MOE_D void join(float2* acc, const uint32_t (&t)[N], float s) {
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j)
+    acc[j] = __ffma2_rn(make_float2(__uint_as_float(t[2 * j]), __uint_as_float(t[2 * j + 1])),
+                        make_float2(s, s), acc[j]);
+}
+// 16 columns of the warp's 32 lanes, arrived.
+MOE_D void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
+  tc::tmem_ld_32x32b_x16_nowait(addr, r);
+  tc::tmem_ld_wait_x16(r);
+}
+MOE_D uint32_t pack_bf16x2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// SiLU with CUDA's expf and the approximate quotient, bounded by 2 ulp; a quotient
+// below 2^-126 (z < -87) is 0.
+MOE_D float silu_f32(float z) { return z * __fdividef(1.f, 1.f + expf(-z)); }
+// 64 values of a row to 64 bf16.
+MOE_D void store64(__nv_bfloat16* dst, const float2* v) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 4)
+    *reinterpret_cast<uint4*>(dst + 2 * j) =
+        make_uint4(pack_bf16x2(v[j].x, v[j].y), pack_bf16x2(v[j + 1].x, v[j + 1].y),
+                   pack_bf16x2(v[j + 2].x, v[j + 2].y), pack_bf16x2(v[j + 3].x, v[j + 3].y));
+}
 
-// 16 rows x two blocks of 128 columns (FC1: gate and up) a block of threads;
-// thread c + 128 i takes rows 8 i .. 8 i + 7 of column c of both.
+struct Tile {
+  int e, row, rows, nb;  // expert, first row, rows of the expert from there, column tile
+};
+MOE_D Tile tile_at(const Ctl& c, int E, int tile) {
+  int lo = 0, hi = E - 1;  // largest e with tile_start[e] <= tile
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c.tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  const int local = tile - c.tile_start[lo], n = c.off[lo + 1] - c.off[lo];
+  const int mblk = (n + TM - 1) / TM;
+  const int nb = local / mblk, mb = local - nb * mblk;
+  return {lo, c.off[lo] + mb * TM, n - mb * TM, nb};
+}
+
+// Expert boundaries kept within the rows and ascending, and the tiles before
+// each expert (nblk column tiles a row tile).  One warp; off[] is loaded.
+MOE_D void scan_tiles(Ctl& c, int E, int nblk, int lane) {
+  int run_t = 0, run_o = c.off[0];
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int e = e0 + lane;
+    int end = max(run_o, e < E ? c.off[e + 1] : 0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end = max(end, t);
+    }
+    const int prev = __shfl_up_sync(0xffffffffu, end, 1), beg = lane ? prev : run_o;
+    if (e < E) c.off[e + 1] = end;
+    run_o = __shfl_sync(0xffffffffu, end, 31);
+    const int tiles = (end - beg + TM - 1) / TM * nblk;
+    int it = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, it, o);
+      if (lane >= o) it += t;
+    }
+    if (e < E) c.tile_start[e] = run_t + it - tiles;
+    run_t += __shfl_sync(0xffffffffu, it, 31);
+  }
+  if (lane == 0) c.tile_start[E] = run_t;
+}
+
 template <bool SWIGLU>
-__global__ void __launch_bounds__(256) fp8_product_simple_kernel(const Fp8Params p) {
-  __shared__ float sA[BM][33], sW[256][33], sO[BM][BLOCK + 1], sTop[BM];
-  __shared__ int s_e, s_row, s_end, s_nb;
-  const int nblk = SWIGLU ? p.N / BLOCK : (p.N + 255) / 256;
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmW, const TcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sW = sA + STAGES * A_BYTES;
+  Ctl& ctl = *reinterpret_cast<Ctl*>(sW + STAGES * W_BYTES);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p.E, KB = p.KB;
+  const int nblk = SWIGLU ? p.N / BLOCK : (p.N + TN - 1) / TN;
+
   if (threadIdx.x == 0) {
-    int64_t left = blockIdx.x;
-    s_e = -1;
-    for (int e = 0; e < p.E; ++e) {
-      const int lo = min(max(p.offsets[e], 0), p.P), hi = min(max(p.offsets[e + 1], 0), p.P);
-      const int64_t tiles = hi > lo ? (int64_t)((hi - lo + BM - 1) / BM) * nblk : 0;
-      if (left < tiles) {
-        s_e = e;
-        s_nb = (int)(left % nblk);
-        s_row = lo + (int)(left / nblk) * BM;
-        s_end = hi;
-        break;
-      }
-      left -= tiles;
+    for (int s = 0; s < STAGES; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.full[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.empty[s]), 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(tc::smem_u32(&ctl.tfull[b]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.tempty[b]), 8);
+    }
+    for (int q = 0; q < 4; ++q) tc::mbar_init(tc::smem_u32(&ctl.meet[q]), 2);
+    tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+    tc::prefetch_tensormap(&tmA);
+    tc::prefetch_tensormap(&tmW);
   }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), 512);
+    tc::tmem_relinquish();
+  }
+  for (int e = threadIdx.x; e <= E; e += kThreads) ctl.off[e] = min(max(__ldg(p.offsets + e), 0), p.P);
   __syncthreads();
-  if (s_e < 0) return;
-  const int e = s_e, row0 = s_row, end = s_end, nb = s_nb;
-  const int KB = p.Kd / BLOCK;
-  const int col0 = SWIGLU ? nb * BLOCK : nb * 256, col1 = SWIGLU ? p.N + nb * BLOCK : col0 + 128;
-  const bool two = col1 < p.Nw;
-  const int c = threadIdx.x & 127, rh = (threadIdx.x >> 7) * 8;
-  float acc[2][8] = {};
-  for (int kb = 0; kb < KB; ++kb) {
-    float part[2][8] = {};
-    for (int k0 = 0; k0 < BLOCK; k0 += 32) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < BM * 32; i += 256) {
-        const int r = row0 + i / 32;
-        sA[i / 32][i % 32] =
-            r < end ? fp8::decode(p.a[(int64_t)r * p.Kd + kb * BLOCK + k0 + i % 32]) : 0.f;
-      }
-      for (int i = threadIdx.x; i < 256 * 32; i += 256) {
-        const int n = i / 32 < 128 ? col0 + i / 32 : col1 + i / 32 - 128;
-        sW[i / 32][i % 32] =
-            n < p.Nw ? fp8::decode(p.w[((int64_t)e * p.Nw + n) * p.Kd + kb * BLOCK + k0 + i % 32])
-                     : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k) {
-        const float w0 = sW[c][k], w1 = sW[128 + c][k];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          part[0][i] = fmaf(sA[rh + i][k], w0, part[0][i]);
-          part[1][i] = fmaf(sA[rh + i][k], w1, part[1][i]);
+  if (warp == 2) scan_tiles(ctl, E, nblk, lane);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem_base = ctl.tmem_base;
+  const int total = ctl.tile_start[E];
+  tc::WaitCtl wc{p.status, &ctl.abort, p.wait_limit_ns, 0};
+  tc::WaitCtl wdrain{p.status, nullptr, 1000000000ull, 0};
+
+  if (warp < 4) {
+   tc::regs_dec<kRegsIssue>();
+   if (warp == 0) {
+    // ================= TMA producer: the warp runs the loop, one lane issues =================
+    const bool elected = tc::elect_one();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const Tile t = tile_at(ctl, E, tile);
+      const int w0 = t.e * p.Nw + (SWIGLU ? t.nb * BLOCK : t.nb * TN);
+      // the second half: FC1's up rows; FC2's next 128 rows, where an odd last tile
+      // takes rows of the next expert (or, past the tensor, zeros) that go nowhere
+      const int w1 = SWIGLU ? w0 + p.N : w0 + BLOCK;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
+        if (elected) {
+          const uint32_t fb = tc::smem_u32(&ctl.full[stage]);
+          const uint32_t wd = tc::smem_u32(sW + stage * W_BYTES);
+          tc::mbar_arrive_expect_tx(fb, A_BYTES + W_BYTES);
+          tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BLOCK, t.row, fb);
+          tc::tma_load_2d(wd, &tmW, kb * BLOCK, w0, fb);
+          tc::tma_load_2d(wd + W_BYTES / 2, &tmW, kb * BLOCK, w1, fb);
         }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
     }
-    const int64_t wb = (int64_t)e * (p.Nw / BLOCK);
-    const float s0 = p.w_sf[(wb + col0 / BLOCK) * KB + kb];
-    const float s1 = two ? p.w_sf[(wb + col1 / BLOCK) * KB + kb] : 0.f;
+    for (int s = 0; s < STAGES; ++s)
+      if ((issued >> s) & 1u)
+        tc::mbar_wait(tc::smem_u32(&ctl.full[s]), (issued_par >> s) & 1u, wdrain);
+    __syncwarp();
+   } else if (warp == 1) {
+    // ================= MMA issuer: likewise =================
+    const bool elected = tc::elect_one();
+    int stage = 0;
+    uint32_t phase = 0, step = 0;
+    bool ok = true;
+    const uint64_t a_base = tc::desc_kmajor_sw128(tc::smem_u32(sA));
+    const uint64_t w_base = tc::desc_kmajor_sw128(tc::smem_u32(sW));
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int kb = 0; kb < KB; ++kb, ++step) {
+        const uint32_t buf = step & 1;
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.tempty[buf]), ((step >> 1) & 1) ^ 1, wc) ||
+            !tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), phase, wc)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint64_t ad = a_base + (uint32_t)(stage * (A_BYTES >> 4));
+        const uint64_t wd = w_base + (uint32_t)(stage * (W_BYTES >> 4));
+        if (elected) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float sa = row0 + rh + i < end ? p.a_sf[(int64_t)(row0 + rh + i) * KB + kb] : 0.f;
-      acc[0][i] = fmaf(part[0][i], sa * s0, acc[0][i]);
-      acc[1][i] = fmaf(part[1][i], sa * s1, acc[1][i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + rh + i;
-    if (r >= end) continue;
-    if (SWIGLU) {
-      const float pr = p.prob ? p.prob[r] : 1.f;
-      const float v = pr * (silu_f(acc[0][i]) * acc[1][i]);
-      if (p.save) {
-        p.save[r * p.Nw + col0 + c] = from_f32<__nv_bfloat16>(acc[0][i]);
-        p.save[r * p.Nw + col1 + c] = from_f32<__nv_bfloat16>(acc[1][i]);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f8(tmem_base + buf * TN, ad + 2 * k, wd + 2 * k, tc::idesc_e4m3_f32(TM, TN), k != 0);
+          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+          tc::mma_commit(tc::smem_u32(&ctl.tfull[buf]));
+        }
+        __syncwarp();
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
       }
-      if (p.out) p.out[r * p.N + col0 + c] = from_f32<__nv_bfloat16>(v);
-      sO[rh + i][c] = v;
-    } else {
-      p.out[r * p.N + col0 + c] = from_f32<__nv_bfloat16>(acc[0][i]);
-      if (two) p.out[r * p.N + col1 + c] = from_f32<__nv_bfloat16>(acc[1][i]);
+    }
+    __syncwarp();
+    if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
+      if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain));
+      tc::mbar_wait(tc::smem_u32(&ctl.drain), 0, wdrain);
+    }
+    __syncwarp();
+   }
+  } else {
+    tc::regs_inc<kRegsJoin>();
+    // ================= joining and epilogue (warps 4..11) =================
+    const int q = warp & 3;          // TMEM lane quarter this warp may access
+    const int hf = (warp - 4) >> 2;  // which half of the columns (FC1: 64 gate and the matching up ones)
+    // a warp's TMEM columns: FC1's gate and up, FC2's one half
+    const uint32_t c0 = SWIGLU ? hf * 64 : hf * 128, c1 = SWIGLU ? 128 + hf * 64 : hf * 128 + 64;
+    const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+    const int i = q * 32 + lane;  // row within the tile
+    uint32_t step = 0, parity = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const Tile t = tile_at(ctl, E, tile);
+      const int n0 = SWIGLU ? t.nb * BLOCK + hf * 64 : t.nb * TN + hf * 128;  // first column
+      // the row's scales and the weight blocks' (FC1: gate and up), one block ahead.  (A
+      // row behind the expert's takes its last row's, a column block behind FC2's last
+      // the last one's: neither goes anywhere.)
+      const float* sa = p.a_sf + (int64_t)(t.row + min(i, t.rows - 1)) * KB;
+      const int wblk = p.Nw / BLOCK;
+      const float* s0 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? t.nb : min(2 * t.nb + hf, wblk - 1))) * KB;
+      const float* s1 = s0 + (int64_t)(wblk / 2) * KB;
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      float na = __ldg(sa), n0s = __ldg(s0), n1s = SWIGLU ? __ldg(s1) : 0.f;
+      for (int kb = 0; kb < KB; ++kb, ++step) {
+        const float g = na * n0s, u = SWIGLU ? na * n1s : g;
+        if (kb + 1 < KB) {
+          na = __ldg(++sa);
+          n0s = __ldg(++s0);
+          if (SWIGLU) n1s = __ldg(++s1);
+        }
+        const uint32_t buf = step & 1;
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.tfull[buf]), (step >> 1) & 1, wc)) { ok = false; break; }
+        tc::fence_after_sync();
+        const uint32_t b0 = tbase + buf * TN + c0, b1 = tbase + buf * TN + c1;
+        constexpr int LD = 16;
+        uint32_t v[LD];
+#pragma unroll
+        for (int c = 0; c < 128 / LD; ++c) {
+          const int col = c * LD;
+          tmem_ld(col < 64 ? b0 + col : b1 + col - 64, v);
+          if (c < 128 / LD - 1) join(acc + col / 2, v, col < 64 ? g : u);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tempty[buf]));
+        join(acc + 64 - LD / 2, v, u);
+      }
+      if (!ok) break;
+      const bool valid = i < t.rows;
+      const int64_t row = (int64_t)t.row + i;
+      if (SWIGLU) {
+        if (p.save && valid) {
+          store64(p.save + row * p.Nw + n0, acc);
+          store64(p.save + row * p.Nw + p.N + n0, acc + 32);
+        }
+        const float pr = p.prob && valid ? __ldg(p.prob + row) : 1.f;
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          acc[j].x = pr * (silu_f32(acc[j].x) * acc[32 + j].x);
+          acc[j].y = pr * (silu_f32(acc[j].y) * acc[32 + j].y);
+          m = max(m, max(fp8::mag_bits(acc[j].x), fp8::mag_bits(acc[j].y)));
+        }
+        if (p.out && valid) store64(p.out + row * p.N + n0, acc);
+        if (p.out_q) {
+          // the block's other 64 columns are the other warp's of this lane quarter; a
+          // buffer is written again two tiles on, behind the next tile's meeting
+          ctl.top[parity][hf][i] = m;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.meet[q]));
+          if (!tc::mbar_wait(tc::smem_u32(&ctl.meet[q]), parity, wc)) break;
+          const float a = fp8::block_top(max(m, ctl.top[parity][hf ^ 1][i]));
+          if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              float f[16];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) f[2 * k] = acc[j + k].x, f[2 * k + 1] = acc[j + k].y;
+              const uint2 x = fp8::codes8(f, a), y = fp8::codes8(f + 8, a);
+              *reinterpret_cast<uint4*>(p.out_q + row * p.N + n0 + 2 * j) = make_uint4(x.x, x.y, y.x, y.y);
+            }
+            if (hf == 0) p.out_sf[row * (p.N / BLOCK) + t.nb] = fp8::block_scale(a);
+          }
+          parity ^= 1;
+        }
+      } else if (valid && n0 < p.N) {
+        store64(p.out + row * p.N + n0, acc);
+        store64(p.out + row * p.N + n0 + 64, acc + 32);
+      }
     }
   }
-  if (!SWIGLU || !p.out_q) return;
+  tc::fence_before_sync();
   __syncthreads();
-  for (int i = threadIdx.x >> 5; i < BM; i += 8) {
-    uint32_t m = 0;
-    for (int j = threadIdx.x & 31; j < BLOCK; j += 32) m = max(m, fp8::mag_bits(sO[i][j]));
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) sTop[i] = fp8::block_top(m);
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem_base, 512);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < BM * 64; i += 256) {
-    const int64_t r = row0 + i / 64;
-    const int j = 2 * (i % 64);
-    if (r >= end) continue;
-    const float a = sTop[i / 64], d = a * 0x1p-9f;
-    *reinterpret_cast<uint16_t*>(p.out_q + r * p.N + col0 + j) = (uint16_t)fp8::codes2(
-        fp8::ratio(sO[i / 64][j], d), fp8::ratio(sO[i / 64][j + 1], d));
-    if (j == 0) p.out_sf[r * (p.N / BLOCK) + nb] = fp8::block_scale(a);
-  }
+}
+
+// 2-D uint8 [rows, cols] map with a {128, box_rows} box, 128-byte swizzle, zero fill.
+bool encode_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  tc::EncodeTiledFn fn = tc::encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {(cuuint32_t)BLOCK, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -138,20 +371,25 @@ cudaError_t launch_fp8_product(bool swiglu, int P, const uint8_t* a, const float
                                const int32_t* offsets, const float* prob, void* save, void* out,
                                uint8_t* out_q, float* out_sf, int sms, int* status,
                                cudaStream_t s) {
-  (void)sms;
-  (void)status;
   if (P == 0) return cudaSuccess;
-  Fp8Params p{};
-  p.offsets = offsets; p.prob = prob; p.a = a; p.a_sf = a_sf; p.w = w; p.w_sf = w_sf;
+  const int Nw = swiglu ? 2 * N : N;
+  CUtensorMap ma, mw;
+  if (!encode_u8(&ma, a, (uint64_t)P, (uint64_t)Kd, TM)) return cudaErrorInvalidValue;
+  if (!encode_u8(&mw, w, (uint64_t)E * Nw, (uint64_t)Kd, 128)) return cudaErrorInvalidValue;
+  TcParams p{};
+  p.offsets = offsets; p.prob = prob; p.a_sf = a_sf; p.w_sf = w_sf;
   p.save = static_cast<__nv_bfloat16*>(save); p.out = static_cast<__nv_bfloat16*>(out);
   p.out_q = out_q; p.out_sf = out_sf;
-  p.P = P; p.E = E; p.Kd = Kd; p.N = N; p.Nw = swiglu ? 2 * N : N;
-  const int nblk = swiglu ? N / BLOCK : (N + 255) / 256;
-  const int64_t tiles = (ceil_div(P, BM) + (E < P ? E : P)) * (int64_t)nblk;
-  if (swiglu)
-    fp8_product_simple_kernel<true><<<(unsigned)tiles, 256, 0, s>>>(p);
-  else
-    fp8_product_simple_kernel<false><<<(unsigned)tiles, 256, 0, s>>>(p);
+  p.P = P; p.E = E; p.KB = Kd / BLOCK; p.N = N; p.Nw = Nw;
+  p.status = status;
+  p.wait_limit_ns = 2000000000ull;
+  const int nblk = swiglu ? N / BLOCK : (N + TN - 1) / TN;
+  const int64_t tiles_max = (ceil_div(P, TM) + (E < P ? E : P)) * (int64_t)nblk;
+  const int grid = (int)(tiles_max < sms ? tiles_max : sms);
+  auto kern = swiglu ? fp8_product_kernel<true> : fp8_product_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, kSmem, s>>>(ma, mw, p);
   return cudaGetLastError();
 }
 
