@@ -80,7 +80,7 @@ size_t rmsnorm_bwd_workspace(int64_t rows, int h);
 cudaError_t launch_rmsnorm_fwd(int64_t, int, int, const void*, const void*, const float*, float,
                                void*, void*, uint8_t*, float*, float*, cudaStream_t);
 cudaError_t launch_rmsnorm_bwd(int64_t, int, int, const void*, const void*, const float*,
-                               const float*, const void*, void*, float*, float*, int,
+                               const float*, const void*, void*, float*, float*, int, int*,
                                cudaStream_t);
 cudaError_t launch_combine_bwd(const moe_config_t&, const void*, const void*, const int32_t*,
                                const float*, void*, float*, int*, cudaStream_t);
@@ -781,7 +781,7 @@ moe_status_t moe_rmsnorm_bwd(int64_t rows, int32_t h, int32_t dtype, const void*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows == 0) return cuda_status(cudaMemsetAsync(dw, 0, (size_t)h * 4, s));
   return cuda_status(launch_rmsnorm_bwd(rows, h, dtype, dy, sum, rstd, w, dsum, dx, dw,
-                                        static_cast<float*>(ws), d->sms, s));
+                                        static_cast<float*>(ws), d->sms, d->status, s));
 }
 
 moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,

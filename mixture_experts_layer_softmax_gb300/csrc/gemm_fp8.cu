@@ -321,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.meet[q]));
           if (!tc::mbar_wait(tc::smem_u32(&ctl.meet[q]), parity, wc)) break;
-          const float a = fp8::block_top(max(m, ctl.top[parity][hf ^ 1][i]));
+          const float a = fp8::block_top(max(m, ctl.top[parity][hf ^ 1][i])), inv = fp8::block_inverse(a);
           if (valid) {
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               float f[16];
 #pragma unroll
               for (int k = 0; k < 8; ++k) f[2 * k] = acc[j + k].x, f[2 * k + 1] = acc[j + k].y;
-              const uint2 x = fp8::codes8(f, a), y = fp8::codes8(f + 8, a);
+              const uint2 x = fp8::codes8(f, inv), y = fp8::codes8(f + 8, inv);
               *reinterpret_cast<uint4*>(p.out_q + row * p.N + n0 + 2 * j) = make_uint4(x.x, x.y, y.x, y.y);
             }
             if (hf == 0) p.out_sf[row * (p.N / BLOCK) + t.nb] = fp8::block_scale(a);

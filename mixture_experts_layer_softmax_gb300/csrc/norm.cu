@@ -7,6 +7,8 @@
 // (dsum: what arrives at v itself by the residual stream; x and res both get dv).
 // Sums are fp32 in a fixed order.
 #include "fp8.cuh"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -43,50 +45,84 @@ MOE_D void store8(float* p, int left, const float* v) {
   if (left > 4) *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Sum over the block's threads, in the same order for every thread; `slot` holds
-// a float a warp.
-MOE_D float block_sum(float v, float* slot) {
+// Eight columns as loaded: asked for together before any is used.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 a;
+  MOE_D void load(const __nv_bfloat16* p, int) { a = *reinterpret_cast<const uint4*>(p); }
+  MOE_D void zero() { a = make_uint4(0, 0, 0, 0); }
+  MOE_D void values(float* v) const {
+    v[0] = fp8::bf16_lo(a.x); v[1] = fp8::bf16_hi(a.x); v[2] = fp8::bf16_lo(a.y);
+    v[3] = fp8::bf16_hi(a.y); v[4] = fp8::bf16_lo(a.z); v[5] = fp8::bf16_hi(a.z);
+    v[6] = fp8::bf16_lo(a.w); v[7] = fp8::bf16_hi(a.w);
+  }
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  MOE_D void load(const float* p, int left) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (left > 4) b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  MOE_D void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  MOE_D void values(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+MOE_D float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int nw = blockDim.x >> 5;
-  if (nw == 1) return v;
-  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.f;
-  for (int i = 0; i < nw; ++i) t += slot[i];
-  __syncthreads();
-  return t;
+  return v;
 }
 
-// A block of threads a row, which stays in its registers (NV vectors a thread).
-template <typename T, int NV>
-__global__ void __launch_bounds__(1024)
-    rmsnorm_fwd_kernel(const T* x, const T* res, const float* __restrict__ w, float eps, int h,
-                       T* sum, T* y, uint8_t* __restrict__ q, float* __restrict__ sf,
-                       float* __restrict__ rstd) {
-  __shared__ float slot[32];
-  const int64_t row = blockIdx.x;
+// blockDim.x threads a row (whole warps, NV vectors a thread), blockDim.y rows a
+// block: a row stays in its threads' registers.  Bound by HBM: every byte moves once.
+template <typename T, int NV, int NT>
+__global__ void __launch_bounds__(NT)
+    rmsnorm_fwd_kernel(const T* x, const T* res, const float* __restrict__ w, float eps,
+                       int64_t rows, int h, T* sum, T* y, uint8_t* __restrict__ q,
+                       float* __restrict__ sf, float* __restrict__ rstd) {
+  __shared__ float slot[NT / 32];
   const int nt = blockDim.x;
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const bool here = row < rows;
+  Raw<T> a[NV], b[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + threadIdx.x) * kCols;
+    a[i].zero();
+    b[i].zero();
+    if (here && c < h) {
+      a[i].load(x + row * h + c, h - c);
+      if (res) b[i].load(res + row * h + c, h - c);
+    }
+  }
   float v[NV][kCols];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + threadIdx.x) * kCols;
+    a[i].values(v[i]);
+    if (res) {
+      float u[kCols];
+      b[i].values(u);
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) v[i][j] = 0.f;
-    if (c < h) {
-      load8(x + row * h + c, h - c, v[i]);
-      if (res) {
-        float u[kCols];
-        load8(res + row * h + c, h - c, u);
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) v[i][j] += u[j];
-      }
+      for (int j = 0; j < kCols; ++j) v[i][j] += u[j];
     }
 #pragma unroll
     for (int j = 0; j < kCols; ++j) ss = fmaf(v[i][j], v[i][j], ss);
   }
-  ss = block_sum(ss, slot);
+  ss = warp_sum(ss);
+  const int nw = nt >> 5;
+  if (nw > 1) {
+    const int first = threadIdx.y * nw;
+    if ((threadIdx.x & 31) == 0) slot[first + (threadIdx.x >> 5)] = ss;
+    __syncthreads();
+    ss = 0.f;
+    for (int i = 0; i < nw; ++i) ss += slot[first + i];
+  }
+  if (!here) return;  // (whole warps: the shuffles below are within a warp)
   const float r = 1.f / sqrtf(ss / (float)h + eps);
   if (rstd && threadIdx.x == 0) rstd[row] = r;
 #pragma unroll
@@ -108,59 +144,194 @@ __global__ void __launch_bounds__(1024)
       for (int j = 0; j < kCols; ++j) m = max(m, fp8::mag_bits(o[j]));
 #pragma unroll
       for (int s = 1; s < 16; s <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-      const float a = fp8::block_top(m);
+      const float top = fp8::block_top(m), inv = fp8::block_inverse(top);
       if (in) {
-        *reinterpret_cast<uint2*>(q + row * h + c) = fp8::codes8(o, a);
+        *reinterpret_cast<uint2*>(q + row * h + c) = fp8::codes8(o, inv);
         if ((threadIdx.x & 15) == 0)
-          sf[row * (h / fp8::BLOCK) + c / fp8::BLOCK] = fp8::block_scale(a);
+          sf[row * (h / fp8::BLOCK) + c / fp8::BLOCK] = fp8::block_scale(top);
       }
     }
   }
 }
 
-// A block of threads takes rows blockIdx.x, + gridDim.x, ...; each thread keeps
-// its columns' part of dw in registers and writes it once, to part[blockIdx.x].
+// ---- gradient ------------------------------------------------------------------
+// Rows of up to 8192 columns.  A persistent block: eight warps that take G rows at a
+// time, W = 8 / G warps a row, and one that brings the next G rows of dy, sum and dsum
+// (each a run of bytes) into a ring of shared-memory stages with bulk copies, as many
+// rows ahead as fit: the loads of a row that is to come never wait for a sum over the
+// present one.  Each thread keeps its columns' part of dw in registers and writes it
+// once, to part[block * G + group]; the parts are added in order by a second kernel.
+constexpr int kRing = 8;                 // stages at most
+constexpr int kRingBytes = 200 * 1024;   // shared memory of the stages
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(288, 1)
+    rmsnorm_bwd_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
+                       const float* __restrict__ w, const T* dsum, int64_t rows, int h, int W,
+                       int stages, T* dx, float* __restrict__ part, int* status) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kRing], empty[kRing];
+  __shared__ float slot[2][8];
+  __shared__ int abort[2], quit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = 8 / W, arrays = dsum ? 3 : 2;
+  const int64_t chunks = (rows + G - 1) / G;
+  const uint32_t chunk_bytes = (uint32_t)(G * h * sizeof(T)), stage_bytes = arrays * chunk_bytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      tc::mbar_init(tc::smem_u32(&full[s]), 1);
+      tc::mbar_init(tc::smem_u32(&empty[s]), 8);
+    }
+    abort[0] = abort[1] = quit = 0;
+    tc::fence_barrier_init();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    if (lane == 0) {
+      const tc::WaitCtl wc{status, &quit, 2000000000ull, 0};
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, par = 0;
+      for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        if (!tc::mbar_wait(tc::smem_u32(&empty[stage]), phase ^ 1, wc)) break;
+        const int64_t at = c * G * h, left = rows - c * G;
+        const uint32_t bytes = left < G ? (uint32_t)(left * h * sizeof(T)) : chunk_bytes;
+        const uint32_t fb = tc::smem_u32(&full[stage]);
+        const uint32_t dst = tc::smem_u32(ring) + stage * stage_bytes;
+        tc::mbar_arrive_expect_tx(fb, arrays * bytes);
+        tc::bulk_load(dst, dy + at, bytes, fb);
+        tc::bulk_load(dst + chunk_bytes, sum + at, bytes, fb);
+        if (dsum) tc::bulk_load(dst + 2 * chunk_bytes, dsum + at, bytes, fb);
+        issued |= 1u << stage;
+        par = (par & ~(1u << stage)) | (phase << stage);
+        if (++stage == stages) { stage = 0; phase ^= 1; }
+      }
+      const tc::WaitCtl wd{status, nullptr, 1000000000ull, 0};
+      for (int s = 0; s < stages; ++s)  // no copy is under way when the block ends
+        if ((issued >> s) & 1u) tc::mbar_wait(tc::smem_u32(&full[s]), (par >> s) & 1u, wd);
+    }
+    return;
+  }
+  const int g = warp / W, tx = (warp % W) * 32 + lane, nt = W * 32;
+  float ww[NV][kCols], acc[NV][kCols] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tx) * kCols;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) ww[i][j] = 0.f;
+    if (c < h) load8(w + c, h - c, ww[i]);
+  }
+  int stage = 0, parity = 0;
+  uint32_t phase = 0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x, parity ^= 1) {
+    const int64_t row = c * G + g;
+    const bool here = row < rows;
+    const float r = here ? __ldg(rstd + row) : 0.f;
+    // a wait that gave up is known to every warp behind the barrier below, by a flag of
+    // this chunk's parity (the next chunk's may be raised before all have read it)
+    const tc::WaitCtl wc{status, &abort[parity], 2000000000ull, 0};
+    tc::mbar_wait(tc::smem_u32(&full[stage]), phase, wc);
+    const T* s_dy = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes) + g * h;
+    const T* s_sum = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes + chunk_bytes) + g * h;
+    const T* s_ds = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes + 2 * chunk_bytes) + g * h;
+    float n[NV][kCols], gy[NV][kCols];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * nt + tx) * kCols;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) n[i][j] = gy[i][j] = 0.f;
+      if (here && col < h) {
+        load8(s_sum + col, h - col, n[i]);
+        load8(s_dy + col, h - col, gy[i]);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          n[i][j] *= r;
+          acc[i][j] = fmaf(gy[i][j], n[i][j], acc[i][j]);
+          gy[i][j] *= ww[i][j];
+          dot = fmaf(gy[i][j], n[i][j], dot);
+        }
+      }
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) slot[parity][warp] = dot;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (abort[parity]) {
+      quit = 1;
+      break;
+    }
+    dot = 0.f;
+    for (int i = 0; i < W; ++i) dot += slot[parity][g * W + i];
+    const float mean = dot / (float)h;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int col = (i * nt + tx) * kCols;
+      if (here && col < h) {
+        float o[kCols], d[kCols] = {};
+        if (dsum) load8(s_ds + col, h - col, d);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[i][j], mean, gy[i][j]), d[j]);
+        store8(dx + row * h + col, h - col, o);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&empty[stage]));
+    if (++stage == stages) { stage = 0; phase ^= 1; }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int col = (i * nt + tx) * kCols;
+    if (col < h) store8(part + ((int64_t)blockIdx.x * G + g) * h + col, h - col, acc[i]);
+  }
+}
+
+// Longer rows: a block of threads takes rows blockIdx.x, + gridDim.x, ...
 template <typename T, int NV>
 __global__ void __launch_bounds__(1024)
-    rmsnorm_bwd_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
-                       const float* __restrict__ w, const T* dsum, int64_t rows, int h, T* dx,
-                       float* __restrict__ part) {
-  __shared__ float slot[32];
-  const int nt = blockDim.x;
+    rmsnorm_bwd_long_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
+                            const float* __restrict__ w, const T* dsum, int64_t rows, int h, T* dx,
+                            float* __restrict__ part) {
+  __shared__ float slot[2][32];
+  const int nt = blockDim.x, nw = nt >> 5;
   float acc[NV][kCols] = {};
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
     const float r = __ldg(rstd + row);
-    float n[NV][kCols], g[NV][kCols];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * nt + threadIdx.x) * kCols;
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) n[i][j] = g[i][j] = 0.f;
       if (c < h) {
-        float ww[kCols];
-        load8(sum + row * h + c, h - c, n[i]);
-        load8(dy + row * h + c, h - c, g[i]);
+        float n[kCols], g[kCols], ww[kCols];
+        load8(sum + row * h + c, h - c, n);
+        load8(dy + row * h + c, h - c, g);
         load8(w + c, h - c, ww);
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
-          n[i][j] *= r;
-          acc[i][j] = fmaf(g[i][j], n[i][j], acc[i][j]);
-          g[i][j] *= ww[j];
-          dot = fmaf(g[i][j], n[i][j], dot);
+          n[j] *= r;
+          acc[i][j] = fmaf(g[j], n[j], acc[i][j]);
+          dot = fmaf(g[j] * ww[j], n[j], dot);
         }
       }
     }
-    const float mean = block_sum(dot, slot) / (float)h;
+    dot = warp_sum(dot);
+    if ((threadIdx.x & 31) == 0) slot[parity][threadIdx.x >> 5] = dot;
+    __syncthreads();
+    dot = 0.f;
+    for (int i = 0; i < nw; ++i) dot += slot[parity][i];
+    const float mean = dot / (float)h;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * nt + threadIdx.x) * kCols;
       if (c < h) {
-        float o[kCols], d[kCols] = {};
+        float n[kCols], g[kCols], ww[kCols], d[kCols] = {};
+        load8(sum + row * h + c, h - c, n);
+        load8(dy + row * h + c, h - c, g);
+        load8(w + c, h - c, ww);
         if (dsum) load8(dsum + row * h + c, h - c, d);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[i][j], mean, g[i][j]), d[j]);
-        store8(dx + row * h + c, h - c, o);
+        for (int j = 0; j < kCols; ++j) g[j] = fmaf(r, fmaf(-(n[j] * r), mean, g[j] * ww[j]), d[j]);
+        store8(dx + row * h + c, h - c, g);
       }
     }
   }
@@ -172,70 +343,111 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// dw = the parts added in order, a thread a column.
-__global__ void __launch_bounds__(128)
+// dw: 32 columns a block, each summed by 16 threads over every 16th part and then
+// over the threads, in order.
+__global__ void __launch_bounds__(512)
     rmsnorm_dw_kernel(const float* __restrict__ part, int parts, int h, float* __restrict__ dw) {
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= h) return;
-  float s = 0.f;
-  for (int i = 0; i < parts; ++i) s += __ldg(part + (int64_t)i * h + c);
-  dw[c] = s;
+  __shared__ float s[16][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  pdl_wait();
+  float v = 0.f;
+  if (c < h) {
+#pragma unroll 4
+    for (int i = threadIdx.y; i < parts; i += 16) v += __ldg(part + (int64_t)i * h + c);
+  }
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y || c >= h) return;
+  v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v += s[i][threadIdx.x];
+  dw[c] = v;
 }
 
-constexpr int kMaxParts = 512;
+constexpr int kMaxBlocks = 256;  // of the gradient's first kernel
 
-// Vectors a thread and threads a block for rows of h columns.
-struct Shape {
-  int nv, threads;
-};
-Shape row_shape(int h) {
-  const int nvec = (int)ceil_div(h, kCols);
-  int nv = 1;
-  while (nv < 8 && ceil_div(nvec, nv) > (nv < 4 ? 256 : 1024)) nv *= 2;
-  return {nv, (int)align_up((size_t)ceil_div(nvec, nv), 32)};
+// Warps a row in the gradient: the fewest that hold it in 4 vectors a thread.
+int bwd_warps(int h) {
+  int w = 1;
+  while (w < 8 && h > w * 32 * 4 * kCols) w *= 2;
+  return w;
+}
+constexpr int kBwdMaxCols = 8 * 32 * 4 * kCols;
+
+template <typename T, int NV, int NT>
+cudaError_t fwd_launch(int64_t rows, int h, int threads, const void* x, const void* res,
+                       const float* w, float eps, void* sum, void* y, uint8_t* q, float* sf,
+                       float* rstd, cudaStream_t s) {
+  // short rows: several a block, up to 128 threads
+  const int per = threads >= 128 ? 1 : 128 / threads;
+  rmsnorm_fwd_kernel<T, NV, NT><<<(unsigned)ceil_div(rows, per), dim3(threads, per), 0, s>>>(
+      static_cast<const T*>(x), static_cast<const T*>(res), w, eps, rows, h, static_cast<T*>(sum),
+      static_cast<T*>(y), q, sf, rstd);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t fwd_t(int64_t rows, int h, const void* x, const void* res, const float* w, float eps,
                   void* sum, void* y, uint8_t* q, float* sf, float* rstd, cudaStream_t s) {
-  const Shape sh = row_shape(h);
-#define MOE_NF(NV)                                                                                \
-  rmsnorm_fwd_kernel<T, NV><<<(unsigned)rows, sh.threads, 0, s>>>(                                \
-      static_cast<const T*>(x), static_cast<const T*>(res), w, eps, h, static_cast<T*>(sum),      \
-      static_cast<T*>(y), q, sf, rstd)
-  if (sh.nv == 1) MOE_NF(1);
-  else if (sh.nv == 2) MOE_NF(2);
-  else if (sh.nv == 4) MOE_NF(4);
-  else MOE_NF(8);
+  const int nvec = (int)ceil_div(h, kCols);
+  auto threads = [&](int nv) { return (int)align_up((size_t)ceil_div(nvec, nv), 32); };
+#define MOE_NF(NV, NT) \
+  return fwd_launch<T, NV, NT>(rows, h, threads(NV), x, res, w, eps, sum, y, q, sf, rstd, s)
+  if (nvec <= 128) MOE_NF(1, 128);
+  if (nvec <= 256) MOE_NF(2, 128);
+  if (nvec <= 1024) MOE_NF(4, 256);
+  if (nvec <= 4096) MOE_NF(4, 1024);
+  MOE_NF(8, 1024);
 #undef MOE_NF
-  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const float* rstd,
                   const float* w, const void* dsum, void* dx, float* dw, float* part, int sms,
-                  cudaStream_t s) {
-  const Shape sh = row_shape(h);
-  const int64_t want = rows < 2LL * sms ? rows : 2LL * sms;
-  const unsigned grid = (unsigned)(want < kMaxParts ? want : kMaxParts);
-#define MOE_NB(NV)                                                                                \
-  rmsnorm_bwd_kernel<T, NV><<<grid, sh.threads, 0, s>>>(                                          \
-      static_cast<const T*>(dy), static_cast<const T*>(sum), rstd, w,                             \
-      static_cast<const T*>(dsum), rows, h, static_cast<T*>(dx), dw ? part : nullptr)
-  if (sh.nv == 1) MOE_NB(1);
-  else if (sh.nv == 2) MOE_NB(2);
-  else if (sh.nv == 4) MOE_NB(4);
-  else MOE_NB(8);
-#undef MOE_NB
-  if (dw) rmsnorm_dw_kernel<<<(unsigned)ceil_div(h, 128), 128, 0, s>>>(part, (int)grid, h, dw);
-  return cudaGetLastError();
+                  int* status, cudaStream_t s) {
+  const T* a = static_cast<const T*>(dy);
+  const T* b = static_cast<const T*>(sum);
+  const T* d = static_cast<const T*>(dsum);
+  T* o = static_cast<T*>(dx);
+  float* pt = dw ? part : nullptr;
+  const int most = sms < kMaxBlocks ? sms : kMaxBlocks;
+  int parts;
+  if (h <= kBwdMaxCols) {
+    const int W = bwd_warps(h), G = 8 / W;
+    const int64_t chunks = ceil_div(rows, G);
+    const unsigned grid = (unsigned)(chunks < most ? chunks : most);
+    const size_t stage = (size_t)G * h * sizeof(T) * (d ? 3 : 2);
+    const int stages = (int)(kRingBytes / stage < kRing ? kRingBytes / stage : kRing);
+    auto kern = h <= W * 256 ? rmsnorm_bwd_kernel<T, 1>
+                             : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2> : rmsnorm_bwd_kernel<T, 4>;
+    const size_t smem = stages * stage;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, 288, smem, s>>>(a, b, rstd, w, d, rows, h, W, stages, o, pt, status);
+    parts = (int)grid * G;
+  } else {
+    const unsigned grid = (unsigned)(rows < most ? rows : most);
+    const int nvec = (int)ceil_div(h, kCols);
+    if (nvec <= 4096)
+      rmsnorm_bwd_long_kernel<T, 4><<<grid, (unsigned)align_up(ceil_div(nvec, 4), 32), 0, s>>>(
+          a, b, rstd, w, d, rows, h, o, pt);
+    else
+      rmsnorm_bwd_long_kernel<T, 8><<<grid, (unsigned)align_up(ceil_div(nvec, 8), 32), 0, s>>>(
+          a, b, rstd, w, d, rows, h, o, pt);
+    parts = (int)grid;
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !dw) return e;
+  return pdl_launch(rmsnorm_dw_kernel, dim3((unsigned)ceil_div(h, 32)), dim3(32, 16), 0, s,
+                    (const float*)part, parts, h, dw);
 }
 
 }  // namespace
 
 size_t rmsnorm_bwd_workspace(int64_t rows, int h) {
-  const int64_t parts = rows < kMaxParts ? rows : kMaxParts;
-  return align_up((size_t)parts * h * 4, 256);
+  const int G = h <= kBwdMaxCols ? 8 / bwd_warps(h) : 1;
+  const int64_t chunks = ceil_div(rows, G), blocks = chunks < kMaxBlocks ? chunks : kMaxBlocks;
+  return align_up((size_t)(blocks * G) * h * 4, 256);
 }
 
 cudaError_t launch_rmsnorm_fwd(int64_t rows, int h, int dtype, const void* x, const void* res,
@@ -248,10 +460,10 @@ cudaError_t launch_rmsnorm_fwd(int64_t rows, int h, int dtype, const void* x, co
 
 cudaError_t launch_rmsnorm_bwd(int64_t rows, int h, int dtype, const void* dy, const void* sum,
                                const float* rstd, const float* w, const void* dsum, void* dx,
-                               float* dw, float* part, int sms, cudaStream_t s) {
+                               float* dw, float* part, int sms, int* status, cudaStream_t s) {
   if (dtype == MOE_BF16)
-    return bwd_t<__nv_bfloat16>(rows, h, dy, sum, rstd, w, dsum, dx, dw, part, sms, s);
-  return bwd_t<float>(rows, h, dy, sum, rstd, w, dsum, dx, dw, part, sms, s);
+    return bwd_t<__nv_bfloat16>(rows, h, dy, sum, rstd, w, dsum, dx, dw, part, sms, status, s);
+  return bwd_t<float>(rows, h, dy, sum, rstd, w, dsum, dx, dw, part, sms, status, s);
 }
 
 }  // namespace moe
