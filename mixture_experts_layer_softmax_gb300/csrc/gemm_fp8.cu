@@ -39,7 +39,7 @@ struct Ctl {
   uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], meet[4], drain;
   uint32_t tmem_base;
   int abort;
-  int off[257], tile_start[257];
+  int off[257], tile_start[257], part[8];
   uint32_t top[2][2][TM];  // tile parity, half of the columns, row
 };
 constexpr size_t kSmem = 1024 + (size_t)STAGES * (A_BYTES + W_BYTES) + sizeof(Ctl);
@@ -90,44 +90,49 @@ MOE_D void store64(__nv_bfloat16* dst, const float2* v) {
 struct Tile {
   int e, row, rows, nb;  // expert, first row, rows of the expert from there, column tile
 };
-MOE_D Tile tile_at(const Ctl& c, int E, int tile) {
+template <int ROWS, class C> MOE_D Tile tile_at(const C& c, int E, int tile) {
   int lo = 0, hi = E - 1;  // largest e with tile_start[e] <= tile
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (c.tile_start[mid] <= tile) lo = mid; else hi = mid - 1;
   }
   const int local = tile - c.tile_start[lo], n = c.off[lo + 1] - c.off[lo];
-  const int mblk = (n + TM - 1) / TM;
+  const int mblk = (n + ROWS - 1) / ROWS;
   const int nb = local / mblk, mb = local - nb * mblk;
-  return {lo, c.off[lo] + mb * TM, n - mb * TM, nb};
+  return {lo, c.off[lo] + mb * ROWS, n - mb * ROWS, nb};
 }
 
-// Expert boundaries kept within the rows and ascending, and the tiles before
-// each expert (nblk column tiles a row tile).  One warp; off[] is loaded.
-MOE_D void scan_tiles(Ctl& c, int E, int nblk, int lane) {
-  int run_t = 0, run_o = c.off[0];
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + lane;
-    int end = max(run_o, e < E ? c.off[e + 1] : 0);
+// Expert boundaries kept within the rows and ascending (c.off), and the tiles before
+// each expert (c.tile_start; nblk column tiles for every ROWS of its rows).  Every
+// thread of the block calls it, at least 256; thread e has expert e.
+template <int ROWS, class C>
+MOE_D void load_tiles(C& c, const int32_t* __restrict__ offsets, int E, int P, int nblk) {
+  const int e = threadIdx.x, lane = e & 31, w = e >> 5;
+  const int first = min(max(__ldg(offsets), 0), P);
+  int end = e < E ? max(min(max(__ldg(offsets + e + 1), 0), P), first) : first;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end = max(end, t);
-    }
-    const int prev = __shfl_up_sync(0xffffffffu, end, 1), beg = lane ? prev : run_o;
-    if (e < E) c.off[e + 1] = end;
-    run_o = __shfl_sync(0xffffffffu, end, 31);
-    const int tiles = (end - beg + TM - 1) / TM * nblk;
-    int it = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, it, o);
-      if (lane >= o) it += t;
-    }
-    if (e < E) c.tile_start[e] = run_t + it - tiles;
-    run_t += __shfl_sync(0xffffffffu, it, 31);
+  for (int o = 1; o < 32; o <<= 1) {  // an expert's end: the largest offset so far
+    const int t = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end = max(end, t);
   }
-  if (lane == 0) c.tile_start[E] = run_t;
+  if (lane == 31 && w < 8) c.part[w] = end;
+  __syncthreads();
+  for (int i = 0; i < min(w, 8); ++i) end = max(end, c.part[i]);
+  if (e < E) c.off[e + 1] = end;
+  if (e == 0) c.off[0] = first;
+  __syncthreads();
+  const int tiles = e < E ? (end - c.off[e] + ROWS - 1) / ROWS * nblk : 0;
+  int sum = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += t;
+  }
+  if (lane == 31 && w < 8) c.part[w] = sum;
+  __syncthreads();
+  for (int i = 0; i < min(w, 8); ++i) sum += c.part[i];
+  if (e < E) c.tile_start[e] = sum - tiles;
+  if (e == E - 1) c.tile_start[E] = sum;
 }
 
 template <bool SWIGLU>
@@ -166,9 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), 512);
     tc::tmem_relinquish();
   }
-  for (int e = threadIdx.x; e <= E; e += kThreads) ctl.off[e] = min(max(__ldg(p.offsets + e), 0), p.P);
-  __syncthreads();
-  if (warp == 2) scan_tiles(ctl, E, nblk, lane);
+  load_tiles<TM>(ctl, p.offsets, E, p.P, nblk);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const Tile t = tile_at(ctl, E, tile);
+      const Tile t = tile_at<TM>(ctl, E, tile);
       const int w0 = t.e * p.Nw + (SWIGLU ? t.nb * BLOCK : t.nb * TN);
       // the second half: FC1's up rows; FC2's next 128 rows, where an odd last tile
       // takes rows of the next expert (or, past the tensor, zeros) that go nowhere
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t step = 0, parity = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const Tile t = tile_at(ctl, E, tile);
+      const Tile t = tile_at<TM>(ctl, E, tile);
       const int n0 = SWIGLU ? t.nb * BLOCK + hf * 64 : t.nb * TN + hf * 128;  // first column
       // the row's scales and the weight blocks' (FC1: gate and up), one block ahead.  (A
       // row behind the expert's takes its last row's, a column block behind FC2's last
@@ -349,6 +352,289 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---- a few rows an expert --------------------------------------------------------
+// The time is the weights' bytes, so the weights are the MMAs' 128 rows and up to 16
+// of an expert's tokens their columns: a unit is 128 output columns (FC1: of the gate
+// and of the up rows) of at most 16 tokens, a stage 128 weight rows x 256 columns of K
+// (256 consecutive bytes a row for the DRAM; FC1's stages take gate and up in turn).
+// A block's products are then 128 x 16, which four warps join in a few cycles, and
+// eight accumulators stand ready, so that no MMA waits for one.
+//   warp 0     TMA producer, 6 stages
+//   warp 1     TMEM owner and MMA issuer
+//   warp 2     scales: the products sa sw of each token and block, to shared memory
+//   warps 4-7  a TMEM lane quarter each; a thread is one output column
+constexpr int FT = 16, FSTAGES = 6, FBUFS = 8, FS = 16;
+constexpr int F_W_BYTES = 2 * BLOCK * BLOCK, F_A_BYTES = 2 * FT * BLOCK;
+constexpr int kFewThreads = 256;
+constexpr int kFewRows = 16;  // rows an expert, on average, up to which this kernel is taken
+
+struct FewCtl {
+  float scale[FS][2][FT];  // ring of stages: sa sw of the stage's two blocks
+  uint64_t full[FSTAGES], empty[FSTAGES], tfull[FBUFS], tempty[FBUFS], sfull[FS], sempty[FS], meet, drain;
+  uint32_t tmem_base;
+  int abort;
+  int off[257], tile_start[257], part[8];
+  uint32_t top[2][4][FT];  // unit parity, warp, token
+};
+constexpr size_t kFewSmem = 1024 + (size_t)FSTAGES * (F_W_BYTES + F_A_BYTES) + sizeof(FewCtl);
+static_assert(kFewSmem <= 227 * 1024, "shared memory");
+
+// acc[j] += t[j] s[j] for the 16 tokens.
+MOE_D void join_few(float (&acc)[FT], const uint32_t (&t)[FT], const float* s) {
+#pragma unroll
+  for (int j = 0; j < FT; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(s + j);
+    acc[j] = fmaf(__uint_as_float(t[j]), v.x, acc[j]);
+    acc[j + 1] = fmaf(__uint_as_float(t[j + 1]), v.y, acc[j + 1]);
+    acc[j + 2] = fmaf(__uint_as_float(t[j + 2]), v.z, acc[j + 2]);
+    acc[j + 3] = fmaf(__uint_as_float(t[j + 3]), v.w, acc[j + 3]);
+  }
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    fp8_product_few_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmW, const TcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sW = smem;
+  uint8_t* sA = sW + FSTAGES * F_W_BYTES;
+  FewCtl& ctl = *reinterpret_cast<FewCtl*>(sA + FSTAGES * F_A_BYTES);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p.E, KB = p.KB;
+  const int nblk = p.N / BLOCK;
+  const int KS = (SWIGLU ? 2 : 1) * ((KB + 1) / 2);  // stages of a unit
+  // stage ks: FC1 gate (even) or up (odd); its blocks 2 pair and, where there is one, 2 pair + 1
+  const auto pair_of = [](int ks) { return SWIGLU ? ks >> 1 : ks; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < FSTAGES; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.full[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.empty[s]), 1);
+    }
+    for (int b = 0; b < FBUFS; ++b) {
+      tc::mbar_init(tc::smem_u32(&ctl.tfull[b]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.tempty[b]), 4);
+    }
+    for (int s = 0; s < FS; ++s) {
+      tc::mbar_init(tc::smem_u32(&ctl.sfull[s]), 1);
+      tc::mbar_init(tc::smem_u32(&ctl.sempty[s]), 4);
+    }
+    tc::mbar_init(tc::smem_u32(&ctl.meet), 4);
+    tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
+    ctl.abort = 0;
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+    tc::prefetch_tensormap(&tmA);
+    tc::prefetch_tensormap(&tmW);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), FBUFS * 2 * FT);
+    tc::tmem_relinquish();
+  }
+  load_tiles<FT>(ctl, p.offsets, E, p.P, nblk);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem_base = ctl.tmem_base;
+  const int total = ctl.tile_start[E];
+  tc::WaitCtl wc{p.status, &ctl.abort, p.wait_limit_ns, 0};
+  tc::WaitCtl wdrain{p.status, nullptr, 1000000000ull, 0};
+
+  if (warp == 0) {
+    const bool elected = tc::elect_one();
+    const uint64_t policy = tc::evict_first_policy();
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, issued_par = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const Tile t = tile_at<FT>(ctl, E, tile);
+      const int w0 = t.e * p.Nw + t.nb * BLOCK;
+      for (int ks = 0; ks < KS; ++ks) {
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
+        if (elected) {
+          const uint32_t fb = tc::smem_u32(&ctl.full[stage]);
+          const uint32_t wd = tc::smem_u32(sW + stage * F_W_BYTES), ad = tc::smem_u32(sA + stage * F_A_BYTES);
+          const int kb = 2 * pair_of(ks), blocks = kb + 1 < KB ? 2 : 1;
+          const int wr = SWIGLU && (ks & 1) ? w0 + p.N : w0;
+          tc::mbar_arrive_expect_tx(fb, blocks * (BLOCK + FT) * BLOCK);
+          for (int b = 0; b < blocks; ++b)
+            tc::tma_load_2d_hint(wd + b * (BLOCK * BLOCK), &tmW, (kb + b) * BLOCK, wr, fb, policy);
+          for (int b = 0; b < blocks; ++b)
+            tc::tma_load_2d(ad + b * (FT * BLOCK), &tmA, (kb + b) * BLOCK, t.row, fb);
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == FSTAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    for (int s = 0; s < FSTAGES; ++s)
+      if ((issued >> s) & 1u)
+        tc::mbar_wait(tc::smem_u32(&ctl.full[s]), (issued_par >> s) & 1u, wdrain);
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool elected = tc::elect_one();
+    int stage = 0;
+    uint32_t phase = 0, step = 0;
+    bool ok = true;
+    const uint64_t a_base = tc::desc_kmajor_sw128(tc::smem_u32(sA));
+    const uint64_t w_base = tc::desc_kmajor_sw128(tc::smem_u32(sW));
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int ks = 0; ks < KS; ++ks, ++step) {
+        const uint32_t buf = step % FBUFS;
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.tempty[buf]), ((step / FBUFS) & 1) ^ 1, wc) ||
+            !tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), phase, wc)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint64_t ad = a_base + (uint32_t)(stage * (F_A_BYTES >> 4));
+        const uint64_t wd = w_base + (uint32_t)(stage * (F_W_BYTES >> 4));
+        const uint32_t d = tmem_base + buf * (2 * FT);
+        const bool two = 2 * pair_of(ks) + 1 < KB;
+        if (elected) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f8(d, wd + 2 * k, ad + 2 * k, tc::idesc_e4m3_f32(BLOCK, FT), k != 0);
+          if (two) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_f8(d + FT, wd + (BLOCK * BLOCK >> 4) + 2 * k, ad + (FT * BLOCK >> 4) + 2 * k,
+                         tc::idesc_e4m3_f32(BLOCK, FT), k != 0);
+          }
+          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+          tc::mma_commit(tc::smem_u32(&ctl.tfull[buf]));
+        }
+        __syncwarp();
+        if (++stage == FSTAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    __syncwarp();
+    if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
+      if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain));
+      tc::mbar_wait(tc::smem_u32(&ctl.drain), 0, wdrain);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // lane = token + 16 (first or second block of the stage); four stages asked for at a time
+    const int tok = lane & 15, half = lane >> 4;
+    uint32_t step = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const Tile t = tile_at<FT>(ctl, E, tile);
+      const int wblk = p.Nw / BLOCK;
+      // (a token behind the expert's takes its last one's scales, which go nowhere)
+      const float* sa = p.a_sf + (int64_t)(t.row + min(tok, t.rows - 1)) * KB;
+      const float* sw = p.w_sf + ((int64_t)t.e * wblk + t.nb) * KB;
+      for (int k0 = 0; k0 < KS && ok; k0 += 4) {
+        float s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = min(2 * pair_of(k0 + j) + half, KB - 1);
+          s[j] = __ldg(sa + k) * __ldg(sw + (SWIGLU && (j & 1) ? (int64_t)(wblk / 2) * KB : 0) + k);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (k0 + j >= KS) break;
+          const uint32_t r = step % FS;
+          if (!tc::mbar_wait(tc::smem_u32(&ctl.sempty[r]), ((step / FS) & 1) ^ 1, wc)) { ok = false; break; }
+          ctl.scale[r][half][tok] = s[j];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sfull[r]));
+          ++step;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3;
+    const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
+    uint32_t step = 0, parity = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const Tile t = tile_at<FT>(ctl, E, tile);
+      float acc[FT], up[FT];
+#pragma unroll
+      for (int j = 0; j < FT; ++j) acc[j] = up[j] = 0.f;
+      for (int ks = 0; ks < KS; ++ks, ++step) {
+        const uint32_t buf = step % FBUFS, s = step % FS;
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.sfull[s]), (step / FS) & 1, wc) ||
+            !tc::mbar_wait(tc::smem_u32(&ctl.tfull[buf]), (step / FBUFS) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint32_t d = tbase + buf * (2 * FT);
+        uint32_t v[FT], w[FT];
+        tmem_ld(d, v);
+        tmem_ld(d + FT, w);  // (without a second block, what an earlier stage left)
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tempty[buf]));
+        const bool two = 2 * pair_of(ks) + 1 < KB;
+        if (SWIGLU && (ks & 1)) {
+          join_few(up, v, ctl.scale[s][0]);
+          if (two) join_few(up, w, ctl.scale[s][1]);
+        } else {
+          join_few(acc, v, ctl.scale[s][0]);
+          if (two) join_few(acc, w, ctl.scale[s][1]);
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sempty[s]));
+      }
+      if (!ok) break;
+      const int n = t.nb * BLOCK + q * 32 + lane;  // this thread's column
+      uint32_t m = 0;                              // lane's token's largest magnitude in the warp's columns
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        if (j >= t.rows) break;
+        const int64_t row = t.row + j;
+        if (SWIGLU) {
+          if (p.save) {
+            p.save[row * p.Nw + n] = from_f32<__nv_bfloat16>(acc[j]);
+            p.save[row * p.Nw + p.N + n] = from_f32<__nv_bfloat16>(up[j]);
+          }
+          acc[j] = (p.prob ? __ldg(p.prob + row) : 1.f) * (silu_f32(acc[j]) * up[j]);
+          if (p.out_q) {
+            const uint32_t r = __reduce_max_sync(0xffffffffu, fp8::mag_bits(acc[j]));
+            if (lane == j) m = r;
+          }
+        }
+        if (p.out) p.out[row * p.N + n] = from_f32<__nv_bfloat16>(acc[j]);
+      }
+      if (SWIGLU && p.out_q) {
+        // a unit's 128 columns are one block of each token: its four warps meet, and
+        // each lane has a token's scale; a buffer is written again two units on, behind
+        // the next unit's meeting
+        if (lane < FT) ctl.top[parity][q][lane] = m;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.meet));
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.meet), parity, wc)) break;
+        const uint32_t(&tp)[4][FT] = ctl.top[parity];
+        const int k = lane & (FT - 1);
+        const float a = fp8::block_top(max(max(tp[0][k], tp[1][k]), max(tp[2][k], tp[3][k])));
+        const float inv = fp8::block_inverse(a);
+        if (q == 0 && lane < min(t.rows, FT)) p.out_sf[(int64_t)(t.row + lane) * nblk + t.nb] = fp8::block_scale(a);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) {
+          if (j >= t.rows) break;
+          p.out_q[(int64_t)(t.row + j) * p.N + n] =
+              (uint8_t)fp8::codes2(acc[j] * __shfl_sync(0xffffffffu, inv, j), 0.f);
+        }
+        parity ^= 1;
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem_base, FBUFS * 2 * FT);
+  }
+}
+
 // 2-D uint8 [rows, cols] map with a {128, box_rows} box, 128-byte swizzle, zero fill.
 bool encode_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   tc::EncodeTiledFn fn = tc::encode_tiled_fn();
@@ -373,9 +659,10 @@ cudaError_t launch_fp8_product(bool swiglu, int P, const uint8_t* a, const float
                                cudaStream_t s) {
   if (P == 0) return cudaSuccess;
   const int Nw = swiglu ? 2 * N : N;
+  const bool few = P <= (int64_t)kFewRows * E;
   CUtensorMap ma, mw;
-  if (!encode_u8(&ma, a, (uint64_t)P, (uint64_t)Kd, TM)) return cudaErrorInvalidValue;
-  if (!encode_u8(&mw, w, (uint64_t)E * Nw, (uint64_t)Kd, 128)) return cudaErrorInvalidValue;
+  if (!encode_u8(&ma, a, (uint64_t)P, (uint64_t)Kd, few ? 16 : TM)) return cudaErrorInvalidValue;
+  if (!encode_u8(&mw, w, (uint64_t)E * Nw, (uint64_t)Kd, BLOCK)) return cudaErrorInvalidValue;
   TcParams p{};
   p.offsets = offsets; p.prob = prob; p.a_sf = a_sf; p.w_sf = w_sf;
   p.save = static_cast<__nv_bfloat16*>(save); p.out = static_cast<__nv_bfloat16*>(out);
@@ -383,13 +670,16 @@ cudaError_t launch_fp8_product(bool swiglu, int P, const uint8_t* a, const float
   p.P = P; p.E = E; p.KB = Kd / BLOCK; p.N = N; p.Nw = Nw;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;
-  const int nblk = swiglu ? N / BLOCK : (N + TN - 1) / TN;
-  const int64_t tiles_max = (ceil_div(P, TM) + (E < P ? E : P)) * (int64_t)nblk;
+  const int nblk = swiglu || few ? N / BLOCK : (N + TN - 1) / TN;
+  const int64_t tiles_max = (ceil_div(P, few ? FT : TM) + (E < P ? E : P)) * (int64_t)nblk;
   const int grid = (int)(tiles_max < sms ? tiles_max : sms);
-  auto kern = swiglu ? fp8_product_kernel<true> : fp8_product_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  auto kern = few ? (swiglu ? fp8_product_few_kernel<true> : fp8_product_few_kernel<false>)
+                  : (swiglu ? fp8_product_kernel<true> : fp8_product_kernel<false>);
+  const int threads = few ? kFewThreads : kThreads;
+  const size_t smem = few ? kFewSmem : kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, kSmem, s>>>(ma, mw, p);
+  kern<<<grid, threads, smem, s>>>(ma, mw, p);
   return cudaGetLastError();
 }
 

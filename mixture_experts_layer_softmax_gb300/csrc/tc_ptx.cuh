@@ -170,6 +170,21 @@ MOE_D void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
+// The same with an L2 cache policy.
+MOE_D void tma_load_2d_hint(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1,
+                            uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+// Data that is read once: the first to leave the L2.
+MOE_D uint64_t evict_first_policy() {
+  uint64_t v;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(v));
+  return v;
+}
 // Four rows of a 2-D tensor (box one row high): rows r0..r3 at column c0,
 // written to shared memory one after the other (the map's swizzle applies by
 // shared-memory address, as for a 4-row box).
