@@ -11,6 +11,9 @@
 //   warp 0     TMA producer: 4 stages of {A 128 x 128 B, W 256 x 128 B}.
 //   warp 1     TMEM owner and MMA issuer: a stage's products go to one of two
 //              256-column accumulators, each given back once a block.
+//   warps 2-3  scales: each row's sa sw of eight blocks at a time, to shared memory
+//              (a joining thread that reads its own row's scales touches a line of its
+//              own with each, and keeps registers for them).
 //   warps 4-11 two warps a TMEM lane quarter (32 rows), each one half of the
 //              columns: a thread keeps 128 fp32 sums of one row.
 // While they evaluate and store a tile the MMAs run at most two blocks ahead.
@@ -32,11 +35,14 @@ constexpr int STAGES = 4;
 constexpr int kThreads = 384;
 // Registers a thread: 384 x 168 at launch; the first warpgroup gives some back and
 // the joining ones take them.
-constexpr int kRegsIssue = 56, kRegsJoin = 224;
+constexpr int kRegsIssue = 88, kRegsJoin = 208;
 static_assert(kRegsIssue + 2 * kRegsJoin <= 3 * 168, "more registers than the launch brings");
 
+constexpr int SB = 8;  // blocks of scales at a time
+
 struct Ctl {
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], meet[4], drain;
+  float2 scale[2][SB][TM + 4];  // [block][row]: sa times the scales of the tile's two weight blocks
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], sfull[2], sempty[2], meet[4], drain;
   uint32_t tmem_base;
   int abort;
   int off[257], tile_start[257], part[8];
@@ -55,6 +61,8 @@ struct TcParams {
   uint8_t* out_q;          // FC1: [P, N] or null
   float* out_sf;           // FC1: [P, N/128]
   int P, E, KB, N, Nw;     // KB: blocks of K; Nw: weight rows an expert (2N or N)
+  bool wide;               // every output is 32-byte aligned (their rows are multiples of 64 bytes)
+  bool once;               // weights are read about once: they leave the L2 first
   int* status;
   uint64_t wait_limit_ns;
 };
@@ -78,13 +86,27 @@ MOE_D uint32_t pack_bf16x2(float a, float b) {
 // SiLU with CUDA's expf and the approximate quotient, bounded by 2 ulp; a quotient
 // below 2^-126 (z < -87) is 0.
 MOE_D float silu_f32(float z) { return z * __fdividef(1.f, 1.f + expf(-z)); }
+// 32 bytes of a row: one store where the row is 32-byte aligned (a warp's rows are
+// lines apart, so its stores cost by their number: 16-byte ones took 4096 cycles a tile).
+MOE_D void store32(void* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 // 64 values of a row to 64 bf16.
-MOE_D void store64(__nv_bfloat16* dst, const float2* v) {
+MOE_D void store64(__nv_bfloat16* dst, const float2* v, bool wide) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 4)
-    *reinterpret_cast<uint4*>(dst + 2 * j) =
-        make_uint4(pack_bf16x2(v[j].x, v[j].y), pack_bf16x2(v[j + 1].x, v[j + 1].y),
-                   pack_bf16x2(v[j + 2].x, v[j + 2].y), pack_bf16x2(v[j + 3].x, v[j + 3].y));
+  for (int j = 0; j < 32; j += 8) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[j + k].x, v[j + k].y);
+    store32(dst + 2 * j, w, wide);
+  }
 }
 
 struct Tile {
@@ -158,6 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(tc::smem_u32(&ctl.tfull[b]), 1);
       tc::mbar_init(tc::smem_u32(&ctl.tempty[b]), 8);
+      tc::mbar_init(tc::smem_u32(&ctl.sfull[b]), 2);
+      tc::mbar_init(tc::smem_u32(&ctl.sempty[b]), 8);
     }
     for (int q = 0; q < 4; ++q) tc::mbar_init(tc::smem_u32(&ctl.meet[q]), 2);
     tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
@@ -185,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
    if (warp == 0) {
     // ================= TMA producer: the warp runs the loop, one lane issues =================
     const bool elected = tc::elect_one();
+    const uint64_t policy = p.once ? tc::evict_first_policy() : tc::evict_normal_policy();
     int stage = 0;
     uint32_t phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
@@ -201,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t wd = tc::smem_u32(sW + stage * W_BYTES);
           tc::mbar_arrive_expect_tx(fb, A_BYTES + W_BYTES);
           tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BLOCK, t.row, fb);
-          tc::tma_load_2d(wd, &tmW, kb * BLOCK, w0, fb);
-          tc::tma_load_2d(wd + W_BYTES / 2, &tmW, kb * BLOCK, w1, fb);
+          tc::tma_load_2d_hint(wd, &tmW, kb * BLOCK, w0, fb, policy);
+          tc::tma_load_2d_hint(wd + W_BYTES / 2, &tmW, kb * BLOCK, w1, fb, policy);
         }
         __syncwarp();
         issued |= 1u << stage;
@@ -250,6 +275,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_wait(tc::smem_u32(&ctl.drain), 0, wdrain);
     }
     __syncwarp();
+   } else {
+    // ================= scales: 64 rows a warp, a lane one block of every fourth row =================
+    const int j = lane & 7, r0 = (warp - 2) * 64 + (lane >> 3);
+    const int wblk = p.Nw / BLOCK;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const Tile t = tile_at<TM>(ctl, E, tile);
+      // FC1: gate and up; FC2: neighbours (the last block twice where there is one)
+      const float* sw0 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? t.nb : 2 * t.nb)) * KB;
+      const float* sw1 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? wblk / 2 + t.nb : min(2 * t.nb + 1, wblk - 1))) * KB;
+      const float* sa = p.a_sf + (int64_t)t.row * KB;
+      for (int kb = 0; kb < KB; kb += SB, ++n) {
+        const uint32_t buf = n & 1;
+        const int k = min(kb + j, KB - 1);
+        const float w0 = __ldg(sw0 + k), w1 = __ldg(sw1 + k);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float a[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // (a row behind the expert's takes its last row's, which go nowhere)
+            a[i] = __ldg(sa + (int64_t)min(r0 + 32 * h + 4 * i, t.rows - 1) * KB + k);
+          if (h == 0 && !tc::mbar_wait(tc::smem_u32(&ctl.sempty[buf]), ((n >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            ctl.scale[buf][j][r0 + 32 * h + 4 * i] = make_float2(a[i] * w0, a[i] * w1);
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sfull[buf]));
+      }
+    }
    }
   } else {
     tc::regs_inc<kRegsJoin>();
@@ -260,32 +317,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t c0 = SWIGLU ? hf * 64 : hf * 128, c1 = SWIGLU ? 128 + hf * 64 : hf * 128 + 64;
     const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16);
     const int i = q * 32 + lane;  // row within the tile
-    uint32_t step = 0, parity = 0;
+    uint32_t step = 0, n = 0, parity = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
       const Tile t = tile_at<TM>(ctl, E, tile);
       const int n0 = SWIGLU ? t.nb * BLOCK + hf * 64 : t.nb * TN + hf * 128;  // first column
-      // the row's scales and the weight blocks' (FC1: gate and up), one block ahead.  (A
-      // row behind the expert's takes its last row's, a column block behind FC2's last
-      // the last one's: neither goes anywhere.)
-      const float* sa = p.a_sf + (int64_t)(t.row + min(i, t.rows - 1)) * KB;
-      const int wblk = p.Nw / BLOCK;
-      const float* s0 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? t.nb : min(2 * t.nb + hf, wblk - 1))) * KB;
-      const float* s1 = s0 + (int64_t)(wblk / 2) * KB;
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float na = __ldg(sa), n0s = __ldg(s0), n1s = SWIGLU ? __ldg(s1) : 0.f;
       for (int kb = 0; kb < KB; ++kb, ++step) {
-        const float g = na * n0s, u = SWIGLU ? na * n1s : g;
-        if (kb + 1 < KB) {
-          na = __ldg(++sa);
-          n0s = __ldg(++s0);
-          if (SWIGLU) n1s = __ldg(++s1);
+        const int j = kb & (SB - 1);
+        const uint32_t sb = n & 1, buf = step & 1;
+        if ((j == 0 && !tc::mbar_wait(tc::smem_u32(&ctl.sfull[sb]), (n >> 1) & 1, wc)) ||
+            !tc::mbar_wait(tc::smem_u32(&ctl.tfull[buf]), (step >> 1) & 1, wc)) {
+          ok = false;
+          break;
         }
-        const uint32_t buf = step & 1;
-        if (!tc::mbar_wait(tc::smem_u32(&ctl.tfull[buf]), (step >> 1) & 1, wc)) { ok = false; break; }
         tc::fence_after_sync();
+        const float2 s = ctl.scale[sb][j][i];
+        const float g = SWIGLU || hf == 0 ? s.x : s.y, u = SWIGLU ? s.y : g;
         const uint32_t b0 = tbase + buf * TN + c0, b1 = tbase + buf * TN + c1;
         constexpr int LD = 16;
         uint32_t v[LD];
@@ -299,14 +349,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.tempty[buf]));
         join(acc + 64 - LD / 2, v, u);
+        if (j == SB - 1 || kb == KB - 1) {
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sempty[sb]));
+          ++n;
+        }
       }
       if (!ok) break;
       const bool valid = i < t.rows;
       const int64_t row = (int64_t)t.row + i;
       if (SWIGLU) {
         if (p.save && valid) {
-          store64(p.save + row * p.Nw + n0, acc);
-          store64(p.save + row * p.Nw + p.N + n0, acc + 32);
+          store64(p.save + row * p.Nw + n0, acc, p.wide);
+          store64(p.save + row * p.Nw + p.N + n0, acc + 32, p.wide);
         }
         const float pr = p.prob && valid ? __ldg(p.prob + row) : 1.f;
         uint32_t m = 0;
@@ -316,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[j].y = pr * (silu_f32(acc[j].y) * acc[32 + j].y);
           m = max(m, max(fp8::mag_bits(acc[j].x), fp8::mag_bits(acc[j].y)));
         }
-        if (p.out && valid) store64(p.out + row * p.N + n0, acc);
+        if (p.out && valid) store64(p.out + row * p.N + n0, acc, p.wide);
         if (p.out_q) {
           // the block's other 64 columns are the other warp's of this lane quarter; a
           // buffer is written again two tiles on, behind the next tile's meeting
@@ -327,20 +381,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a = fp8::block_top(max(m, ctl.top[parity][hf ^ 1][i])), inv = fp8::block_inverse(a);
           if (valid) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              float f[16];
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t w[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) f[2 * k] = acc[j + k].x, f[2 * k + 1] = acc[j + k].y;
-              const uint2 x = fp8::codes8(f, inv), y = fp8::codes8(f + 8, inv);
-              *reinterpret_cast<uint4*>(p.out_q + row * p.N + n0 + 2 * j) = make_uint4(x.x, x.y, y.x, y.y);
+              for (int k = 0; k < 8; ++k) {
+                const float2 x = acc[j + 2 * k], y = acc[j + 2 * k + 1];
+                w[k] = fp8::codes4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+              }
+              store32(p.out_q + row * p.N + n0 + 2 * j, w, p.wide);
             }
             if (hf == 0) p.out_sf[row * (p.N / BLOCK) + t.nb] = fp8::block_scale(a);
           }
           parity ^= 1;
         }
       } else if (valid && n0 < p.N) {
-        store64(p.out + row * p.N + n0, acc);
-        store64(p.out + row * p.N + n0 + 64, acc + 32);
+        store64(p.out + row * p.N + n0, acc, p.wide);
+        store64(p.out + row * p.N + n0 + 64, acc + 32, p.wide);
       }
     }
   }
@@ -668,6 +724,11 @@ cudaError_t launch_fp8_product(bool swiglu, int P, const uint8_t* a, const float
   p.save = static_cast<__nv_bfloat16*>(save); p.out = static_cast<__nv_bfloat16*>(out);
   p.out_q = out_q; p.out_sf = out_sf;
   p.P = P; p.E = E; p.KB = Kd / BLOCK; p.N = N; p.Nw = Nw;
+  p.wide = ((reinterpret_cast<uintptr_t>(save) | reinterpret_cast<uintptr_t>(out) |
+             reinterpret_cast<uintptr_t>(out_q)) & 31u) == 0;
+  // up to 64 rows an expert on average most have one row tile: evict-first is 5 to 12%
+  // faster at 32 and 64, and 2 to 5% slower at 128 and 256, where tiles share weights
+  p.once = P <= 64LL * E;
   p.status = status;
   p.wait_limit_ns = 2000000000ull;
   const int nblk = swiglu || few ? N / BLOCK : (N + TN - 1) / TN;

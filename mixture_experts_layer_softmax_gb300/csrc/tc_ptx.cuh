@@ -185,6 +185,11 @@ MOE_D uint64_t evict_first_policy() {
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(v));
   return v;
 }
+MOE_D uint64_t evict_normal_policy() {
+  uint64_t v;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(v));
+  return v;
+}
 // Four rows of a 2-D tensor (box one row high): rows r0..r3 at column c0,
 // written to shared memory one after the other (the map's swizzle applies by
 // shared-memory address, as for a 4-row box).
