@@ -155,133 +155,165 @@ __global__ void __launch_bounds__(NT)
 }
 
 // ---- gradient ------------------------------------------------------------------
-// Rows of up to 8192 columns.  A persistent block: eight warps that take G rows at a
-// time, W = 8 / G warps a row, and one that brings the next G rows of dy, sum and dsum
-// (each a run of bytes) into a ring of shared-memory stages with bulk copies, as many
-// rows ahead as fit: the loads of a row that is to come never wait for a sum over the
-// present one.  Each thread keeps its columns' part of dw in registers and writes it
-// once, to part[block * G + group]; the parts are added in order by a second kernel.
-constexpr int kRing = 8;                 // stages at most
-constexpr int kRingBytes = 200 * 1024;   // shared memory of the stages
+// Rows of up to 8192 columns.  A persistent block: G groups of W warps, each a row at a
+// time with a ring of shared-memory stages of its own, and one warp that fills the rings
+// with bulk copies (dy, sum and dsum of a row), as many rows ahead as fit: no load of a
+// row to come waits for a sum over the present one, and while one group adds up its
+// dot product the others compute.  A thread reads its columns from the stage twice,
+// before and after the sum, and keeps its part of dw in registers; it is written once,
+// to part[block * G + group], and the parts are added in order by a second kernel.
+constexpr int kBwdWarps = 16;
+constexpr int kRing = 8;                 // stages a group at most
+constexpr int kRingBytes = 216 * 1024;   // shared memory of w and the stages
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(288, 1)
+__global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
     rmsnorm_bwd_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
                        const float* __restrict__ w, const T* dsum, int64_t rows, int h, int W,
-                       int stages, T* dx, float* __restrict__ part, int* status) {
-  extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t full[kRing], empty[kRing];
-  __shared__ float slot[2][8];
-  __shared__ int abort[2], quit;
+                       int G, int stages, T* dx, float* __restrict__ part, int* status) {
+  extern __shared__ __align__(128) uint8_t dyn[];
+  __shared__ uint64_t full[kBwdWarps][kRing], empty[kBwdWarps][kRing];
+  __shared__ float slot[2][kBwdWarps];
+  __shared__ int abort[kBwdWarps][2], quit;
+  pdl_trigger();  // (the second kernel waits for all of this one before it reads a part)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = 8 / W, arrays = dsum ? 3 : 2;
-  const int64_t chunks = (rows + G - 1) / G;
-  const uint32_t chunk_bytes = (uint32_t)(G * h * sizeof(T)), stage_bytes = arrays * chunk_bytes;
+  const int arrays = dsum ? 3 : 2;
+  float* s_w = reinterpret_cast<float*>(dyn);
+  const uint32_t row_bytes = (uint32_t)(h * sizeof(T)), stage_bytes = arrays * row_bytes;
+  uint8_t* ring = dyn + align_up((size_t)h * 4, 128);  // [group][stage][array]
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      tc::mbar_init(tc::smem_u32(&full[s]), 1);
-      tc::mbar_init(tc::smem_u32(&empty[s]), 8);
+    for (int g = 0; g < G; ++g) {
+      for (int s = 0; s < stages; ++s) {
+        tc::mbar_init(tc::smem_u32(&full[g][s]), 1);
+        tc::mbar_init(tc::smem_u32(&empty[g][s]), W);
+      }
+      abort[g][0] = abort[g][1] = 0;
     }
-    abort[0] = abort[1] = quit = 0;
+    quit = 0;
     tc::fence_barrier_init();
   }
+  for (int c = threadIdx.x * 4; c < h; c += blockDim.x * 4)
+    *reinterpret_cast<float4*>(s_w + c) = __ldg(reinterpret_cast<const float4*>(w + c));
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kBwdWarps) {
     if (lane == 0) {
       const tc::WaitCtl wc{status, &quit, 2000000000ull, 0};
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, par = 0;
-      for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        if (!tc::mbar_wait(tc::smem_u32(&empty[stage]), phase ^ 1, wc)) break;
-        const int64_t at = c * G * h, left = rows - c * G;
-        const uint32_t bytes = left < G ? (uint32_t)(left * h * sizeof(T)) : chunk_bytes;
-        const uint32_t fb = tc::smem_u32(&full[stage]);
-        const uint32_t dst = tc::smem_u32(ring) + stage * stage_bytes;
-        tc::mbar_arrive_expect_tx(fb, arrays * bytes);
-        tc::bulk_load(dst, dy + at, bytes, fb);
-        tc::bulk_load(dst + chunk_bytes, sum + at, bytes, fb);
-        if (dsum) tc::bulk_load(dst + 2 * chunk_bytes, dsum + at, bytes, fb);
-        issued |= 1u << stage;
-        par = (par & ~(1u << stage)) | (phase << stage);
-        if (++stage == stages) { stage = 0; phase ^= 1; }
-      }
       const tc::WaitCtl wd{status, nullptr, 1000000000ull, 0};
-      for (int s = 0; s < stages; ++s)  // no copy is under way when the block ends
-        if ((issued >> s) & 1u) tc::mbar_wait(tc::smem_u32(&full[s]), (par >> s) & 1u, wd);
+      int stage = 0, g = 0;
+      uint32_t phase = 0, laps = 0;  // laps: stages filled by all groups so far
+      int64_t issued = 0;
+      for (int64_t row = (int64_t)blockIdx.x * G; row < rows;) {
+        if (!tc::mbar_wait(tc::smem_u32(&empty[g][stage]), phase ^ 1, wc)) break;
+        const uint32_t fb = tc::smem_u32(&full[g][stage]);
+        const uint32_t dst = tc::smem_u32(ring) + (uint32_t)(g * stages + stage) * stage_bytes;
+        tc::mbar_arrive_expect_tx(fb, stage_bytes);
+        tc::bulk_load(dst, dy + row * h, row_bytes, fb);
+        tc::bulk_load(dst + row_bytes, sum + row * h, row_bytes, fb);
+        if (dsum) tc::bulk_load(dst + 2 * row_bytes, dsum + row * h, row_bytes, fb);
+        ++issued;
+        if (++g == G) {
+          g = 0;
+          ++laps;
+          row += (int64_t)(gridDim.x - 1) * G + 1;
+          if (++stage == stages) { stage = 0; phase ^= 1; }
+        } else {
+          ++row;
+        }
+      }
+      // no copy is under way when the block ends: the last one of every stage has come
+      const int64_t n = (int64_t)G * stages;
+      for (int64_t k = issued > n ? issued - n : 0; k < issued; ++k) {
+        const int64_t lap = k / G;
+        tc::mbar_wait(tc::smem_u32(&full[k % G][lap % stages]), (uint32_t)(lap / stages) & 1u, wd);
+      }
     }
     return;
   }
   const int g = warp / W, tx = (warp % W) * 32 + lane, nt = W * 32;
-  float ww[NV][kCols], acc[NV][kCols] = {};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tx) * kCols;
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) ww[i][j] = 0.f;
-    if (c < h) load8(w + c, h - c, ww[i]);
-  }
+  if (g >= G) return;
+  float acc[NV][kCols] = {};
   int stage = 0, parity = 0;
   uint32_t phase = 0;
-  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x, parity ^= 1) {
-    const int64_t row = c * G + g;
-    const bool here = row < rows;
-    const float r = here ? __ldg(rstd + row) : 0.f;
-    // a wait that gave up is known to every warp behind the barrier below, by a flag of
-    // this chunk's parity (the next chunk's may be raised before all have read it)
-    const tc::WaitCtl wc{status, &abort[parity], 2000000000ull, 0};
-    tc::mbar_wait(tc::smem_u32(&full[stage]), phase, wc);
-    const T* s_dy = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes) + g * h;
-    const T* s_sum = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes + chunk_bytes) + g * h;
-    const T* s_ds = reinterpret_cast<const T*>(ring + (size_t)stage * stage_bytes + 2 * chunk_bytes) + g * h;
-    float n[NV][kCols], gy[NV][kCols];
+  for (int64_t row = (int64_t)blockIdx.x * G + g; row < rows;
+       row += (int64_t)gridDim.x * G, parity ^= 1) {
+    const float r = __ldg(rstd + row);
+    // a wait that gave up is known to every warp of the group behind the barrier below, by
+    // a flag of this row's parity (the next row's may be raised before all have read it)
+    const tc::WaitCtl wc{status, &abort[g][parity], 2000000000ull, 0};
+    tc::mbar_wait(tc::smem_u32(&full[g][stage]), phase, wc);
+    const T* s_dy = reinterpret_cast<const T*>(ring + (size_t)(g * stages + stage) * stage_bytes);
+    const T *s_sum = s_dy + h, *s_ds = s_dy + 2 * h;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * nt + tx) * kCols;
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) n[i][j] = gy[i][j] = 0.f;
-      if (here && col < h) {
-        load8(s_sum + col, h - col, n[i]);
-        load8(s_dy + col, h - col, gy[i]);
+      const int c = (i * nt + tx) * kCols;
+      if (c < h) {
+        float n[kCols], d[kCols], ww[kCols];
+        load8(s_sum + c, h - c, n);
+        load8(s_dy + c, h - c, d);
+        load8(s_w + c, h - c, ww);
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
-          n[i][j] *= r;
-          acc[i][j] = fmaf(gy[i][j], n[i][j], acc[i][j]);
-          gy[i][j] *= ww[i][j];
-          dot = fmaf(gy[i][j], n[i][j], dot);
+          n[j] *= r;
+          acc[i][j] = fmaf(d[j], n[j], acc[i][j]);
+          dot = fmaf(d[j] * ww[j], n[j], dot);
         }
       }
     }
     dot = warp_sum(dot);
     if (lane == 0) slot[parity][warp] = dot;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (abort[parity]) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (g & 7)), "r"(nt) : "memory");
+    if (abort[g][parity]) {
       quit = 1;
       break;
     }
     dot = 0.f;
     for (int i = 0; i < W; ++i) dot += slot[parity][g * W + i];
-    const float mean = dot / (float)h;
+    const float mr = dot / (float)h * r;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * nt + tx) * kCols;
-      if (here && col < h) {
-        float o[kCols], d[kCols] = {};
-        if (dsum) load8(s_ds + col, h - col, d);
+      const int c = (i * nt + tx) * kCols;
+      if (c < h) {
+        float n[kCols], d[kCols], ww[kCols], o[kCols] = {};
+        load8(s_sum + c, h - c, n);
+        load8(s_dy + c, h - c, d);
+        load8(s_w + c, h - c, ww);
+        if (dsum) load8(s_ds + c, h - c, o);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[i][j], mean, gy[i][j]), d[j]);
-        store8(dx + row * h + col, h - col, o);
+        for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[j], mr, d[j] * ww[j]), o[j]);
+        store8(dx + row * h + c, h - c, o);
       }
     }
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&empty[stage]));
+    if (lane == 0) tc::mbar_arrive(tc::smem_u32(&empty[g][stage]));
     if (++stage == stages) { stage = 0; phase ^= 1; }
   }
   if (!part) return;
+  // the groups' parts, added in order by the first one: the others leave theirs in the
+  // stages, which no copy is under way to once every group has had all its rows
+  const int threads = G * nt;
+  float* left = reinterpret_cast<float*>(ring);
+  asm volatile("bar.sync 9, %0;" ::"r"(threads) : "memory");
+  if (g > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * nt + tx) * kCols;
+      if (c < h) store8(left + (size_t)(g - 1) * h + c, h - c, acc[i]);
+    }
+  }
+  asm volatile("bar.sync 9, %0;" ::"r"(threads) : "memory");
+  if (g > 0) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * nt + tx) * kCols;
-    if (col < h) store8(part + ((int64_t)blockIdx.x * G + g) * h + col, h - col, acc[i]);
+    const int c = (i * nt + tx) * kCols;
+    if (c >= h) continue;
+    for (int k = 1; k < G; ++k) {
+      float v[kCols];
+      load8(left + (size_t)(k - 1) * h + c, h - c, v);
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[i][j] += v[j];
+    }
+    store8(part + (int64_t)blockIdx.x * h + c, h - c, acc[i]);
   }
 }
 
@@ -366,11 +398,17 @@ __global__ void __launch_bounds__(512)
 
 constexpr int kMaxBlocks = 256;  // of the gradient's first kernel
 
-// Warps a row in the gradient: the fewest that hold it in 4 vectors a thread.
+// Warps a row in the gradient (the fewest that hold it in 4 vectors a thread) and groups
+// a block: at most 8, which have a barrier each, and so many that each has two stages.
 int bwd_warps(int h) {
   int w = 1;
   while (w < 8 && h > w * 32 * 4 * kCols) w *= 2;
   return w;
+}
+int bwd_groups(int h, int W, size_t stage) {
+  int g = kBwdWarps / W < 8 ? kBwdWarps / W : 8;
+  while (g > 1 && 2 * g * stage > kRingBytes - align_up((size_t)h * 4, 128)) g /= 2;
+  return g;
 }
 constexpr int kBwdMaxCols = 8 * 32 * 4 * kCols;
 
@@ -413,18 +451,18 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
   const int most = sms < kMaxBlocks ? sms : kMaxBlocks;
   int parts;
   if (h <= kBwdMaxCols) {
-    const int W = bwd_warps(h), G = 8 / W;
+    const size_t stage = (size_t)h * sizeof(T) * (d ? 3 : 2), head = align_up((size_t)h * 4, 128);
+    const int W = bwd_warps(h), G = bwd_groups(h, W, stage);
     const int64_t chunks = ceil_div(rows, G);
     const unsigned grid = (unsigned)(chunks < most ? chunks : most);
-    const size_t stage = (size_t)G * h * sizeof(T) * (d ? 3 : 2);
-    const int stages = (int)(kRingBytes / stage < kRing ? kRingBytes / stage : kRing);
+    const int fit = (int)((kRingBytes - head) / (G * stage)), stages = fit < kRing ? fit : kRing;
     auto kern = h <= W * 256 ? rmsnorm_bwd_kernel<T, 1>
                              : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2> : rmsnorm_bwd_kernel<T, 4>;
-    const size_t smem = stages * stage;
+    const size_t smem = head + G * stages * stage;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 288, smem, s>>>(a, b, rstd, w, d, rows, h, W, stages, o, pt, status);
-    parts = (int)grid * G;
+    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, stages, o, pt, status);
+    parts = (int)grid;
   } else {
     const unsigned grid = (unsigned)(rows < most ? rows : most);
     const int nvec = (int)ceil_div(h, kCols);
@@ -445,9 +483,8 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
 }  // namespace
 
 size_t rmsnorm_bwd_workspace(int64_t rows, int h) {
-  const int G = h <= kBwdMaxCols ? 8 / bwd_warps(h) : 1;
-  const int64_t chunks = ceil_div(rows, G), blocks = chunks < kMaxBlocks ? chunks : kMaxBlocks;
-  return align_up((size_t)(blocks * G) * h * 4, 256);
+  const int64_t blocks = rows < kMaxBlocks ? rows : kMaxBlocks;
+  return align_up((size_t)blocks * h * 4, 256);
 }
 
 cudaError_t launch_rmsnorm_fwd(int64_t rows, int h, int dtype, const void* x, const void* res,

@@ -229,6 +229,8 @@ __global__ void __launch_bounds__(256) chunk_scan_kernel(const int32_t* __restri
                                                          int32_t* __restrict__ counts) {
   const int lane = threadIdx.x & 31;
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  pdl_wait();
+  pdl_trigger();
   if (e < E) scan_expert(e, lane, hist, NC, E, cap, base, counts);
 }
 
@@ -241,6 +243,8 @@ __global__ void __launch_bounds__(256) chunk_ranks_kernel(
     int32_t* __restrict__ src_token, float* __restrict__ perm_prob, int* status) {
   __shared__ int32_t s_off[257];
   __shared__ int32_t s_warp[8];
+  pdl_wait();
+  pdl_trigger();
   block_offsets(counts, E, s_off, s_warp, offsets_out);
   const int c = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (c < NC)
@@ -353,11 +357,13 @@ cudaError_t launch_permute_maps(const moe_config_t& c, const int32_t* idx, const
                       c.K, c.E, c.capacity, NC, (const int32_t*)hist, counts, offsets, dst_row,
                       src_token, perm_prob, status);
   }
-  chunk_scan_kernel<<<(unsigned)ceil_div(c.E, 8), 256, 0, s>>>(hist, NC, c.E, c.capacity, base,
-                                                                counts);
-  chunk_ranks_kernel<<<blocks, 256, 0, s>>>(idx, prob, c.T, c.K, c.E, c.capacity, NC, base, counts,
-                                            offsets, dst_row, src_token, perm_prob, status);
-  return cudaGetLastError();
+  // each step may be scheduled while the one before it ends (it waits for it first)
+  cudaError_t e = pdl_launch(chunk_scan_kernel, dim3((unsigned)ceil_div(c.E, 8)), dim3(256), 0, s,
+                             (const int32_t*)hist, NC, c.E, c.capacity, base, counts);
+  if (e != cudaSuccess) return e;
+  return pdl_launch(chunk_ranks_kernel, dim3(blocks), dim3(256), 0, s, idx, prob, c.T, c.K, c.E,
+                    c.capacity, NC, (const int32_t*)base, (const int32_t*)counts, offsets, dst_row,
+                    src_token, perm_prob, status);
 }
 
 int scatter_grid(int ntok, int sms) {
