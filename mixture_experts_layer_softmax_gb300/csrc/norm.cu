@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(NT)
 
 // ---- gradient ------------------------------------------------------------------
 // Rows of up to 8192 columns.  A persistent block: G groups of W warps, each a row at a
-// time with a ring of shared-memory stages of its own, and one warp that fills the rings
-// with bulk copies (dy, sum and dsum of a row), as many rows ahead as fit: no load of a
-// row to come waits for a sum over the present one, and while one group adds up its
+// time with a ring of shared-memory stages of its own (R rows each, more than one where
+// they are short), and one warp that fills the rings with bulk copies (dy, sum and dsum
+// of a stage's rows), as many stages ahead as fit: no load of a row to come waits for a sum over the present one, and while one group adds up its
 // dot product the others compute.  A thread reads its columns from the stage twice,
 // before and after the sum, and keeps its part of dw in registers; it is written once,
 // to part[block * G + group], and the parts are added in order by a second kernel.
@@ -166,11 +166,12 @@ constexpr int kBwdWarps = 16;
 constexpr int kRing = 8;                 // stages a group at most
 constexpr int kRingBytes = 216 * 1024;   // shared memory of w and the stages
 
-template <typename T, int NV>
+template <typename T, int NV, bool ONE>  // ONE: R is 1
 __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
     rmsnorm_bwd_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
                        const float* __restrict__ w, const T* dsum, int64_t rows, int h, int W,
-                       int G, int stages, T* dx, float* __restrict__ part, int* status) {
+                       int G, int r_stage, int stages, T* dx, float* __restrict__ part, int* status) {
+  const int R = ONE ? 1 : r_stage;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ uint64_t full[kBwdWarps][kRing], empty[kBwdWarps][kRing];
   __shared__ float slot[2][kBwdWarps];
@@ -179,7 +180,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int arrays = dsum ? 3 : 2;
   float* s_w = reinterpret_cast<float*>(dyn);
-  const uint32_t row_bytes = (uint32_t)(h * sizeof(T)), stage_bytes = arrays * row_bytes;
+  const uint32_t array_bytes = (uint32_t)(R * h * sizeof(T)), stage_bytes = arrays * array_bytes;
+  const int64_t chunks = (rows + R - 1) / R;
   uint8_t* ring = dyn + align_up((size_t)h * 4, 128);  // [group][stage][array]
   if (threadIdx.x == 0) {
     for (int g = 0; g < G; ++g) {
@@ -202,22 +204,24 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
       int stage = 0, g = 0;
       uint32_t phase = 0, laps = 0;  // laps: stages filled by all groups so far
       int64_t issued = 0;
-      for (int64_t row = (int64_t)blockIdx.x * G; row < rows;) {
+      for (int64_t c = (int64_t)blockIdx.x * G; c < chunks;) {
         if (!tc::mbar_wait(tc::smem_u32(&empty[g][stage]), phase ^ 1, wc)) break;
         const uint32_t fb = tc::smem_u32(&full[g][stage]);
         const uint32_t dst = tc::smem_u32(ring) + (uint32_t)(g * stages + stage) * stage_bytes;
-        tc::mbar_arrive_expect_tx(fb, stage_bytes);
-        tc::bulk_load(dst, dy + row * h, row_bytes, fb);
-        tc::bulk_load(dst + row_bytes, sum + row * h, row_bytes, fb);
-        if (dsum) tc::bulk_load(dst + 2 * row_bytes, dsum + row * h, row_bytes, fb);
+        const int64_t at = c * R * h, left = rows - c * R;
+        const uint32_t bytes = left < R ? (uint32_t)(left * h * sizeof(T)) : array_bytes;
+        tc::mbar_arrive_expect_tx(fb, arrays * bytes);
+        tc::bulk_load(dst, dy + at, bytes, fb);
+        tc::bulk_load(dst + array_bytes, sum + at, bytes, fb);
+        if (dsum) tc::bulk_load(dst + 2 * array_bytes, dsum + at, bytes, fb);
         ++issued;
         if (++g == G) {
           g = 0;
           ++laps;
-          row += (int64_t)(gridDim.x - 1) * G + 1;
+          c += (int64_t)(gridDim.x - 1) * G + 1;
           if (++stage == stages) { stage = 0; phase ^= 1; }
         } else {
-          ++row;
+          ++c;
         }
       }
       // no copy is under way when the block ends: the last one of every stage has come
@@ -234,54 +238,60 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
   float acc[NV][kCols] = {};
   int stage = 0, parity = 0;
   uint32_t phase = 0;
-  for (int64_t row = (int64_t)blockIdx.x * G + g; row < rows;
-       row += (int64_t)gridDim.x * G, parity ^= 1) {
-    const float r = __ldg(rstd + row);
-    // a wait that gave up is known to every warp of the group behind the barrier below, by
-    // a flag of this row's parity (the next row's may be raised before all have read it)
+  bool ok = true;
+  for (int64_t c = (int64_t)blockIdx.x * G + g; c < chunks && ok; c += (int64_t)gridDim.x * G) {
+    // a wait that gave up is known to every warp of the group behind the next barrier, by
+    // a flag of that row's parity (the other may be raised before all have read it)
     const tc::WaitCtl wc{status, &abort[g][parity], 2000000000ull, 0};
     tc::mbar_wait(tc::smem_u32(&full[g][stage]), phase, wc);
     const T* s_dy = reinterpret_cast<const T*>(ring + (size_t)(g * stages + stage) * stage_bytes);
-    const T *s_sum = s_dy + h, *s_ds = s_dy + 2 * h;
-    float dot = 0.f;
+    const int64_t row0 = c * R;
+    const int n_rows = rows - row0 < R ? (int)(rows - row0) : R;
+    for (int k = 0; k < n_rows; ++k, parity ^= 1, s_dy += h) {
+      const T *s_sum = s_dy + R * h, *s_ds = s_dy + 2 * R * h;
+      const int64_t row = row0 + k;
+      const float r = __ldg(rstd + row);
+      float dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * nt + tx) * kCols;
-      if (c < h) {
-        float n[kCols], d[kCols], ww[kCols];
-        load8(s_sum + c, h - c, n);
-        load8(s_dy + c, h - c, d);
-        load8(s_w + c, h - c, ww);
+      for (int i = 0; i < NV; ++i) {
+        const int col = (i * nt + tx) * kCols;
+        if (col < h) {
+          float n[kCols], d[kCols], ww[kCols];
+          load8(s_sum + col, h - col, n);
+          load8(s_dy + col, h - col, d);
+          load8(s_w + col, h - col, ww);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          n[j] *= r;
-          acc[i][j] = fmaf(d[j], n[j], acc[i][j]);
-          dot = fmaf(d[j] * ww[j], n[j], dot);
+          for (int j = 0; j < kCols; ++j) {
+            n[j] *= r;
+            acc[i][j] = fmaf(d[j], n[j], acc[i][j]);
+            dot = fmaf(d[j] * ww[j], n[j], dot);
+          }
         }
       }
-    }
-    dot = warp_sum(dot);
-    if (lane == 0) slot[parity][warp] = dot;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + (g & 7)), "r"(nt) : "memory");
-    if (abort[g][parity]) {
-      quit = 1;
-      break;
-    }
-    dot = 0.f;
-    for (int i = 0; i < W; ++i) dot += slot[parity][g * W + i];
-    const float mr = dot / (float)h * r;
+      dot = warp_sum(dot);
+      if (lane == 0) slot[parity][warp] = dot;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(nt) : "memory");
+      if (abort[g][parity]) {
+        quit = 1;
+        ok = false;
+        break;
+      }
+      dot = 0.f;
+      for (int i = 0; i < W; ++i) dot += slot[parity][g * W + i];
+      const float mr = dot / (float)h * r;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * nt + tx) * kCols;
-      if (c < h) {
-        float n[kCols], d[kCols], ww[kCols], o[kCols] = {};
-        load8(s_sum + c, h - c, n);
-        load8(s_dy + c, h - c, d);
-        load8(s_w + c, h - c, ww);
-        if (dsum) load8(s_ds + c, h - c, o);
+      for (int i = 0; i < NV; ++i) {
+        const int col = (i * nt + tx) * kCols;
+        if (col < h) {
+          float n[kCols], d[kCols], ww[kCols], o[kCols] = {};
+          load8(s_sum + col, h - col, n);
+          load8(s_dy + col, h - col, d);
+          load8(s_w + col, h - col, ww);
+          if (dsum) load8(s_ds + col, h - col, o);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[j], mr, d[j] * ww[j]), o[j]);
-        store8(dx + row * h + c, h - c, o);
+          for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[j], mr, d[j] * ww[j]), o[j]);
+          store8(dx + row * h + col, h - col, o);
+        }
       }
     }
     __syncwarp();
@@ -314,6 +324,63 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
       for (int j = 0; j < kCols; ++j) acc[i][j] += v[j];
     }
     store8(part + (int64_t)blockIdx.x * h + c, h - c, acc[i]);
+  }
+}
+
+// Few rows: one launch, whose first `rows` blocks have a row of dx each and whose others
+// 32 columns of dw, summed by 8 threads each over every 8th row and then in order (the
+// inputs come a second time, from the L2).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    rmsnorm_bwd_few_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
+                           const float* __restrict__ w, const T* dsum, int rows, int h, T* dx,
+                           float* __restrict__ dw) {
+  __shared__ float slot[8][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x >= (unsigned)rows) {
+    const int c = (blockIdx.x - rows) * 32 + lane;
+    float v = 0.f;
+    if (c < h) {
+#pragma unroll 4
+      for (int i = warp; i < rows; i += 8)
+        v = fmaf(to_f32(dy[(int64_t)i * h + c]), to_f32(sum[(int64_t)i * h + c]) * __ldg(rstd + i), v);
+    }
+    slot[warp][lane] = v;
+    __syncthreads();
+    if (warp || c >= h) return;
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += slot[i][lane];
+    dw[c] = v;
+    return;
+  }
+  const int64_t at = (int64_t)blockIdx.x * h;
+  const float r = __ldg(rstd + blockIdx.x);
+  float dot = 0.f;
+  for (int c = threadIdx.x * kCols; c < h; c += 256 * kCols) {
+    float n[kCols], d[kCols], ww[kCols];
+    load8(sum + at + c, h - c, n);
+    load8(dy + at + c, h - c, d);
+    load8(w + c, h - c, ww);
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) dot = fmaf(d[j] * ww[j], n[j] * r, dot);
+  }
+  dot = warp_sum(dot);
+  if (lane == 0) slot[warp][0] = dot;
+  __syncthreads();
+  dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dot += slot[i][0];
+  const float mr = dot / (float)h * r;
+  for (int c = threadIdx.x * kCols; c < h; c += 256 * kCols) {
+    float n[kCols], d[kCols], ww[kCols], o[kCols] = {};
+    load8(sum + at + c, h - c, n);
+    load8(dy + at + c, h - c, d);
+    load8(w + c, h - c, ww);
+    if (dsum) load8(dsum + at + c, h - c, o);
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) o[j] = fmaf(r, fmaf(-n[j], mr, d[j] * ww[j]), o[j]);
+    store8(dx + at + c, h - c, o);
   }
 }
 
@@ -397,6 +464,7 @@ __global__ void __launch_bounds__(512)
 }
 
 constexpr int kMaxBlocks = 256;  // of the gradient's first kernel
+constexpr int kFewRows = 512;    // up to which the gradient is one launch
 
 // Warps a row in the gradient (the fewest that hold it in 4 vectors a thread) and groups
 // a block: at most 8, which have a barrier each, and so many that each has two stages.
@@ -449,19 +517,34 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
   T* o = static_cast<T*>(dx);
   float* pt = dw ? part : nullptr;
   const int most = sms < kMaxBlocks ? sms : kMaxBlocks;
+  if (rows <= kFewRows && (!dw || (a != o && b != o))) {
+    // (in place, dx would go where the blocks for dw still read)
+    rmsnorm_bwd_few_kernel<T><<<(unsigned)(rows + (dw ? ceil_div(h, 32) : 0)), 256, 0, s>>>(
+        a, b, rstd, w, d, (int)rows, h, o, dw);
+    return cudaGetLastError();
+  }
   int parts;
   if (h <= kBwdMaxCols) {
-    const size_t stage = (size_t)h * sizeof(T) * (d ? 3 : 2), head = align_up((size_t)h * 4, 128);
-    const int W = bwd_warps(h), G = bwd_groups(h, W, stage);
-    const int64_t chunks = ceil_div(rows, G);
-    const unsigned grid = (unsigned)(chunks < most ? chunks : most);
+    const size_t row = (size_t)h * sizeof(T), head = align_up((size_t)h * 4, 128);
+    const int W = bwd_warps(h), G = bwd_groups(h, W, row * (d ? 3 : 2));
+    // short rows come in copies of up to 4 KB (one thread issues them all), while every
+    // group has some
+    const int64_t share = rows / ((int64_t)most * G), want = 4096 / (int64_t)row;
+    const int R = (int)(share < 2 || want < 2 ? 1 : share < want ? share : want);
+    const size_t stage = R * row * (d ? 3 : 2);
+    const int64_t blocks = ceil_div(ceil_div(rows, R), G);
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     const int fit = (int)((kRingBytes - head) / (G * stage)), stages = fit < kRing ? fit : kRing;
-    auto kern = h <= W * 256 ? rmsnorm_bwd_kernel<T, 1>
-                             : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2> : rmsnorm_bwd_kernel<T, 4>;
+    auto kern = R > 1 ? (h <= W * 256   ? rmsnorm_bwd_kernel<T, 1, false>
+                         : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2, false>
+                                        : rmsnorm_bwd_kernel<T, 4, false>)
+                      : (h <= W * 256   ? rmsnorm_bwd_kernel<T, 1, true>
+                         : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2, true>
+                                        : rmsnorm_bwd_kernel<T, 4, true>);
     const size_t smem = head + G * stages * stage;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, stages, o, pt, status);
+    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, R, stages, o, pt, status);
     parts = (int)grid;
   } else {
     const unsigned grid = (unsigned)(rows < most ? rows : most);
