@@ -72,7 +72,7 @@ cudaError_t launch_fp8_quantize(int64_t, int, const void*, uint8_t*, float*, int
 cudaError_t launch_fp8_quantize_weights(int, int, int, const void*, uint8_t*, float*, uint8_t*,
                                         float*, cudaStream_t);
 cudaError_t launch_fp8_scatter(const moe_config_t&, const uint8_t*, const float*, const int32_t*,
-                               uint8_t*, float*, int*, cudaStream_t);
+                               uint8_t*, float*, int, int*, cudaStream_t);
 cudaError_t launch_fp8_product(bool, int, const uint8_t*, const float*, int, const uint8_t*,
                                const float*, int, int, const int32_t*, const float*, void*, void*,
                                uint8_t*, float*, int, int*, cudaStream_t);
@@ -83,7 +83,7 @@ cudaError_t launch_rmsnorm_bwd(int64_t, int, int, const void*, const void*, cons
                                const float*, const void*, void*, float*, float*, int, int*,
                                cudaStream_t);
 cudaError_t launch_combine_bwd(const moe_config_t&, const void*, const void*, const int32_t*,
-                               const float*, void*, float*, int*, cudaStream_t);
+                               const float*, void*, float*, int, int*, cudaStream_t);
 }  // namespace moe
 
 using namespace moe;
@@ -690,7 +690,7 @@ moe_status_t moe_permute_fp8(const moe_config_t* cfg, const uint8_t* x_q, const 
                                       src_token, perm_prob, d->status, s,
                                       (cfg->flags & MOE_FLAG_HIST_FROM_ROUTER) != 0);
   if (e == cudaSuccess)
-    e = launch_fp8_scatter(*cfg, x_q, x_sf, dst_row, xp_q, xp_sf, d->status, s);
+    e = launch_fp8_scatter(*cfg, x_q, x_sf, dst_row, xp_q, xp_sf, d->sms, d->status, s);
   return cuda_status(e);
 }
 
@@ -797,7 +797,7 @@ moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,
   const DeviceInfo* d = device_info();
   if (!d) return MOE_ERR_CUDA;
   return cuda_status(launch_combine_bwd(*cfg, dy, y_perm, dst_row, topk_prob, dy_perm, dprob,
-                                        d->status, static_cast<cudaStream_t>(stream)));
+                                        d->sms, d->status, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_unpermute_combine(const moe_config_t* cfg, const void* y_perm,

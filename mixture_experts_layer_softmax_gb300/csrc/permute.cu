@@ -9,13 +9,13 @@
 // bit-reproducible: inside an expert's segment rows are in ascending token
 // order.  Tokens are cut into chunks of 32 (one warp each):
 //   1. chunk_hist:   hist[c][e] = pairs of chunk c routed to e
-//   2. chunk_scan:   base[c][e] = sum_{c' < c} hist[c'][e]; counts[e] (warp per expert);
+//   2. chunk_scan:   base[c][e] = sum_{c' < c} hist[c'][e]; counts[e];
 //                    for small batches (ceil(T/32) * E <= 8192) every block of
 //                    step 3 redoes this scan in shared memory instead (one
 //                    launch fewer)
 //   3. chunk_ranks:  offsets = exclusive scan of counts; for every pair
 //                    dst_row = offsets[e] + base[c][e] + rank inside the chunk
-//                    (ranks from ballots over the lanes' expert ids);
+//                    (a bit per token in a word per expert);
 //                    src_token, perm_prob are the inverse maps.
 //   With an expert capacity C (skill page "emerging-techniques-moe-training",
 //   "Capacity Factor Tuning"), counts[e] = min(slots, C) and a pair whose
@@ -95,14 +95,37 @@ MOE_D void block_offsets(const int32_t* __restrict__ counts, int E, int32_t* s_o
   if (blockIdx.x == 0 && offsets_out && E == 256 && e == 0) offsets_out[256] = s_off[256];
 }
 
+// A pair's destination row: offsets[e] + its position among expert e's slots, or -1
+// when cap > 0 and position >= cap (dropped: beyond the expert's capacity).
+// src_token and perm_prob are the inverse maps of the kept pairs.
+MOE_D void place_pair(int64_t t, int k, int e, int pos, int T, int K, int cap,
+                      const float* __restrict__ prob, const int32_t* s_off,
+                      int32_t* __restrict__ dst_row, int32_t* __restrict__ src_token,
+                      float* __restrict__ perm_prob, int* status) {
+  const int64_t i = t * K + k;
+  if (e < 0 || (cap > 0 && pos >= cap)) {
+    dst_row[i] = -1;
+    return;
+  }
+  const int r = s_off[e] + pos;
+  if (r < 0 || (int64_t)r >= (int64_t)T * K) {  // histograms that do not match idx
+    report(status, MOE_ERR_DEVICE_BOUNDS);
+    dst_row[i] = -1;
+    return;
+  }
+  dst_row[i] = r;
+  src_token[r] = (int32_t)t;
+  if (perm_prob) perm_prob[r] = prob ? __ldg(prob + i) : 1.f;
+}
+
 // Destination rows of chunk c's pairs: the pair's position among expert e's
-// slots is base[c][e] + its rank among the chunk's earlier tokens routed to e
-// (from ballots over the lanes' expert-id bits, E <= 256); dst_row =
-// offsets[e] + position, or -1 when cap > 0 and position >= cap (dropped:
-// beyond the expert's capacity).  src_token and perm_prob are the inverse
-// maps of the kept pairs.  Expert ids outside [0, E) get dst_row = -1
-// (reported by the histogram step).
-MOE_D void ranks_chunk(int c, int lane, const int32_t* __restrict__ idx,
+// slots is base[c][e] + its rank among the chunk's earlier tokens routed to e.
+// Every expert has a word of `my` ([E], this warp's) with a bit for each token
+// routed to it, so a rank is the number of lower bits.  (A token that names an
+// expert twice, which no router of this library does, has one bit for both: such
+// a chunk counts by ballots over the lanes' expert-id bits, E <= 256.)  Expert
+// ids outside [0, E) get dst_row = -1 (reported by the histogram step).
+MOE_D void ranks_chunk(int c, int lane, uint32_t* my, const int32_t* __restrict__ idx,
                        const float* __restrict__ prob, int T, int K, int E, int cap,
                        const int32_t* base, const int32_t* s_off, int32_t* __restrict__ dst_row,
                        int32_t* __restrict__ src_token, float* __restrict__ perm_prob,
@@ -110,48 +133,46 @@ MOE_D void ranks_chunk(int c, int lane, const int32_t* __restrict__ idx,
   const int64_t t = (int64_t)c * kChunk + lane;
   const bool valid = t < T;
   const unsigned lt_mask = (1u << lane) - 1u;
-  int my_e[16], rank[16];
-  for (int k = 0; k < K; ++k) {
-    const int e = valid ? __ldg(idx + t * K + k) : -1;
-    my_e[k] = (e >= 0 && e < E) ? e : -1;
-    rank[k] = 0;
-  }
-  for (int k2 = 0; k2 < K; ++k2) {
-    const int v = my_e[k2];
-    const unsigned present = __ballot_sync(0xffffffffu, v >= 0);
-    unsigned bits[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) bits[b] = __ballot_sync(0xffffffffu, (v >> b) & 1);
-    for (int k = 0; k < K; ++k) {
-      const int e = my_e[k];
-      unsigned m = present & lt_mask;
-#pragma unroll
-      for (int b = 0; b < 8; ++b) m &= ((e >> b) & 1) ? bits[b] : ~bits[b];
-      rank[k] += __popc(m);
-    }
-  }
+  for (int e = lane; e < E; e += 32) my[e] = 0;
+  __syncwarp();
+  bool twice = false;
   if (valid) {
+#pragma unroll 4
     for (int k = 0; k < K; ++k) {
-      const int e = my_e[k];
-      if (e < 0) {
-        dst_row[t * K + k] = -1;
-        continue;
-      }
-      const int pos = base[(int64_t)c * E + e] + rank[k];  // global or shared memory
-      if (cap > 0 && pos >= cap) {
-        dst_row[t * K + k] = -1;
-        continue;
-      }
-      const int r = s_off[e] + pos;
-      if (r < 0 || (int64_t)r >= (int64_t)T * K) {  // histograms that do not match idx
-        report(status, MOE_ERR_DEVICE_BOUNDS);
-        dst_row[t * K + k] = -1;
-        continue;
-      }
-      dst_row[t * K + k] = r;
-      src_token[r] = (int32_t)t;
-      if (perm_prob) perm_prob[r] = prob ? __ldg(prob + t * K + k) : 1.f;
+      const int e = __ldg(idx + t * K + k);
+      if (e >= 0 && e < E) twice |= (atomicOr(&my[e], 1u << lane) >> lane) & 1u;
     }
+  }
+  __syncwarp();
+  if (!__any_sync(0xffffffffu, twice)) {
+    if (!valid) return;
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+      int e = __ldg(idx + t * K + k);
+      if (e < 0 || e >= E) e = -1;
+      const int pos = e < 0 ? 0 : base[(int64_t)c * E + e] + __popc(my[e] & lt_mask);
+      place_pair(t, k, e, pos, T, K, cap, prob, s_off, dst_row, src_token, perm_prob, status);
+    }
+    return;
+  }
+  for (int k = 0; k < K; ++k) {
+    int e = valid ? __ldg(idx + t * K + k) : -1;
+    if (e < 0 || e >= E) e = -1;
+    int rank = 0;
+    for (int k2 = 0; k2 < K; ++k2) {
+      int v = valid ? __ldg(idx + t * K + k2) : -1;
+      if (v < 0 || v >= E) v = -1;
+      unsigned m = __ballot_sync(0xffffffffu, v >= 0) & lt_mask;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const unsigned bits = __ballot_sync(0xffffffffu, (v >> b) & 1);
+        m &= ((e >> b) & 1) ? bits : ~bits;
+      }
+      rank += __popc(m);
+    }
+    if (valid)
+      place_pair(t, k, e, e < 0 ? 0 : base[(int64_t)c * E + e] + rank, T, K, cap, prob, s_off,
+                 dst_row, src_token, perm_prob, status);
   }
 }
 
@@ -222,16 +243,47 @@ __global__ void __launch_bounds__(256) chunk_hist_kernel(const int32_t* __restri
   if (c < NC) hist_chunk(c, lane, sh + warp * E, idx, T, K, E, hist, status);
 }
 
-// Warp per expert: exclusive scan of hist[:, e] over the chunks.
-__global__ void __launch_bounds__(256) chunk_scan_kernel(const int32_t* __restrict__ hist, int NC,
-                                                         int E, int cap,
-                                                         int32_t* __restrict__ base,
-                                                         int32_t* __restrict__ counts) {
-  const int lane = threadIdx.x & 31;
-  const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+// 32 experts a block (a lane each, so that a warp's loads are whole lines), the chunks
+// shared among 32 warps: each adds up its chunks, the sums are scanned, and each writes
+// the exclusive scan of its own.
+__global__ void __launch_bounds__(1024) chunk_scan_kernel(const int32_t* __restrict__ hist, int NC,
+                                                          int E, int cap,
+                                                          int32_t* __restrict__ base,
+                                                          int32_t* __restrict__ counts) {
+  __shared__ int32_t s_sum[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  const int per = (NC + 31) / 32, c0 = min(warp * per, NC), c1 = min(c0 + per, NC);
   pdl_wait();
   pdl_trigger();
-  if (e < E) scan_expert(e, lane, hist, NC, E, cap, base, counts);
+  int sum = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) sum += __ldg(hist + (int64_t)c * E + e);
+  }
+  s_sum[lane][warp] = sum;
+  __syncthreads();
+  {  // warp w scans expert w's 32 sums
+    const int v = s_sum[warp][lane];
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    s_sum[warp][lane] = incl - v;
+    const int ew = blockIdx.x * 32 + warp;
+    if (lane == 31 && ew < E) counts[ew] = (cap > 0 && incl > cap) ? cap : incl;
+  }
+  __syncthreads();
+  if (e >= E) return;
+  int run = s_sum[lane][warp];
+#pragma unroll 8
+  for (int c = c0; c < c1; ++c) {
+    const int v = __ldg(hist + (int64_t)c * E + e);
+    base[(int64_t)c * E + e] = run;
+    run += v;
+  }
 }
 
 // Block: exclusive scan of counts into shared offsets, then one warp per chunk
@@ -243,13 +295,14 @@ __global__ void __launch_bounds__(256) chunk_ranks_kernel(
     int32_t* __restrict__ src_token, float* __restrict__ perm_prob, int* status) {
   __shared__ int32_t s_off[257];
   __shared__ int32_t s_warp[8];
+  extern __shared__ uint32_t s_bits[];  // [8][E]
   pdl_wait();
   pdl_trigger();
   block_offsets(counts, E, s_off, s_warp, offsets_out);
   const int c = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (c < NC)
-    ranks_chunk(c, threadIdx.x & 31, idx, prob, T, K, E, cap, base, s_off, dst_row, src_token,
-                perm_prob, status);
+    ranks_chunk(c, threadIdx.x & 31, s_bits + (threadIdx.x >> 5) * E, idx, prob, T, K, E, cap, base,
+                s_off, dst_row, src_token, perm_prob, status);
 }
 
 // Steps 2 and 3 in one kernel for small batches (NC * E <= kScanInBlock):
@@ -270,10 +323,25 @@ __global__ void __launch_bounds__(256) chunk_scan_ranks_kernel(
   int32_t* s_base = sh;                        // [NC][E]: hist, then base in place
   int32_t* s_cnt = s_base + (int64_t)NC * E;   // [E]
   int32_t* s_off = s_cnt + E;                  // [E + 1]
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_off + E + 1);  // [8][E]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t i = threadIdx.x; i < (int64_t)NC * E; i += blockDim.x) s_base[i] = __ldg(hist + i);
+#pragma unroll 8
+  for (int i = threadIdx.x; i < NC * E; i += 256) s_base[i] = __ldg(hist + i);
   __syncthreads();
-  for (int e = warp; e < E; e += 8) scan_expert(e, lane, s_base, NC, E, cap, s_base, s_cnt);
+  if (NC <= 64) {  // a thread an expert (at most 256), else a warp
+    const int e = threadIdx.x;
+    int run = 0;
+    if (e < E) {
+      for (int c = 0; c < NC; ++c) {
+        const int v = s_base[c * E + e];
+        s_base[c * E + e] = run;
+        run += v;
+      }
+      s_cnt[e] = (cap > 0 && run > cap) ? cap : run;
+    }
+  } else {
+    for (int e = warp; e < E; e += 8) scan_expert(e, lane, s_base, NC, E, cap, s_base, s_cnt);
+  }
   __syncthreads();
   if (warp == 0) {  // s_off = exclusive scan of the counts
     int running = 0;
@@ -303,8 +371,8 @@ __global__ void __launch_bounds__(256) chunk_scan_ranks_kernel(
   __syncthreads();
   const int c = blockIdx.x * 8 + warp;
   if (c < NC)
-    ranks_chunk(c, lane, idx, prob, T, K, E, cap, s_base, s_off, dst_row, src_token, perm_prob,
-                status);
+    ranks_chunk(c, lane, s_bits + warp * E, idx, prob, T, K, E, cap, s_base, s_off, dst_row,
+                src_token, perm_prob, status);
 }
 
 // One warp per token (the grid covers every token, so the block scheduler
@@ -352,16 +420,16 @@ cudaError_t launch_permute_maps(const moe_config_t& c, const int32_t* idx, const
     chunk_hist_kernel<<<blocks, 256, 8 * c.E * sizeof(int32_t), s>>>(idx, c.T, c.K, c.E, NC, hist,
                                                                     status);
   if ((int64_t)NC * c.E <= kScanInBlock) {
-    const size_t bytes = sizeof(int32_t) * ((size_t)NC * c.E + 2 * c.E + 1);
+    const size_t bytes = sizeof(int32_t) * ((size_t)NC * c.E + 2 * c.E + 1 + 8 * c.E);
     return pdl_launch(chunk_scan_ranks_kernel, dim3(blocks), dim3(256), bytes, s, idx, prob, c.T,
                       c.K, c.E, c.capacity, NC, (const int32_t*)hist, counts, offsets, dst_row,
                       src_token, perm_prob, status);
   }
   // each step may be scheduled while the one before it ends (it waits for it first)
-  cudaError_t e = pdl_launch(chunk_scan_kernel, dim3((unsigned)ceil_div(c.E, 8)), dim3(256), 0, s,
+  cudaError_t e = pdl_launch(chunk_scan_kernel, dim3((unsigned)ceil_div(c.E, 32)), dim3(1024), 0, s,
                              (const int32_t*)hist, NC, c.E, c.capacity, base, counts);
   if (e != cudaSuccess) return e;
-  return pdl_launch(chunk_ranks_kernel, dim3(blocks), dim3(256), 0, s, idx, prob, c.T, c.K, c.E,
+  return pdl_launch(chunk_ranks_kernel, dim3(blocks), dim3(256), 8 * c.E * sizeof(uint32_t), s, idx, prob, c.T, c.K, c.E,
                     c.capacity, NC, (const int32_t*)base, (const int32_t*)counts, offsets, dst_row,
                     src_token, perm_prob, status);
 }

@@ -117,15 +117,15 @@ __global__ void __launch_bounds__(256)
     *reinterpret_cast<uint4*>(dt + (int64_t)j * N) = make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
 }
 
-// One warp a token: its h codes and h / 128 scales to its K rows.  The token's row is
-// in registers before the maps' last step has ended (programmatic dependent launch);
-// the destinations are read after it.
-template <int KMAX>
+// One warp V x 512 bytes of a token's codes (grid.y of them a row), to its K rows, and
+// the row's h / 128 scales with the first.  What it reads is in registers before the
+// maps' last step has ended (programmatic dependent launch); the destinations are read
+// after it.
+template <int KMAX, int V>
 __global__ void __launch_bounds__(256)
     fp8_scatter_kernel(const uint8_t* __restrict__ x_q, const float* __restrict__ x_sf,
                        const int32_t* __restrict__ dst_row, int T, int K, int h,
                        uint8_t* __restrict__ q, float* __restrict__ sf, int* status) {
-  constexpr int kMaxVec = 8;
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (t >= T) {
@@ -133,13 +133,13 @@ __global__ void __launch_bounds__(256)
     return;
   }
   const int64_t P = (int64_t)T * K;
-  const int nvec = h / 16, KB = h / BLOCK;
+  const int nvec = h / 16, KB = h / BLOCK, v0 = blockIdx.y * (32 * V) + lane;
   const uint4* src = reinterpret_cast<const uint4*>(x_q + t * h);
-  uint4 u[kMaxVec];
+  uint4 u[V];
 #pragma unroll
-  for (int i = 0; i < kMaxVec; ++i)
-    if (i * 32 + lane < nvec) u[i] = __ldcs(src + i * 32 + lane);
-  float s0 = lane < KB ? __ldg(x_sf + t * KB + lane) : 0.f;
+  for (int i = 0; i < V; ++i)
+    if (v0 + i * 32 < nvec) u[i] = __ldcs(src + v0 + i * 32);
+  float s0 = blockIdx.y == 0 && lane < KB ? __ldg(x_sf + t * KB + lane) : 0.f;
   pdl_wait();
   int64_t row[KMAX];
 #pragma unroll
@@ -153,21 +153,15 @@ __global__ void __launch_bounds__(256)
         report(status, MOE_ERR_DEVICE_BOUNDS);
     }
   }
-  for (int v0 = 0; v0 < nvec; v0 += 32 * kMaxVec) {
-    if (v0 > 0) {
 #pragma unroll
-      for (int i = 0; i < kMaxVec; ++i)
-        if (v0 + i * 32 + lane < nvec) u[i] = __ldcs(src + v0 + i * 32 + lane);
-    }
+  for (int k = 0; k < KMAX; ++k) {
+    if (row[k] < 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(q + row[k] * h);
 #pragma unroll
-    for (int k = 0; k < KMAX; ++k) {
-      if (row[k] < 0) continue;
-      uint4* dst = reinterpret_cast<uint4*>(q + row[k] * h) + v0;
-#pragma unroll
-      for (int i = 0; i < kMaxVec; ++i)
-        if (v0 + i * 32 + lane < nvec) dst[i * 32 + lane] = u[i];
-    }
+    for (int i = 0; i < V; ++i)
+      if (v0 + i * 32 < nvec) dst[v0 + i * 32] = u[i];
   }
+  if (blockIdx.y) return;
   for (int b = lane; b < KB; b += 32) {
     if (b >= 32) s0 = __ldg(x_sf + t * KB + b);
 #pragma unroll
@@ -199,14 +193,19 @@ cudaError_t launch_fp8_quantize_weights(int groups, int N, int K, const void* w,
 }
 
 cudaError_t launch_fp8_scatter(const moe_config_t& c, const uint8_t* x_q, const float* x_sf,
-                               const int32_t* dst_row, uint8_t* q, float* sf, int* status,
+                               const int32_t* dst_row, uint8_t* q, float* sf, int sms, int* status,
                                cudaStream_t s) {
   if (c.T == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)ceil_div(c.T, 8);
-// (directly behind the maps' steps on the stream: see the kernel)
-#define MOE_FS(KM)                                                                                 \
-  pdl_launch(fp8_scatter_kernel<KM>, dim3(grid), dim3(256), 0, s, x_q, x_sf, dst_row, c.T, c.K,    \
-             c.h, q, sf, status)
+  // 8 vectors a thread; 2 while that leaves an SM less than 16 warps
+  const bool small = c.T * ceil_div(c.h, 4096) < 16LL * sms;
+  const int per = small ? 1024 : 4096;
+  const dim3 grid((unsigned)ceil_div(c.T, 8), (unsigned)ceil_div(c.h, per));
+  // (directly behind the maps' steps on the stream: see the kernel)
+#define MOE_FS(KM)                                                                                  \
+  (small ? pdl_launch(fp8_scatter_kernel<KM, 2>, grid, dim3(256), 0, s, x_q, x_sf, dst_row, c.T,    \
+                      c.K, c.h, q, sf, status)                                                      \
+         : pdl_launch(fp8_scatter_kernel<KM, 8>, grid, dim3(256), 0, s, x_q, x_sf, dst_row, c.T,    \
+                      c.K, c.h, q, sf, status))
   return c.K <= 2 ? MOE_FS(2) : c.K <= 4 ? MOE_FS(4) : c.K <= 8 ? MOE_FS(8) : MOE_FS(16);
 #undef MOE_FS
 }
