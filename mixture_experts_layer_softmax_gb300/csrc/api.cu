@@ -78,7 +78,7 @@ cudaError_t launch_fp8_product(bool, int, const uint8_t*, const float*, int, con
                                uint8_t*, float*, int, int*, cudaStream_t);
 size_t rmsnorm_bwd_workspace(int64_t rows, int h);
 cudaError_t launch_rmsnorm_fwd(int64_t, int, int, const void*, const void*, const float*, float,
-                               void*, void*, uint8_t*, float*, float*, cudaStream_t);
+                               void*, void*, uint8_t*, float*, float*, int, cudaStream_t);
 cudaError_t launch_rmsnorm_bwd(int64_t, int, int, const void*, const void*, const float*,
                                const float*, const void*, void*, float*, float*, int, int*,
                                cudaStream_t);
@@ -752,8 +752,9 @@ moe_status_t moe_rmsnorm_fwd(int64_t rows, int32_t h, int32_t dtype, const void*
       !al16(rstd))
     return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (!device_info()) return MOE_ERR_CUDA;
-  return cuda_status(launch_rmsnorm_fwd(rows, h, dtype, x, res, w, eps, sum, y, q, sf, rstd,
+  const DeviceInfo* d = device_info();
+  if (!d) return MOE_ERR_CUDA;
+  return cuda_status(launch_rmsnorm_fwd(rows, h, dtype, x, res, w, eps, sum, y, q, sf, rstd, d->sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 

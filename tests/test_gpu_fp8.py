@@ -492,3 +492,69 @@ def test_path_captured_twice_and_replayed():
             for t, u in zip(p.outputs(), outs):
                 assert torch.equal(t.view(torch.uint8), u.view(torch.uint8))
     assert M.moe_get_error() == M.MOE_OK
+
+
+@pytest.mark.parametrize("T,K", [(100, 2), (3, 2)])
+@pytest.mark.parametrize("offsets", [[5, -3, 900, 2, 7], [-10, 0, 10 ** 9, -(10 ** 9), 3], [0, 4, 4, 2, 6], [6, 6, 6, 6, 6]])
+def test_offsets_outside_the_rows_are_kept_within_them(T, K, offsets):
+    """Boundaries are taken between 0 and P and never before the one ahead of them."""
+    M = lib()
+    c = _case(61, T, K, 4, 256, 128)
+    c["offsets"] = np.maximum.accumulate(np.clip(offsets, 0, c["P"]))
+    want = _check_products(M, c)
+    P, h, F = c["P"], c["h"], c["F"]
+    cfg = M.make_config(T, h, 4, K, F)
+    xq, xsf = quantize_dev(M, c["x"])
+    w1q, w1sf = weights_dev(M, c["w1"], 4)
+    a = torch.full((P, F), 33.0, dtype=torch.bfloat16, device="cuda")
+    M.moe_expert_fc1_fp8(cfg, xq, xsf, torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                         torch.from_numpy(c["p"]).cuda(), w1q, w1sf, None, a, None, None)
+    assert M.moe_get_error() == M.MOE_OK and torch.equal(a, want[1])
+
+
+def test_strided_and_host_tensors_are_refused():
+    M = lib()
+    x = torch.zeros(128, 256, dtype=torch.bfloat16, device="cuda")
+    q, sf = u8(128, 256), f32(128, 2)
+    for bad in (x.t().contiguous().t(), x[:, :128], x.cpu()):
+        with pytest.raises(ValueError):
+            M.moe_fp8_quantize(128, 256, bad, q, sf)
+    with pytest.raises(ValueError):
+        M.moe_rmsnorm_fwd(128, 256, M.MOE_BF16, x, x.t().contiguous().t(), f32(256), 1e-6, y=x)
+
+
+def test_large_offsets_of_bytes():
+    """Rows whose byte offsets pass 2^31 and 2^32: the last rows are computed like the first."""
+    M = lib()
+    T, K, h, F = 300_000, 1, 16384, 128                    # 4.9e9 code bytes, 9.8e9 of bf16
+    blk = bf16(np.random.default_rng(71).standard_normal((300, h)))
+    x = to_dev(blk, "bf16").repeat(T // 300, 1)
+    q, sf = torch.empty(T, h, dtype=torch.uint8, device="cuda"), torch.empty(T, h // 128, device="cuda")
+    M.moe_fp8_quantize(T, h, x, q, sf)
+    oq, osf = X.quantize(blk)
+    for lo in (0, T // 2 // 300 * 300, T - 300):
+        np.testing.assert_array_equal(q[lo:lo + 300].cpu().numpy(), oq)
+        np.testing.assert_array_equal(sf[lo:lo + 300].cpu().numpy(), osf)
+    w1 = bf16(np.random.default_rng(72).standard_normal((2 * F, h)) / 128)
+    wq, wsf = weights_dev(M, w1, 1)
+    cfg = M.make_config(T, h, 1, 1, F)
+    a = torch.empty(T, F, dtype=torch.bfloat16, device="cuda")
+    M.moe_expert_fc1_fp8(cfg, q, sf, torch.tensor([0, T], dtype=torch.int32, device="cuda"), None, wq, wsf, None, a,
+                         None, None)
+    assert M.moe_get_error() == M.MOE_OK
+    assert torch.equal(a[:300], a[-300:]) and torch.equal(a[:300], a[150_000:150_300])
+    y, rq = torch.empty_like(x), torch.empty_like(q)
+    M.moe_rmsnorm_fwd(T, h, M.MOE_BF16, x, None, torch.ones(h, device="cuda"), 1e-6, y=y, q=rq, sf=sf)
+    assert torch.equal(y[:300], y[-300:]) and torch.equal(rq[:300], rq[-300:])
+    dx, dw = torch.empty_like(x), torch.empty(h, device="cuda")
+    r = torch.rand(300, device="cuda").repeat(T // 300)
+    ws = torch.empty(M.moe_rmsnorm_bwd_workspace_size(T, h), dtype=torch.uint8, device="cuda")
+    M.moe_rmsnorm_bwd(T, h, M.MOE_BF16, y, x, r, torch.ones(h, device="cuda"), None, dx, dw, ws)
+    assert torch.equal(dx[:300], dx[-300:])
+    dst = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).view(T, 1).contiguous()
+    M.moe_unpermute_combine_bwd(cfg, x, None, dst, None, y)
+    assert torch.equal(y[:300], x[-300:].flip(0)) and torch.equal(y[-300:], x[:300].flip(0))
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    cws = torch.empty(M.moe_workspace_size(M.make_config(T, h, 1, 1, 8)), dtype=torch.uint8, device="cuda")
+    M.moe_permute_fp8(M.make_config(T, h, 1, 1, 8), q, sf, idx, None, rq, torch.empty_like(sf), ws=cws, **_maps(M, T, 1, 1))
+    assert M.moe_get_error() == M.MOE_OK and torch.equal(rq[-300:], q[-300:]) and torch.equal(rq[:300], q[:300])
