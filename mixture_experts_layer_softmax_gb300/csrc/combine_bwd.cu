@@ -10,7 +10,7 @@ namespace {
 
 // W warps a token; below four, several tokens a block of 128 threads.
 template <typename T, int KMAX, int W>
-__global__ void __launch_bounds__(W > 4 ? 32 * W : 128)
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : KMAX <= 8 ? 5 : 4)
     combine_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ y_perm,
                        const int32_t* __restrict__ dst_row, const float* __restrict__ w, int ntok,
                        int K, int h, T* __restrict__ dy_perm, float* __restrict__ dw, int* status) {

@@ -9,9 +9,9 @@
 // Persistent kernel, one CTA an SM, tiles of 128 rows x 256 weight rows (FC1: 128
 // gate and the matching 128 up rows):
 //   warp 0     TMA producer: 4 stages of {A 128 x 128 B, W 256 x 128 B}.
-//   warp 1     TMEM owner and MMA issuer: a stage's products go to one of two
+//   warps 1-2  MMA issuers (warp 1 owns TMEM): a stage's products go to one of two
 //              256-column accumulators, each given back once a block.
-//   warps 2-3  scales: each row's sa sw of eight blocks at a time, to shared memory
+//   warp 3     scales: each row's sa sw of eight blocks at a time, to shared memory
 //              (a joining thread that reads its own row's scales touches a line of its
 //              own with each, and keeps registers for them).
 //   warps 4-11 two warps a TMEM lane quarter (32 rows), each one half of the
@@ -42,7 +42,7 @@ constexpr int SB = 8;  // blocks of scales at a time
 
 struct Ctl {
   float2 scale[2][SB][TM + 4];  // [block][row]: sa times the scales of the tile's two weight blocks
-  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], sfull[2], sempty[2], meet[4], drain;
+  uint64_t full[STAGES], empty[STAGES], tfull[2], tempty[2], sfull[2], sempty[2], meet[4], drain[2];
   uint32_t tmem_base;
   int abort;
   int off[257], tile_start[257], part[8];
@@ -180,11 +180,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(tc::smem_u32(&ctl.tfull[b]), 1);
       tc::mbar_init(tc::smem_u32(&ctl.tempty[b]), 8);
-      tc::mbar_init(tc::smem_u32(&ctl.sfull[b]), 2);
+      tc::mbar_init(tc::smem_u32(&ctl.sfull[b]), 1);
       tc::mbar_init(tc::smem_u32(&ctl.sempty[b]), 8);
+      tc::mbar_init(tc::smem_u32(&ctl.drain[b]), 1);
     }
     for (int q = 0; q < 4; ++q) tc::mbar_init(tc::smem_u32(&ctl.meet[q]), 2);
-    tc::mbar_init(tc::smem_u32(&ctl.drain), 1);
     ctl.abort = 0;
     tc::fence_barrier_init();
     tc::fence_proxy_async_smem();
@@ -239,45 +239,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((issued >> s) & 1u)
         tc::mbar_wait(tc::smem_u32(&ctl.full[s]), (issued_par >> s) & 1u, wdrain);
     __syncwarp();
-   } else if (warp == 1) {
-    // ================= MMA issuer: likewise =================
+   } else if (warp <= 2) {
+    // ================= MMA issuers: likewise, one for each accumulator =================
+    // (A step's two waits, four MMAs and two commits take one warp longer than the 512
+    // cycles that the MMAs do.)
     const bool elected = tc::elect_one();
-    int stage = 0;
-    uint32_t phase = 0, step = 0;
-    bool ok = true;
+    const uint32_t buf = warp - 1;
     const uint64_t a_base = tc::desc_kmajor_sw128(tc::smem_u32(sA));
     const uint64_t w_base = tc::desc_kmajor_sw128(tc::smem_u32(sW));
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      for (int kb = 0; kb < KB; ++kb, ++step) {
-        const uint32_t buf = step & 1;
-        if (!tc::mbar_wait(tc::smem_u32(&ctl.tempty[buf]), ((step >> 1) & 1) ^ 1, wc) ||
-            !tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), phase, wc)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        const uint64_t ad = a_base + (uint32_t)(stage * (A_BYTES >> 4));
-        const uint64_t wd = w_base + (uint32_t)(stage * (W_BYTES >> 4));
-        if (elected) {
+    const int tiles = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int64_t steps = tiles > 0 ? (int64_t)tiles * KB : 0;
+    for (int64_t step = buf; step < steps; step += 2) {
+      const uint32_t stage = (uint32_t)step % STAGES;
+      if (!tc::mbar_wait(tc::smem_u32(&ctl.tempty[buf]), ((uint32_t)(step >> 1) & 1) ^ 1, wc) ||
+          !tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), (uint32_t)(step / STAGES) & 1, wc))
+        break;
+      tc::fence_after_sync();
+      const uint64_t ad = a_base + stage * (A_BYTES >> 4), wd = w_base + stage * (W_BYTES >> 4);
+      if (elected) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_f8(tmem_base + buf * TN, ad + 2 * k, wd + 2 * k, tc::idesc_e4m3_f32(TM, TN), k != 0);
-          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
-          tc::mma_commit(tc::smem_u32(&ctl.tfull[buf]));
-        }
-        __syncwarp();
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        for (int k = 0; k < 4; ++k)
+          tc::mma_f8(tmem_base + buf * TN, ad + 2 * k, wd + 2 * k, tc::idesc_e4m3_f32(TM, TN), k != 0);
+        tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+        tc::mma_commit(tc::smem_u32(&ctl.tfull[buf]));
       }
+      __syncwarp();
     }
     __syncwarp();
     if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
-      if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain));
-      tc::mbar_wait(tc::smem_u32(&ctl.drain), 0, wdrain);
+      if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain[buf]));
+      tc::mbar_wait(tc::smem_u32(&ctl.drain[buf]), 0, wdrain);
     }
     __syncwarp();
    } else {
-    // ================= scales: 64 rows a warp, a lane one block of every fourth row =================
-    const int j = lane & 7, r0 = (warp - 2) * 64 + (lane >> 3);
+    // ================= scales: a lane has one block of every fourth row =================
+    const int j = lane & 7, r0 = lane >> 3;
     const int wblk = p.Nw / BLOCK;
     uint32_t n = 0;
     bool ok = true;
@@ -291,16 +287,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t buf = n & 1;
         const int k = min(kb + j, KB - 1);
         const float w0 = __ldg(sw0 + k), w1 = __ldg(sw1 + k);
+#pragma unroll 1
+        for (int r = r0; r < TM; r += 64) {
+          float a[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float a[8];
+          for (int i = 0; i < 16; ++i)  // (a row behind the expert's takes its last row's, which go nowhere)
+            a[i] = __ldg(sa + (int64_t)min(r + 4 * i, t.rows - 1) * KB + k);
+          if (r == r0 && !tc::mbar_wait(tc::smem_u32(&ctl.sempty[buf]), ((n >> 1) & 1) ^ 1, wc)) { ok = false; break; }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)  // (a row behind the expert's takes its last row's, which go nowhere)
-            a[i] = __ldg(sa + (int64_t)min(r0 + 32 * h + 4 * i, t.rows - 1) * KB + k);
-          if (h == 0 && !tc::mbar_wait(tc::smem_u32(&ctl.sempty[buf]), ((n >> 1) & 1) ^ 1, wc)) { ok = false; break; }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ctl.scale[buf][j][r0 + 32 * h + 4 * i] = make_float2(a[i] * w0, a[i] * w1);
+          for (int i = 0; i < 16; ++i) ctl.scale[buf][j][r + 4 * i] = make_float2(a[i] * w0, a[i] * w1);
         }
         if (!ok) break;
         __syncwarp();
