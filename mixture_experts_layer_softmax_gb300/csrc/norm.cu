@@ -173,7 +173,7 @@ template <typename T, int NV, bool ONE>  // ONE: R is 1
 __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
     rmsnorm_bwd_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
                        const float* __restrict__ w, const T* dsum, int64_t rows, int h, int W,
-                       int G, int r_stage, int stages, T* dx, float* __restrict__ part, int* status) {
+                       int G, int r_stage, int stages, bool w_shared, T* dx, float* __restrict__ part, int* status) {
   const int R = ONE ? 1 : r_stage;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ uint64_t full[kBwdWarps][kRing], empty[kBwdWarps][kRing];
@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
   pdl_trigger();  // (the second kernel waits for all of this one before it reads a part)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int arrays = dsum ? 3 : 2;
-  float* s_w = reinterpret_cast<float*>(dyn);
+  // (w stays where it is when it would cost the second stage)
+  const float* s_w = w_shared ? reinterpret_cast<float*>(dyn) : w;
   const uint32_t array_bytes = (uint32_t)(R * h * sizeof(T)), stage_bytes = arrays * array_bytes;
   const int64_t chunks = (rows + R - 1) / R;
-  uint8_t* ring = dyn + align_up((size_t)h * 4, 128);  // [group][stage][array]
+  uint8_t* ring = dyn + (w_shared ? align_up((size_t)h * 4, 128) : 0);  // [group][stage][array]
   if (threadIdx.x == 0) {
     for (int g = 0; g < G; ++g) {
       for (int s = 0; s < stages; ++s) {
@@ -197,8 +198,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
     quit = 0;
     tc::fence_barrier_init();
   }
-  for (int c = threadIdx.x * 4; c < h; c += blockDim.x * 4)
-    *reinterpret_cast<float4*>(s_w + c) = __ldg(reinterpret_cast<const float4*>(w + c));
+  if (w_shared)
+    for (int c = threadIdx.x * 4; c < h; c += blockDim.x * 4)
+      *reinterpret_cast<float4*>(dyn + 4 * c) = __ldg(reinterpret_cast<const float4*>(w + c));
   __syncthreads();
   if (warp == kBwdWarps) {
     if (lane == 0) {
@@ -246,14 +248,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
     // a wait that gave up is known to every warp of the group behind the next barrier, by
     // a flag of that row's parity (the other may be raised before all have read it)
     const tc::WaitCtl wc{status, &abort[g][parity], 2000000000ull, 0};
+    const int64_t row0 = c * R;
+    const int n_rows = ONE ? 1 : rows - row0 < R ? (int)(rows - row0) : R;
+    float r = __ldg(rstd + row0);
     tc::mbar_wait(tc::smem_u32(&full[g][stage]), phase, wc);
     const T* s_dy = reinterpret_cast<const T*>(ring + (size_t)(g * stages + stage) * stage_bytes);
-    const int64_t row0 = c * R;
-    const int n_rows = rows - row0 < R ? (int)(rows - row0) : R;
     for (int k = 0; k < n_rows; ++k, parity ^= 1, s_dy += h) {
       const T *s_sum = s_dy + R * h, *s_ds = s_dy + 2 * R * h;
       const int64_t row = row0 + k;
-      const float r = __ldg(rstd + row);
+      const float r_next = k + 1 < n_rows ? __ldg(rstd + row + 1) : 0.f;
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -296,6 +299,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
           store8(dx + row * h + col, h - col, o);
         }
       }
+      r = r_next;
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(tc::smem_u32(&empty[g][stage]));
@@ -530,13 +534,17 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
   }
   int parts;
   if (h <= kBwdMaxCols) {
-    const size_t row = (size_t)h * sizeof(T), head = align_up((size_t)h * 4, 128);
-    const int W = bwd_warps(h), G = bwd_groups(h, W, row * (d ? 3 : 2));
+    const size_t row = (size_t)h * sizeof(T);
+    size_t head = align_up((size_t)h * 4, 128);
+    int W = bwd_warps(h);
+    const int G = bwd_groups(h, W, row * (d ? 3 : 2));
+    while (G * W < kBwdWarps && h > W * 256) W *= 2;  // warps that would be idle: fewer vectors a thread
     // short rows come in copies of up to 4 KB (one thread issues them all), while every
     // group has some
     const int64_t share = rows / ((int64_t)most * G), want = 4096 / (int64_t)row;
     const int R = (int)(share < 2 || want < 2 ? 1 : share < want ? share : want);
     const size_t stage = R * row * (d ? 3 : 2);
+    if (2 * G * stage > kRingBytes - head) head = 0;
     const int64_t blocks = ceil_div(ceil_div(rows, R), G);
     const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     const int fit = (int)((kRingBytes - head) / (G * stage)), stages = fit < kRing ? fit : kRing;
@@ -549,7 +557,8 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
     const size_t smem = head + G * stages * stage;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, R, stages, o, pt, status);
+    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, R, stages, head > 0, o,
+                                                   pt, status);
     parts = (int)grid;
   } else {
     const unsigned grid = (unsigned)(rows < most ? rows : most);
