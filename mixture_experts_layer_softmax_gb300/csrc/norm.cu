@@ -169,11 +169,14 @@ constexpr int kBwdWarps = 16;
 constexpr int kRing = 8;                 // stages a group at most
 constexpr int kRingBytes = 216 * 1024;   // shared memory of w and the stages
 
-template <typename T, int NV, bool ONE>  // ONE: R is 1
+enum BwdStage { kManyRows, kOneRow, kOneRowAlone };  // (the last: w stays where it is)
+
+template <typename T, int NV, BwdStage MODE>
 __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
     rmsnorm_bwd_kernel(const T* dy, const T* sum, const float* __restrict__ rstd,
                        const float* __restrict__ w, const T* dsum, int64_t rows, int h, int W,
-                       int G, int r_stage, int stages, bool w_shared, T* dx, float* __restrict__ part, int* status) {
+                       int G, int r_stage, int stages, T* dx, float* __restrict__ part, int* status) {
+  constexpr bool ONE = MODE != kManyRows, w_shared = MODE != kOneRowAlone;
   const int R = ONE ? 1 : r_stage;
   extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ uint64_t full[kBwdWarps][kRing], empty[kBwdWarps][kRing];
@@ -182,7 +185,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
   pdl_trigger();  // (the second kernel waits for all of this one before it reads a part)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int arrays = dsum ? 3 : 2;
-  // (w stays where it is when it would cost the second stage)
   const float* s_w = w_shared ? reinterpret_cast<float*>(dyn) : w;
   const uint32_t array_bytes = (uint32_t)(R * h * sizeof(T)), stage_bytes = arrays * array_bytes;
   const int64_t chunks = (rows + R - 1) / R;
@@ -544,21 +546,20 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
     const int64_t share = rows / ((int64_t)most * G), want = 4096 / (int64_t)row;
     const int R = (int)(share < 2 || want < 2 ? 1 : share < want ? share : want);
     const size_t stage = R * row * (d ? 3 : 2);
-    if (2 * G * stage > kRingBytes - head) head = 0;
+    if (2 * G * stage > kRingBytes - head) head = 0;  // w in shared memory would cost the second stage
     const int64_t blocks = ceil_div(ceil_div(rows, R), G);
     const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     const int fit = (int)((kRingBytes - head) / (G * stage)), stages = fit < kRing ? fit : kRing;
-    auto kern = R > 1 ? (h <= W * 256   ? rmsnorm_bwd_kernel<T, 1, false>
-                         : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2, false>
-                                        : rmsnorm_bwd_kernel<T, 4, false>)
-                      : (h <= W * 256   ? rmsnorm_bwd_kernel<T, 1, true>
-                         : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2, true>
-                                        : rmsnorm_bwd_kernel<T, 4, true>);
+#define MOE_BWD(MODE)                                             \
+  (h <= W * 256   ? rmsnorm_bwd_kernel<T, 1, MODE>                \
+   : h <= W * 512 ? rmsnorm_bwd_kernel<T, 2, MODE>                \
+                  : rmsnorm_bwd_kernel<T, 4, MODE>)
+    auto kern = R > 1 ? MOE_BWD(kManyRows) : head ? MOE_BWD(kOneRow) : MOE_BWD(kOneRowAlone);
+#undef MOE_BWD
     const size_t smem = head + G * stages * stage;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, R, stages, head > 0, o,
-                                                   pt, status);
+    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, R, stages, o, pt, status);
     parts = (int)grid;
   } else {
     const unsigned grid = (unsigned)(rows < most ? rows : most);
