@@ -416,7 +416,8 @@ moe_status_t moe_expert_fc2_fp8(const moe_config_t* cfg, const uint8_t* a_q, con
  *   outputs: sum [rows,h] dtype or NULL (v, the residual stream's new value); y
  *   [rows,h] dtype and / or q [rows,h] + sf [rows,h/128] (y in FP8, from fp32), one of
  *   them at least; rstd [rows] f32 or NULL (r, for the gradient).
- * Sums in fp32 and a fixed order.  sum and y may be x's or res's own buffers.
+ * Sums in fp32 and a fixed order (a sum of squares past fp32's range makes r 0).  sum
+ * and y may be x's or res's own buffers.
  * h: multiples of 4 (fp32) or 8 (bf16), of 128 for q, at most 65536, else
  * MOE_ERR_UNSUPPORTED; eps finite and >= 0. */
 moe_status_t moe_rmsnorm_fwd(int64_t rows, int32_t h, int32_t dtype, const void* x,
@@ -428,8 +429,9 @@ moe_status_t moe_rmsnorm_fwd(int64_t rows, int32_t h, int32_t dtype, const void*
  *   dy, sum (v) [rows,h] dtype; rstd [rows]; w [h]; dsum [rows,h] dtype or NULL (the
  *   gradient that reaches v by the residual stream); outputs dx [rows,h] (the
  *   gradient of x and of res; may be dy's, sum's or dsum's own buffer), dw [h] f32 or
- *   NULL.  ws: moe_rmsnorm_bwd_workspace_size(rows, h) bytes, needed for dw only.
- * Bitwise reproducible on one kind of device. */
+ *   NULL.  ws: moe_rmsnorm_bwd_workspace_size(rows, h) bytes, needed for dw only; calls
+ *   that can overlap on the GPU (two captured graphs, say) need one each.
+ * Bitwise reproducible on one kind of device; in place the last bits may be others. */
 moe_status_t moe_rmsnorm_bwd(int64_t rows, int32_t h, int32_t dtype, const void* dy,
                              const void* sum, const float* rstd, const float* w,
                              const void* dsum, void* dx, float* dw, void* ws, size_t ws_bytes,

@@ -19,8 +19,18 @@
 // While they evaluate and store a tile the MMAs run at most two blocks ahead.
 // Every wait is bounded; one that gives up records MOE_ERR_TIMEOUT and every role
 // leaves its loop.
+//
+// What bounds it, by leaving parts of the work out, for FC1 of 16384 rows, 8 experts,
+// 4096 -> 2 x 14336 (1552 us, 2.48 PFLOP/s; 1005 us at twice the measured bf16 rate):
+// the stages' copies alone 1100 us (48 KB a 512-cycle step, 75 bytes a clock and SM), the
+// MMAs and the hand-over 944, the joining alone 1190 (a packed FMA takes an SM quarter
+// 2.3 to 3 cycles, a TMEM load of 16 columns its latency), all but SiLU and stores 1444.
+// Steps: 4.0 ms with the joining's registers capped at 168 a thread (spills), 2.2 ms with
+// a register split, 1.78 with 16-column loads and intrinsics for the packed FMA (half the
+// moves), 1.65 with the scales in a warp of their own, 1.57 with 32-byte stores.
+// A tile of 128 x 128 (four accumulators) was slower (2.1 ms: the MMAs read A twice), and
+// so were 16 joining warps (2.1 ms).
 #include "fp8.cuh"
-#include "mx.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -205,104 +215,104 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::WaitCtl wdrain{p.status, nullptr, 1000000000ull, 0};
 
   if (warp < 4) {
-   tc::regs_dec<kRegsIssue>();
-   if (warp == 0) {
-    // ================= TMA producer: the warp runs the loop, one lane issues =================
-    const bool elected = tc::elect_one();
-    const uint64_t policy = p.once ? tc::evict_first_policy() : tc::evict_normal_policy();
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, issued_par = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const Tile t = tile_at<TM>(ctl, E, tile);
-      const int w0 = t.e * p.Nw + (SWIGLU ? t.nb * BLOCK : t.nb * TN);
-      // the second half: FC1's up rows; FC2's next 128 rows, where an odd last tile
-      // takes rows of the next expert (or, past the tensor, zeros) that go nowhere
-      const int w1 = SWIGLU ? w0 + p.N : w0 + BLOCK;
-      for (int kb = 0; kb < KB; ++kb) {
-        if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
+    tc::regs_dec<kRegsIssue>();
+    if (warp == 0) {
+      // ================= TMA producer: the warp runs the loop, one lane issues =================
+      const bool elected = tc::elect_one();
+      const uint64_t policy = p.once ? tc::evict_first_policy() : tc::evict_normal_policy();
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, issued_par = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        const Tile t = tile_at<TM>(ctl, E, tile);
+        const int w0 = t.e * p.Nw + (SWIGLU ? t.nb * BLOCK : t.nb * TN);
+        // the second half: FC1's up rows; FC2's next 128 rows, where an odd last tile
+        // takes rows of the next expert (or, past the tensor, zeros) that go nowhere
+        const int w1 = SWIGLU ? w0 + p.N : w0 + BLOCK;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!tc::mbar_wait(tc::smem_u32(&ctl.empty[stage]), phase ^ 1, wc)) { ok = false; break; }
+          if (elected) {
+            const uint32_t fb = tc::smem_u32(&ctl.full[stage]);
+            const uint32_t wd = tc::smem_u32(sW + stage * W_BYTES);
+            tc::mbar_arrive_expect_tx(fb, A_BYTES + W_BYTES);
+            tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BLOCK, t.row, fb);
+            tc::tma_load_2d_hint(wd, &tmW, kb * BLOCK, w0, fb, policy);
+            tc::tma_load_2d_hint(wd + W_BYTES / 2, &tmW, kb * BLOCK, w1, fb, policy);
+          }
+          __syncwarp();
+          issued |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      for (int s = 0; s < STAGES; ++s)
+        if ((issued >> s) & 1u)
+          tc::mbar_wait(tc::smem_u32(&ctl.full[s]), (issued_par >> s) & 1u, wdrain);
+      __syncwarp();
+    } else if (warp <= 2) {
+      // ================= MMA issuers: likewise, one for each accumulator =================
+      // (a step's two waits, four MMAs and two commits in one warp for both: 1567 us for
+      // FC1 of 16384 rows, against 1552)
+      const bool elected = tc::elect_one();
+      const uint32_t buf = warp - 1;
+      const uint64_t a_base = tc::desc_kmajor_sw128(tc::smem_u32(sA));
+      const uint64_t w_base = tc::desc_kmajor_sw128(tc::smem_u32(sW));
+      const int tiles = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+      const int64_t steps = tiles > 0 ? (int64_t)tiles * KB : 0;
+      for (int64_t step = buf; step < steps; step += 2) {
+        const uint32_t stage = (uint32_t)step % STAGES;
+        if (!tc::mbar_wait(tc::smem_u32(&ctl.tempty[buf]), ((uint32_t)(step >> 1) & 1) ^ 1, wc) ||
+            !tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), (uint32_t)(step / STAGES) & 1, wc))
+          break;
+        tc::fence_after_sync();
+        const uint64_t ad = a_base + stage * (A_BYTES >> 4), wd = w_base + stage * (W_BYTES >> 4);
         if (elected) {
-          const uint32_t fb = tc::smem_u32(&ctl.full[stage]);
-          const uint32_t wd = tc::smem_u32(sW + stage * W_BYTES);
-          tc::mbar_arrive_expect_tx(fb, A_BYTES + W_BYTES);
-          tc::tma_load_2d(tc::smem_u32(sA + stage * A_BYTES), &tmA, kb * BLOCK, t.row, fb);
-          tc::tma_load_2d_hint(wd, &tmW, kb * BLOCK, w0, fb, policy);
-          tc::tma_load_2d_hint(wd + W_BYTES / 2, &tmW, kb * BLOCK, w1, fb, policy);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f8(tmem_base + buf * TN, ad + 2 * k, wd + 2 * k, tc::idesc_e4m3_f32(TM, TN), k != 0);
+          tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
+          tc::mma_commit(tc::smem_u32(&ctl.tfull[buf]));
         }
         __syncwarp();
-        issued |= 1u << stage;
-        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
-      }
-    }
-    for (int s = 0; s < STAGES; ++s)
-      if ((issued >> s) & 1u)
-        tc::mbar_wait(tc::smem_u32(&ctl.full[s]), (issued_par >> s) & 1u, wdrain);
-    __syncwarp();
-   } else if (warp <= 2) {
-    // ================= MMA issuers: likewise, one for each accumulator =================
-    // (A step's two waits, four MMAs and two commits take one warp longer than the 512
-    // cycles that the MMAs do.)
-    const bool elected = tc::elect_one();
-    const uint32_t buf = warp - 1;
-    const uint64_t a_base = tc::desc_kmajor_sw128(tc::smem_u32(sA));
-    const uint64_t w_base = tc::desc_kmajor_sw128(tc::smem_u32(sW));
-    const int tiles = (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int64_t steps = tiles > 0 ? (int64_t)tiles * KB : 0;
-    for (int64_t step = buf; step < steps; step += 2) {
-      const uint32_t stage = (uint32_t)step % STAGES;
-      if (!tc::mbar_wait(tc::smem_u32(&ctl.tempty[buf]), ((uint32_t)(step >> 1) & 1) ^ 1, wc) ||
-          !tc::mbar_wait(tc::smem_u32(&ctl.full[stage]), (uint32_t)(step / STAGES) & 1, wc))
-        break;
-      tc::fence_after_sync();
-      const uint64_t ad = a_base + stage * (A_BYTES >> 4), wd = w_base + stage * (W_BYTES >> 4);
-      if (elected) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::mma_f8(tmem_base + buf * TN, ad + 2 * k, wd + 2 * k, tc::idesc_e4m3_f32(TM, TN), k != 0);
-        tc::mma_commit(tc::smem_u32(&ctl.empty[stage]));
-        tc::mma_commit(tc::smem_u32(&ctl.tfull[buf]));
       }
       __syncwarp();
-    }
-    __syncwarp();
-    if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
-      if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain[buf]));
-      tc::mbar_wait(tc::smem_u32(&ctl.drain[buf]), 0, wdrain);
-    }
-    __syncwarp();
-   } else {
-    // ================= scales: a lane has one block of every fourth row =================
-    const int j = lane & 7, r0 = lane >> 3;
-    const int wblk = p.Nw / BLOCK;
-    uint32_t n = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const Tile t = tile_at<TM>(ctl, E, tile);
-      // FC1: gate and up; FC2: neighbours (the last block twice where there is one)
-      const float* sw0 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? t.nb : 2 * t.nb)) * KB;
-      const float* sw1 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? wblk / 2 + t.nb : min(2 * t.nb + 1, wblk - 1))) * KB;
-      const float* sa = p.a_sf + (int64_t)t.row * KB;
-      for (int kb = 0; kb < KB; kb += SB, ++n) {
-        const uint32_t buf = n & 1;
-        const int k = min(kb + j, KB - 1);
-        const float w0 = __ldg(sw0 + k), w1 = __ldg(sw1 + k);
+      if (ctl.abort) {  // let every issued MMA finish before TMEM is freed
+        if (elected) tc::mma_commit(tc::smem_u32(&ctl.drain[buf]));
+        tc::mbar_wait(tc::smem_u32(&ctl.drain[buf]), 0, wdrain);
+      }
+      __syncwarp();
+    } else {
+      // ================= scales: a lane has one block of every fourth row =================
+      const int j = lane & 7, r0 = lane >> 3;
+      const int wblk = p.Nw / BLOCK;
+      uint32_t n = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        const Tile t = tile_at<TM>(ctl, E, tile);
+        // FC1: gate and up; FC2: neighbours (the last block twice where there is one)
+        const float* sw0 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? t.nb : 2 * t.nb)) * KB;
+        const float* sw1 = p.w_sf + ((int64_t)t.e * wblk + (SWIGLU ? wblk / 2 + t.nb : min(2 * t.nb + 1, wblk - 1))) * KB;
+        const float* sa = p.a_sf + (int64_t)t.row * KB;
+        for (int kb = 0; kb < KB; kb += SB, ++n) {
+          const uint32_t buf = n & 1;
+          const int k = min(kb + j, KB - 1);
+          const float w0 = __ldg(sw0 + k), w1 = __ldg(sw1 + k);
 #pragma unroll 1
-        for (int r = r0; r < TM; r += 64) {
-          float a[16];
+          for (int r = r0; r < TM; r += 64) {
+            float a[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)  // (a row behind the expert's takes its last row's, which go nowhere)
-            a[i] = __ldg(sa + (int64_t)min(r + 4 * i, t.rows - 1) * KB + k);
-          if (r == r0 && !tc::mbar_wait(tc::smem_u32(&ctl.sempty[buf]), ((n >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+            for (int i = 0; i < 16; ++i)  // (a row behind the expert's takes its last row's, which go nowhere)
+              a[i] = __ldg(sa + (int64_t)min(r + 4 * i, t.rows - 1) * KB + k);
+            if (r == r0 && !tc::mbar_wait(tc::smem_u32(&ctl.sempty[buf]), ((n >> 1) & 1) ^ 1, wc)) { ok = false; break; }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ctl.scale[buf][j][r + 4 * i] = make_float2(a[i] * w0, a[i] * w1);
+            for (int i = 0; i < 16; ++i) ctl.scale[buf][j][r + 4 * i] = make_float2(a[i] * w0, a[i] * w1);
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sfull[buf]));
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ctl.sfull[buf]));
       }
     }
-   }
   } else {
     tc::regs_inc<kRegsJoin>();
     // ================= joining and epilogue (warps 4..11) =================
@@ -409,7 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // and of the up rows) of at most 16 tokens, a stage 128 weight rows x 256 columns of K
 // (256 consecutive bytes a row for the DRAM; FC1's stages take gate and up in turn).
 // A block's products are then 128 x 16, which four warps join in a few cycles, and
-// eight accumulators stand ready, so that no MMA waits for one.
+// eight accumulators stand ready, so that no MMA waits for one.  T = 13 of 64 experts,
+// 2048 -> 2 x 1024: 39 us (the kernel above 49; without evict-first weights 45), T = 1 of
+// 256, 2048 -> 7168: 28.7 (36.9; 32.8), both with 5 us of the event pair's own.  At 16
+// rows an expert on average it takes 0.78 to 1.08 times the other's time (8, 64 and 32
+// experts), at 32 rows 1.06 to 1.31 times.
 //   warp 0     TMA producer, 6 stages
 //   warp 1     TMEM owner and MMA issuer
 //   warp 2     scales: the products sa sw of each token and block, to shared memory

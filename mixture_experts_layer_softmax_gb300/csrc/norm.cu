@@ -6,6 +6,11 @@
 //   dv = r (g - n mean(g n)) + dsum,   dw = sum over the rows of dy n
 // (dsum: what arrives at v itself by the residual stream; x and res both get dv).
 // Sums are fp32 in a fixed order.
+//
+// Both directions are bound by HBM.  Forward of 8192 x 4096, bf16, all outputs: 44.4 us on
+// the device (303 MB, 6.8 TB/s).  Gradient of 4096 x 7168: 43 us and 5 for dw's sum
+// (235 MB); as blocks that load, add up and store row by row it took 152 us, with one
+// group of eight warps behind a ring of bulk copies 49 + 5.
 #include "fp8.cuh"
 #include "pdl.cuh"
 #include "tc_ptx.cuh"
