@@ -3,6 +3,7 @@
 // dy[t] is read once, each y_perm row once, each dy_perm row written once: bound by HBM.
 // The dot products are fp32 in a fixed order.
 #include "common.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 
@@ -17,6 +18,8 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : KMAX <= 8 ? 
   constexpr int V = Vec<T>::N, B = W > 4 ? 1 : 4 / W;
   __shared__ int64_t s_off[B][KMAX];
   __shared__ float s_w[B][KMAX], s_dot[B * W][KMAX];
+  pdl_wait();
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, b = warp / W, tx = threadIdx.x - b * (32 * W);
   const int64_t t = (int64_t)blockIdx.x * B + b, P = (int64_t)ntok * K;
   if (tx < KMAX) {
@@ -80,21 +83,22 @@ cudaError_t combine_bwd_t(const moe_config_t& c, const void* dy, const void* y_p
   // not a token for every SM twice over (100 tokens of 7168, top-8: 20.5 -> 12.3 us)
   const int nvec = c.h / Vec<T>::N;
 #define MOE_CB(KM, W)                                                                          \
-  combine_bwd_kernel<T, KM, W><<<(unsigned)ceil_div(c.T, W > 4 ? 1 : 4 / W), W > 4 ? 32 * W : 128, 0, s>>>( \
-      static_cast<const T*>(dy), static_cast<const T*>(y_perm), dst_row, w, c.T, c.K, c.h,     \
-      static_cast<T*>(dy_perm), dw, status)
+  return pdl_launch(combine_bwd_kernel<T, KM, W>,                                              \
+                    dim3((unsigned)ceil_div(c.T, W > 4 ? 1 : 4 / W)),                          \
+                    dim3(W > 4 ? 32 * W : 128), 0, s, static_cast<const T*>(dy),               \
+                    static_cast<const T*>(y_perm), dst_row, w, c.T, c.K, c.h,                  \
+                    static_cast<T*>(dy_perm), dw, status)
 #define MOE_CBW(KM)                                                                            \
   if (nvec < 128) MOE_CB(KM, 1);                                                               \
   else if (nvec < 256) MOE_CB(KM, 2);                                                          \
   else if (c.T > 2 * sms) MOE_CB(KM, 4);                                                       \
   else MOE_CB(KM, 16)
   if (c.K <= 2) { MOE_CBW(2); }
-  else if (c.K <= 4) { MOE_CBW(4); }
-  else if (c.K <= 8) { MOE_CBW(8); }
-  else { MOE_CBW(16); }
+  if (c.K <= 4) { MOE_CBW(4); }
+  if (c.K <= 8) { MOE_CBW(8); }
+  MOE_CBW(16);
 #undef MOE_CBW
 #undef MOE_CB
-  return cudaGetLastError();
 }
 
 }  // namespace

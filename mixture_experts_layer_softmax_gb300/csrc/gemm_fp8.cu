@@ -31,6 +31,7 @@
 // A tile of 128 x 128 (four accumulators) was slower (2.1 ms: the MMAs read A twice), and
 // so were 16 joining warps (2.1 ms).
 #include "fp8.cuh"
+#include "pdl.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -205,6 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), 512);
     tc::tmem_relinquish();
   }
+  pdl_wait();  // before here only the block's own state
+  pdl_trigger();
   load_tiles<TM>(ctl, p.offsets, E, p.P, nblk);
   tc::fence_before_sync();
   __syncthreads();
@@ -499,6 +502,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     tc::tmem_alloc(tc::smem_u32(&ctl.tmem_base), FBUFS * 2 * FT);
     tc::tmem_relinquish();
   }
+  pdl_wait();
+  pdl_trigger();
   load_tiles<FT>(ctl, p.offsets, E, p.P, nblk);
   tc::fence_before_sync();
   __syncthreads();
@@ -749,8 +754,7 @@ cudaError_t launch_fp8_product(bool swiglu, int P, const uint8_t* a, const float
   const size_t smem = few ? kFewSmem : kSmem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, threads, smem, s>>>(ma, mw, p);
-  return cudaGetLastError();
+  return pdl_launch(kern, dim3(grid), dim3(threads), smem, s, ma, mw, p);
 }
 
 }  // namespace moe

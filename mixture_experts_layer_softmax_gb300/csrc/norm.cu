@@ -90,6 +90,8 @@ __global__ void __launch_bounds__(NT)
                        int64_t rows, int h, T* sum, T* y, uint8_t* __restrict__ q,
                        float* __restrict__ sf, float* __restrict__ rstd) {
   __shared__ float slot[NT / 32];
+  pdl_wait();
+  pdl_trigger();
   const int nt = blockDim.x;
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const bool here = row < rows;
@@ -187,7 +189,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps + 32, 1)
   __shared__ uint64_t full[kBwdWarps][kRing], empty[kBwdWarps][kRing];
   __shared__ float slot[2][kBwdWarps];
   __shared__ int abort[kBwdWarps][2], quit;
-  pdl_trigger();  // (the second kernel waits for all of this one before it reads a part)
+  pdl_wait();
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int arrays = dsum ? 3 : 2;
   const float* s_w = w_shared ? reinterpret_cast<float*>(dyn) : w;
@@ -350,6 +353,8 @@ __global__ void __launch_bounds__(256)
                            const float* __restrict__ w, const T* dsum, int rows, int h, T* dx,
                            float* __restrict__ dw) {
   __shared__ float slot[8][33];
+  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x >= (unsigned)rows) {
     const int c = (blockIdx.x - rows) * 32 + lane;
@@ -463,6 +468,7 @@ __global__ void __launch_bounds__(512)
   __shared__ float s[16][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   pdl_wait();
+  pdl_trigger();
   float v = 0.f;
   if (c < h) {
 #pragma unroll 4
@@ -500,10 +506,9 @@ cudaError_t fwd_launch(int64_t rows, int h, int threads, const void* x, const vo
                        float* rstd, cudaStream_t s) {
   // short rows: several a block, up to 128 threads
   const int per = threads >= 128 ? 1 : 128 / threads;
-  rmsnorm_fwd_kernel<T, NV, NT><<<(unsigned)ceil_div(rows, per), dim3(threads, per), 0, s>>>(
-      static_cast<const T*>(x), static_cast<const T*>(res), w, eps, rows, h, static_cast<T*>(sum),
-      static_cast<T*>(y), q, sf, rstd);
-  return cudaGetLastError();
+  return pdl_launch(rmsnorm_fwd_kernel<T, NV, NT>, dim3((unsigned)ceil_div(rows, per)),
+                    dim3(threads, per), 0, s, static_cast<const T*>(x), static_cast<const T*>(res), w,
+                    eps, rows, h, static_cast<T*>(sum), static_cast<T*>(y), q, sf, rstd);
 }
 
 template <typename T>
@@ -535,9 +540,8 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
   const int most = sms < kMaxBlocks ? sms : kMaxBlocks;
   if (rows <= kFewRows && (!dw || (a != o && b != o))) {
     // (in place, dx would go where the blocks for dw still read)
-    rmsnorm_bwd_few_kernel<T><<<(unsigned)(rows + (dw ? ceil_div(h, 32) : 0)), 256, 0, s>>>(
-        a, b, rstd, w, d, (int)rows, h, o, dw);
-    return cudaGetLastError();
+    return pdl_launch(rmsnorm_bwd_few_kernel<T>, dim3((unsigned)(rows + (dw ? ceil_div(h, 32) : 0))),
+                      dim3(256), 0, s, a, b, rstd, w, d, (int)rows, h, o, dw);
   }
   int parts;
   if (h <= kBwdMaxCols) {
@@ -564,7 +568,9 @@ cudaError_t bwd_t(int64_t rows, int h, const void* dy, const void* sum, const fl
     const size_t smem = head + G * stages * stage;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 32 * kBwdWarps + 32, smem, s>>>(a, b, rstd, w, d, rows, h, W, G, R, stages, o, pt, status);
+    e = pdl_launch(kern, dim3(grid), dim3(32 * kBwdWarps + 32), smem, s, a, b, rstd, w, d, rows, h, W, G,
+                   R, stages, o, pt, status);
+    if (e != cudaSuccess) return e;
     parts = (int)grid;
   } else {
     const unsigned grid = (unsigned)(rows < most ? rows : most);

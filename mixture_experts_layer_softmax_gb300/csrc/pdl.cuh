@@ -1,4 +1,7 @@
-// Programmatic dependent launch within a call's own chain of kernels.
+// Programmatic dependent launch: within a call's own chain of kernels, and between the
+// calls that launch with it: their kernels wait at their start (every thread: a block
+// that ended without would let the next kernel pass the one before), touch no memory
+// before it, and let the next kernel come as soon as all their blocks have.
 #pragma once
 
 #include "common.cuh"

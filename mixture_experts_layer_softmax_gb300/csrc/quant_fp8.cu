@@ -24,6 +24,8 @@ template <int U>
 __global__ void __launch_bounds__(256)
     fp8_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t blocks,
                         uint8_t* __restrict__ q, float* __restrict__ sf) {
+  pdl_wait();
+  pdl_trigger();
   const int sub = threadIdx.x & 7;
   const int64_t b0 = (int64_t)blockIdx.x * (32 * U) + (threadIdx.x >> 3);
   uint4 u[U][2];
@@ -63,6 +65,8 @@ __global__ void __launch_bounds__(256)
                                 uint8_t* __restrict__ q_t, float* __restrict__ sf_t) {
   __shared__ uint32_t s_max[8];
   __shared__ __align__(16) uint32_t s_q[BLOCK][32];
+  pdl_wait();
+  pdl_trigger();
   const int NB = N / BLOCK, KB = K / BLOCK;
   const int kb = blockIdx.x % KB, gn = blockIdx.x / KB;
   const int nb = gn % NB;
@@ -144,6 +148,7 @@ __global__ void __launch_bounds__(256)
     if (v0 + i * 32 < nvec) u[i] = __ldcs(src + v0 + i * 32);
   float s0 = blockIdx.y == 0 && lane < KB ? __ldg(x_sf + t * KB + lane) : 0.f;
   pdl_wait();
+  pdl_trigger();
   int64_t row[KMAX];
 #pragma unroll
   for (int k = 0; k < KMAX; ++k) {
@@ -181,18 +186,17 @@ cudaError_t launch_fp8_quantize(int64_t rows, int K, const void* x, uint8_t* q, 
   const __nv_bfloat16* xs = static_cast<const __nv_bfloat16*>(x);
   // four blocks a thread while that leaves every SM four blocks of threads
   if (blocks >= 32LL * 4 * 4 * sms)
-    fp8_quantize_kernel<4><<<(unsigned)ceil_div(blocks, 128), 256, 0, s>>>(xs, blocks, q, sf);
-  else
-    fp8_quantize_kernel<1><<<(unsigned)ceil_div(blocks, 32), 256, 0, s>>>(xs, blocks, q, sf);
-  return cudaGetLastError();
+    return pdl_launch(fp8_quantize_kernel<4>, dim3((unsigned)ceil_div(blocks, 128)), dim3(256), 0, s, xs,
+                      blocks, q, sf);
+  return pdl_launch(fp8_quantize_kernel<1>, dim3((unsigned)ceil_div(blocks, 32)), dim3(256), 0, s, xs,
+                    blocks, q, sf);
 }
 
 cudaError_t launch_fp8_quantize_weights(int groups, int N, int K, const void* w, uint8_t* q,
                                         float* sf, uint8_t* q_t, float* sf_t, cudaStream_t s) {
   const unsigned grid = (unsigned)((int64_t)groups * (N / BLOCK) * (K / BLOCK));
-  fp8_quantize_weights_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(w), N, K, q,
-                                                   sf, q_t, sf_t);
-  return cudaGetLastError();
+  return pdl_launch(fp8_quantize_weights_kernel, dim3(grid), dim3(256), 0, s,
+                    static_cast<const __nv_bfloat16*>(w), N, K, q, sf, q_t, sf_t);
 }
 
 cudaError_t launch_fp8_scatter(const moe_config_t& c, const uint8_t* x_q, const float* x_sf,

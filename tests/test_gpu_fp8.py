@@ -558,3 +558,60 @@ def test_large_offsets_of_bytes():
     cws = torch.empty(M.moe_workspace_size(M.make_config(T, h, 1, 1, 8)), dtype=torch.uint8, device="cuda")
     M.moe_permute_fp8(M.make_config(T, h, 1, 1, 8), q, sf, idx, None, rq, torch.empty_like(sf), ws=cws, **_maps(M, T, 1, 1))
     assert M.moe_get_error() == M.MOE_OK and torch.equal(rq[-300:], q[-300:]) and torch.equal(rq[:300], q[:300])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_behind_copies_and_other_streams(captured):
+    """Calls that follow a copy, a fill and another stream's work (eager and in a graph), each
+    reading what those wrote and overwriting what the one before read, many times over."""
+    M = lib()
+    rows, h, n = 700, 1024, 6
+    g = torch.Generator(device="cuda").manual_seed(81)
+    src = [torch.randn(rows, h, device="cuda", generator=g).bfloat16() for _ in range(n)]
+    dst = torch.arange(rows, dtype=torch.int32, device="cuda").flip(0).view(rows, 1).contiguous()
+    cfg = M.make_config(rows, h, 1, 1, 8)
+    wt = torch.ones(h, device="cuda")
+    x, y, z, res = (torch.zeros(rows, h, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    q, sf = u8(rows, h), f32(rows, h // 128)
+    outs = [torch.zeros(rows, h, dtype=torch.bfloat16, device="cuda") for _ in range(n)]
+    codes = [u8(rows, h) for _ in range(n)]
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        for i in range(n):
+            x.copy_(src[i])                                     # a copy, then a call that reads it
+            M.moe_fp8_quantize(rows, h, x, q, sf)
+            fork, join = torch.cuda.Event(), torch.cuda.Event()
+            fork.record(main)
+            other.wait_event(fork)
+            with torch.cuda.stream(other):                      # another stream writes the residual
+                res.copy_(src[(i + 1) % n])
+                join.record(other)
+            main.wait_event(join)
+            M.moe_rmsnorm_fwd(rows, h, M.MOE_BF16, x, res, wt, 1e-6, x, y, q, sf)
+            M.moe_unpermute_combine_bwd(cfg, y, None, dst, None, z)
+            M.moe_unpermute_combine_bwd(cfg, z, None, dst, None, y)
+            codes[i].copy_(q)
+            outs[i].copy_(y)
+            y.zero_()
+
+    with torch.cuda.stream(main):
+        if captured:
+            work()
+            main.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                work()
+            for t in outs + codes:
+                t.zero_()
+            for _ in range(3):
+                graph.replay()
+        else:
+            work()
+    torch.cuda.synchronize()
+    assert M.moe_get_error() == M.MOE_OK
+    for i in range(n):
+        v, yw, qw, sw = src[i].clone(), torch.empty_like(x), u8(rows, h), f32(rows, h // 128)
+        M.moe_rmsnorm_fwd(rows, h, M.MOE_BF16, v, src[(i + 1) % n], wt, 1e-6, None, yw, qw, sw)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], yw) and torch.equal(codes[i], qw), i
