@@ -615,3 +615,57 @@ def test_calls_behind_copies_and_other_streams(captured):
         M.moe_rmsnorm_fwd(rows, h, M.MOE_BF16, v, src[(i + 1) % n], wt, 1e-6, None, yw, qw, sw)
         torch.cuda.synchronize()
         assert torch.equal(outs[i], yw) and torch.equal(codes[i], qw), i
+
+
+@pytest.mark.parametrize("T,K", [(200, 2), (5, 2)])
+def test_outputs_aligned_to_16_bytes_only(T, K):
+    """Outputs on 16-byte boundaries that are not 32-byte ones: the same bits, nothing beside them."""
+    M = lib()
+    c = _case(91, T, K, 4, 384, 256)
+    save, a, aq, asf, y = _check_products(M, c)
+    P, E, h, F = c["P"], c["E"], c["h"], c["F"]
+    cfg = M.make_config(T, h, E, K, F)
+    od = torch.from_numpy(c["offsets"].astype(np.int32)).cuda()
+    xq, xsf = quantize_dev(M, c["x"])
+    w1q, w1sf = weights_dev(M, c["w1"], E)
+    w2q, w2sf = weights_dev(M, c["w2"], E)
+
+    def odd(like, skip):
+        buf = torch.full((like.numel() + 64,), 7, dtype=like.dtype, device="cuda")
+        view = buf[skip:skip + like.numel()].view(like.shape)
+        assert view.data_ptr() % 32 == 16
+        return buf, view
+
+    bufs = {n: odd(t, 16 // t.element_size()) for n, t in dict(save=save, a=a, aq=aq, asf=asf, y=y).items()}
+    v = {n: b[1] for n, b in bufs.items()}
+    M.moe_expert_fc1_fp8(cfg, xq, xsf, od, torch.from_numpy(c["p"]).cuda(), w1q, w1sf, v["save"], v["a"], v["aq"], v["asf"])
+    M.moe_expert_fc2_fp8(cfg, v["aq"], v["asf"], od, w2q, w2sf, v["y"])
+    assert M.moe_get_error() == M.MOE_OK
+    for n, want in dict(save=save, a=a, aq=aq, asf=asf, y=y).items():
+        assert torch.equal(v[n], want), n
+        skip = 16 // want.element_size()
+        assert torch.all(bufs[n][0][:skip] == 7) and torch.all(bufs[n][0][skip + want.numel():] == 7)
+
+
+@pytest.mark.parametrize("T,E", [(200, 8), (5000, 64)])
+def test_permute_fp8_from_the_routers_histograms(T, E):
+    """With MOE_FLAG_HIST_FROM_ROUTER the maps start from what the router left in the workspace."""
+    M = lib()
+    h, K = 256, 2
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, h, device="cuda", generator=g).bfloat16()
+    w_r = torch.randn(E, h, device="cuda", generator=g) * 0.05
+    q, sf = u8(T, h), f32(T, h // 128)
+    got = []
+    for flags in (M.MOE_FLAG_RENORM, M.MOE_FLAG_RENORM | M.MOE_FLAG_HIST_FROM_ROUTER):
+        cfg = M.make_config(T, h, E, K, 128, flags=flags)
+        ws = torch.empty(M.moe_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        idx, prob = torch.empty(T, K, dtype=torch.int32, device="cuda"), f32(T, K)
+        M.moe_fp8_quantize(T, h, x, q, sf)
+        M.moe_router_topk(cfg, x, w_r, None, None, None, idx, prob, ws=ws)
+        m, pq, psf = _maps(M, T, E, K), u8(T * K, h), f32(T * K, h // 128)
+        M.moe_permute_fp8(cfg, q, sf, idx, prob, pq, psf, ws=ws, **m)
+        got.append([idx, prob, pq, psf, *m.values()])
+    assert M.moe_get_error() == M.MOE_OK
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
