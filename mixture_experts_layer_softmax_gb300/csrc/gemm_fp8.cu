@@ -20,18 +20,19 @@
 // Every wait is bounded; one that gives up records MOE_ERR_TIMEOUT and every role
 // leaves its loop.
 //
-// What bounds it, by leaving parts of the work out, for FC1 of 16384 rows, 8 experts,
-// 4096 -> 2 x 14336 (then 1552 us, now 1515: 2.54 PFLOP/s; 1005 us at twice the measured
-// bf16 rate):
-// the stages' copies alone 1100 us (48 KB a 512-cycle step, 75 bytes a clock and SM), the
-// MMAs and the hand-over 944, the joining alone 1190 (a packed FMA takes an SM quarter
-// 2.3 to 3 cycles, a TMEM load of 16 columns its latency), all but SiLU and stores 1444.
+// FC1 of 16384 rows, 8 experts, 4096 -> 2 x 14336: 1515 us, 2.54 PFLOP/s (1005 us at
+// twice the measured bf16 rate).  What bounds it, by leaving parts of the work out when
+// it took 1552: the stages' copies alone 1100 us (48 KB a 512-cycle step, 75 bytes a clock
+// and SM), the MMAs and the hand-over 944, the joining alone 1190 (a packed FMA takes an
+// SM quarter 2.3 to 3 cycles, a TMEM load of 16 columns its latency), all but SiLU and
+// stores 1444.
 // Steps: 4.0 ms with the joining's registers capped at 168 a thread (spills), 2.2 ms with
 // a register split, 1.78 with 16-column loads and intrinsics for the packed FMA (half the
 // moves), 1.65 with the scales in a warp of their own, 1.57 with 32-byte stores, 1.55 with
 // two MMA issuers, 1.515 with the joining loop unrolled twice.
-// A tile of 128 x 128 (four accumulators) was slower (2.1 ms: the MMAs read A twice), and
-// so were 16 joining warps (2.1 ms).
+// Slower were a tile of 128 x 128 (four accumulators, 2.1 ms: the MMAs read A twice), 16
+// joining warps (2.1 ms), and rows exchanged between four lanes so that a store covers 8
+// rows x 128 bytes instead of 32 x 32 (1.62 ms: the exchange costs more than the lines).
 #include "fp8.cuh"
 #include "pdl.cuh"
 #include "tc_ptx.cuh"

@@ -429,9 +429,9 @@ cudaError_t launch_permute_maps(const moe_config_t& c, const int32_t* idx, const
   cudaError_t e = pdl_launch(chunk_scan_kernel, dim3((unsigned)ceil_div(c.E, 32)), dim3(1024), 0, s,
                              (const int32_t*)hist, NC, c.E, c.capacity, base, counts);
   if (e != cudaSuccess) return e;
-  return pdl_launch(chunk_ranks_kernel, dim3(blocks), dim3(256), 8 * c.E * sizeof(uint32_t), s, idx, prob, c.T, c.K, c.E,
-                    c.capacity, NC, (const int32_t*)base, (const int32_t*)counts, offsets, dst_row,
-                    src_token, perm_prob, status);
+  return pdl_launch(chunk_ranks_kernel, dim3(blocks), dim3(256), 8 * c.E * sizeof(uint32_t), s, idx,
+                    prob, c.T, c.K, c.E, c.capacity, NC, (const int32_t*)base,
+                    (const int32_t*)counts, offsets, dst_row, src_token, perm_prob, status);
 }
 
 int scatter_grid(int ntok, int sms) {
