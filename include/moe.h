@@ -455,11 +455,13 @@ moe_status_t moe_unpermute_combine(const moe_config_t* cfg, const void* y_perm,
 /* Gradient of the combine (the weights' and the rows'; dshared_y is dy itself):
  *   dy_perm[dst_row[t,k]] = w[t,k] dy[t],  dprob[t,k] = <dy[t], y_perm[dst_row[t,k]]>
  * with w = topk_prob, or 1 when it is NULL; slots with dst_row -1 get dprob 0, rows
- * of y_perm that no slot names are left as they were in dy_perm.
+ * of y_perm that no slot names are left as they were in dy_perm.  Slots of one token
+ * that share a row (moe_permute's, of a token that names an expert twice) add their
+ * weights there; no row is two tokens'.
  *   dy [T,h]; y_perm [P,h] and dprob [T,K] f32 (both or neither); dst_row [T,K];
  *   dy_perm [P,h] out (not y_perm's buffer).
  * The gradient of the dispatch, dx[t] = sum_k dx_perm[dst_row[t,k]], is
- * moe_unpermute_combine without weights. */
+ * moe_unpermute_combine without weights (for tokens whose rows are all different). */
 moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,
                                        const void* y_perm, const int32_t* dst_row,
                                        const float* topk_prob, void* dy_perm, float* dprob,

@@ -1,5 +1,7 @@
 // Gradient of the combine y[t] = sum_k w[t,k] y_perm[dst_row[t,k]]:
 //   dy_perm[dst_row[t,k]] = w[t,k] dy[t],   dw[t,k] = <dy[t], y_perm[dst_row[t,k]]>
+// (slots of a token that share a row, as a token that names an expert twice has them, add
+// their weights: the combine adds the row once for each).
 // dy[t] is read once, each y_perm row once, each dy_perm row written once: bound by HBM.
 // The dot products are fp32 in a fixed order.
 #include "common.cuh"
@@ -22,18 +24,32 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : KMAX <= 8 ? 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, b = warp / W, tx = threadIdx.x - b * (32 * W);
   const int64_t t = (int64_t)blockIdx.x * B + b, P = (int64_t)ntok * K;
-  if (tx < KMAX) {
+  if (tx < 32) {  // the token's first warp, a lane a slot
     const int k = tx;
-    int64_t off = -1;
+    int row = -2 - k;  // of no other slot
     if (k < K && t < ntok) {
       const int r = __ldg(dst_row + t * K + k);
       if (r >= 0 && r < P)
-        off = (int64_t)r * h;
+        row = r;
       else if (r != -1)
         report(status, MOE_ERR_DEVICE_BOUNDS);
     }
-    s_off[b][k] = off;
-    s_w[b][k] = off >= 0 && w ? __ldg(w + t * K + k) : 1.f;
+    float wk = row >= 0 && w ? __ldg(w + t * K + k) : 1.f;
+    // every slot of a shared row gets the sum, and so writes the same values
+    const unsigned same = __match_any_sync(0xffffffffu, row);
+    if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wk, j);
+        if ((same >> j) & 1u) sum += wj;
+      }
+      wk = sum;
+    }
+    if (k < KMAX) {
+      s_off[b][k] = row >= 0 ? (int64_t)row * h : -1;
+      s_w[b][k] = wk;
+    }
   }
   __syncthreads();
   float dot[KMAX] = {};
