@@ -416,9 +416,10 @@ cudaError_t launch_permute_maps(const moe_config_t& c, const int32_t* idx, const
     return e;
   }
   const int blocks = (int)ceil_div(NC, 8);
-  if (!hist_ready)
-    chunk_hist_kernel<<<blocks, 256, 8 * c.E * sizeof(int32_t), s>>>(idx, c.T, c.K, c.E, NC, hist,
-                                                                    status);
+  if (!hist_ready) {
+    const cudaError_t e = launch_chunk_hist(c, idx, hist, status, s);
+    if (e != cudaSuccess) return e;
+  }
   if ((int64_t)NC * c.E <= kScanInBlock) {
     const size_t bytes = sizeof(int32_t) * ((size_t)NC * c.E + 2 * c.E + 1 + 8 * c.E);
     return pdl_launch(chunk_scan_ranks_kernel, dim3(blocks), dim3(256), bytes, s, idx, prob, c.T,
