@@ -1,7 +1,8 @@
 """Python binding of the C ABI in include/moe.h (ctypes; argument marshalling
 only).  Every function here has the C entry point's name and forwards torch
-tensors' device pointers and the current CUDA stream; all computation runs in
-the library's CUDA kernels.  There is no fallback: if the library has not been
+tensors' device pointers and the current CUDA stream (the calls of the FP8 layer
+path and its gradients check the tensors' element types first); all computation
+runs in the library's CUDA kernels.  There is no fallback: if the library has not been
 built (``mixture_experts_layer_softmax_gb300._build.build()``) importing this
 module raises.
 """
@@ -126,6 +127,40 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
+
+
+_dtypes = None  # fp32, bf16, int32, and the activations' types by moe_dtype_t
+
+
+def _types():
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        f32, bf16 = torch.float32, torch.bfloat16
+        _dtypes = f32, bf16, torch.int32, {MOE_F32: f32, MOE_BF16: bf16}
+    return _dtypes
+
+
+def _typed(t, dtype):
+    """_ptr of a tensor whose elements are `dtype` (None: the call refuses the type itself)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype and dtype is not None:
+        raise ValueError(f"expected a {dtype} tensor, not {t.dtype}")
+    if t.is_cuda and t.is_contiguous():  # (as _ptr, without its call: 0.1 us a tensor)
+        return t.data_ptr()
+    return _ptr(t)
+
+
+def _codes(t):
+    """_ptr of a tensor of one-byte elements."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype.itemsize != 1:
+        raise ValueError(f"expected a tensor of 8-bit codes, not {t.dtype}")
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t)
 
 
 def _stream(stream):
@@ -306,47 +341,57 @@ def moe_expert_fc2_mxfp4(cfg, a_q, a_sf, offsets, w2_q, w2_sf, y_perm, stream=No
 
 def moe_fp8_quantize(rows, K, x, q, sf, stream=None):
     """x [rows, K] bf16 -> E4M3 codes q [rows, K] and scales sf [rows, K/128]."""
+    f32, bf16, _, _ = _types()
     _check("moe_fp8_quantize", _lib.moe_fp8_quantize(
-        int(rows), int(K), _ptr(x), _ptr(q), _ptr(sf), _stream(stream)))
+        int(rows), int(K), _typed(x, bf16), _codes(q), _typed(sf, f32), _stream(stream)))
 
 
 def moe_fp8_quantize_weights(groups, N, K, w, q, sf, q_t=None, sf_t=None, stream=None):
     """w [groups, N, K] bf16 -> codes q and scales sf [groups, N/128, K/128] of its
     128 x 128 blocks and, if given, the transposed tensors q_t, sf_t."""
+    f32, bf16, _, _ = _types()
     _check("moe_fp8_quantize_weights", _lib.moe_fp8_quantize_weights(
-        int(groups), int(N), int(K), _ptr(w), _ptr(q), _ptr(sf), _ptr(q_t), _ptr(sf_t),
-        _stream(stream)))
+        int(groups), int(N), int(K), _typed(w, bf16), _codes(q), _typed(sf, f32), _codes(q_t),
+        _typed(sf_t, f32), _stream(stream)))
 
 
 def moe_permute_fp8(cfg, x_q, x_sf, topk_idx, topk_prob, xp_q, xp_sf, counts, offsets, dst_row,
                     src_token, perm_prob, ws, stream=None):
     """moe_permute of rows that are in FP8 already."""
+    f32, _, i32, _ = _types()
     wp, wb = _ws(ws)
     _check("moe_permute_fp8", _lib.moe_permute_fp8(
-        ctypes.byref(cfg), _ptr(x_q), _ptr(x_sf), _ptr(topk_idx), _ptr(topk_prob), _ptr(xp_q),
-        _ptr(xp_sf), _ptr(counts), _ptr(offsets), _ptr(dst_row), _ptr(src_token), _ptr(perm_prob),
+        ctypes.byref(cfg), _codes(x_q), _typed(x_sf, f32), _typed(topk_idx, i32),
+        _typed(topk_prob, f32), _codes(xp_q), _typed(xp_sf, f32), _typed(counts, i32),
+        _typed(offsets, i32), _typed(dst_row, i32), _typed(src_token, i32), _typed(perm_prob, f32),
         wp, wb, _stream(stream)))
 
 
 def moe_expert_fc1_fp8(cfg, x_q, x_sf, offsets, perm_prob, w1_q, w1_sf, act_save, a, a_q, a_sf,
                        stream=None):
+    f32, bf16, i32, _ = _types()
     _check("moe_expert_fc1_fp8", _lib.moe_expert_fc1_fp8(
-        ctypes.byref(cfg), _ptr(x_q), _ptr(x_sf), _ptr(offsets), _ptr(perm_prob), _ptr(w1_q),
-        _ptr(w1_sf), _ptr(act_save), _ptr(a), _ptr(a_q), _ptr(a_sf), _stream(stream)))
+        ctypes.byref(cfg), _codes(x_q), _typed(x_sf, f32), _typed(offsets, i32),
+        _typed(perm_prob, f32), _codes(w1_q), _typed(w1_sf, f32), _typed(act_save, bf16),
+        _typed(a, bf16), _codes(a_q), _typed(a_sf, f32), _stream(stream)))
 
 
 def moe_expert_fc2_fp8(cfg, a_q, a_sf, offsets, w2_q, w2_sf, y_perm, stream=None):
+    f32, bf16, i32, _ = _types()
     _check("moe_expert_fc2_fp8", _lib.moe_expert_fc2_fp8(
-        ctypes.byref(cfg), _ptr(a_q), _ptr(a_sf), _ptr(offsets), _ptr(w2_q), _ptr(w2_sf),
-        _ptr(y_perm), _stream(stream)))
+        ctypes.byref(cfg), _codes(a_q), _typed(a_sf, f32), _typed(offsets, i32), _codes(w2_q),
+        _typed(w2_sf, f32), _typed(y_perm, bf16), _stream(stream)))
 
 
 def moe_rmsnorm_fwd(rows, h, dtype, x, res, w, eps, sum=None, y=None, q=None, sf=None, rstd=None,
                     stream=None):
-    """y = RMS norm of x + res, in `dtype` and / or FP8; sum = x + res."""
+    """y = RMS norm of x + res, in `dtype` and / or FP8; sum = x + res; w is fp32."""
+    f32, _, _, acts = _types()
+    act = acts.get(dtype)
     _check("moe_rmsnorm_fwd", _lib.moe_rmsnorm_fwd(
-        int(rows), int(h), int(dtype), _ptr(x), _ptr(res), _ptr(w), float(eps), _ptr(sum), _ptr(y),
-        _ptr(q), _ptr(sf), _ptr(rstd), _stream(stream)))
+        int(rows), int(h), int(dtype), _typed(x, act), _typed(res, act), _typed(w, f32), float(eps),
+        _typed(sum, act), _typed(y, act), _codes(q), _typed(sf, f32), _typed(rstd, f32),
+        _stream(stream)))
 
 
 def moe_rmsnorm_bwd_workspace_size(rows, h) -> int:
@@ -354,10 +399,13 @@ def moe_rmsnorm_bwd_workspace_size(rows, h) -> int:
 
 
 def moe_rmsnorm_bwd(rows, h, dtype, dy, sum, rstd, w, dsum, dx, dw=None, ws=None, stream=None):
+    f32, _, _, acts = _types()
+    act = acts.get(dtype)
     wp, wb = _ws(ws)
     _check("moe_rmsnorm_bwd", _lib.moe_rmsnorm_bwd(
-        int(rows), int(h), int(dtype), _ptr(dy), _ptr(sum), _ptr(rstd), _ptr(w), _ptr(dsum),
-        _ptr(dx), _ptr(dw), wp, wb, _stream(stream)))
+        int(rows), int(h), int(dtype), _typed(dy, act), _typed(sum, act), _typed(rstd, f32),
+        _typed(w, f32), _typed(dsum, act), _typed(dx, act), _typed(dw, f32), wp, wb,
+        _stream(stream)))
 
 
 def moe_unpermute_combine(cfg, y_perm, dst_row, topk_prob, shared_y, y, stream=None):
@@ -368,9 +416,11 @@ def moe_unpermute_combine(cfg, y_perm, dst_row, topk_prob, shared_y, y, stream=N
 
 def moe_unpermute_combine_bwd(cfg, dy, y_perm, dst_row, topk_prob, dy_perm, dprob=None,
                               stream=None):
+    f32, _, i32, acts = _types()
+    act = acts.get(cfg.dtype)
     _check("moe_unpermute_combine_bwd", _lib.moe_unpermute_combine_bwd(
-        ctypes.byref(cfg), _ptr(dy), _ptr(y_perm), _ptr(dst_row), _ptr(topk_prob), _ptr(dy_perm),
-        _ptr(dprob), _stream(stream)))
+        ctypes.byref(cfg), _typed(dy, act), _typed(y_perm, act), _typed(dst_row, i32),
+        _typed(topk_prob, f32), _typed(dy_perm, act), _typed(dprob, f32), _stream(stream)))
 
 
 def moe_layer_fwd(cfg, x, w_r, gate_bias, sel_bias, w1, b1, w2, b2, w1_shared, w2_shared, y,
