@@ -459,7 +459,7 @@ moe_status_t moe_unpermute_combine(const moe_config_t* cfg, const void* y_perm,
  * that share a row (moe_permute's, of a token that names an expert twice) add their
  * weights there; no row is two tokens'.
  *   dy [T,h]; y_perm [P,h] and dprob [T,K] f32 (both or neither); dst_row [T,K];
- *   dy_perm [P,h] out (not y_perm's buffer).
+ *   dy_perm [P,h] out (not y_perm's buffer, and nowhere over dy).
  * The gradient of the dispatch, dx[t] = sum_k dx_perm[dst_row[t,k]], is
  * moe_unpermute_combine without weights (for tokens whose rows are all different). */
 moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,

@@ -167,6 +167,12 @@ const DeviceInfo* device_info(bool inject = true) {
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether the m bytes at a and the n bytes at b have any in common.
+bool overlap(const void* a, int64_t m, const void* b, int64_t n) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return m > 0 && n > 0 && p < q + n && q < p + m;
+}
+
 moe_status_t check_config(const moe_config_t* c) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->T < 0 || c->h < 1 || c->E < 1 || c->K < 1 || c->F < 1) return MOE_ERR_INVALID_ARG;
@@ -794,9 +800,13 @@ moe_status_t moe_unpermute_combine_bwd(const moe_config_t* cfg, const void* dy,
   if (cfg->T > 0 && (!dy || !dst_row || !dy_perm)) return MOE_ERR_INVALID_ARG;
   if (!y_perm != !dprob || (y_perm && y_perm == dy_perm)) return MOE_ERR_INVALID_ARG;
   if (!al16(dy) || !al16(y_perm) || !al16(dy_perm)) return MOE_ERR_INVALID_ARG;
-  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return MOE_OK;
+  // tokens' rows are written while others' are read
+  const int64_t dy_bytes = (int64_t)cfg->T * cfg->h * elem_bytes(cfg->dtype);
+  const bool apart = !overlap(dy, dy_bytes, dy_perm, dy_bytes * cfg->K);
+  if (cfg->flags & MOE_FLAG_VALIDATE_ONLY) return apart ? MOE_OK : MOE_ERR_INVALID_ARG;
   const DeviceInfo* d = device_info();
   if (!d) return MOE_ERR_CUDA;
+  if (!apart) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_combine_bwd(*cfg, dy, y_perm, dst_row, topk_prob, dy_perm, dprob,
                                         d->sms, d->status, static_cast<cudaStream_t>(stream)));
 }
