@@ -358,7 +358,9 @@ moe_status_t moe_expert_fc2_mxfp4(const moe_config_t* cfg, const uint8_t* a_q,
  * block (w_sf [N/128, K/128] per expert).  A block whose largest magnitude is m
  * has a = max(m, 448 2^-125), the scale a / 448 (fp32) and the codes
  * E4M3(448 x / a), to nearest even: of an infinity or a NaN, a NaN scale and NaN
- * codes.  A code stands for its E4M3 value times the block's scale.
+ * codes.  (Of bf16 values exactly; of the fp32 ones that the norm and FC1 quantise, a
+ * quotient within 2^-23 of the border of two codes may fall to either.)  A code stands
+ * for its E4M3 value times the block's scale.
  *
  * Errors: NULL or 16-byte-misaligned tensors -> MOE_ERR_INVALID_ARG; K, N or the
  * config's h / F not multiples of 128, act not SwiGLU, has_bias, fp32 dtype ->
@@ -390,7 +392,8 @@ moe_status_t moe_permute_fp8(const moe_config_t* cfg, const uint8_t* x_q, const 
                              moe_stream_t stream);
 
 /* FP8 FC1 with the SwiGLU epilogue: H = x_perm W1_e^T over the values that the codes
- * stand for (tensor-core products of 128 columns, joined in fp32), a[r] = p_r
+ * stand for (tensor-core products of 128 columns, joined in fp32 with the product of
+ * their two scales, which keeps fewer bits below 2^-126 and ends at 2^128), a[r] = p_r
  * silu(H[r, :F]) H[r, F:] (p_r = perm_prob[r], 1 when NULL).  Outputs, each optional
  * but one of a and a_q:  act_save [P,2F] bf16 (H: what moe_grouped_mlp_bwd reads),
  * a [P,F] bf16, a_q [P,F] + a_sf [P,F/128] (a in FP8, from fp32).

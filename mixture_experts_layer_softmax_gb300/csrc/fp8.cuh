@@ -44,7 +44,9 @@ MOE_D uint32_t codes2(float lo, float hi) {
 MOE_D uint32_t codes4(float a, float b, float c, float d) {
   return codes2(a, b) | (codes2(c, d) << 16);
 }
-// Eight fp32 values of a block -> eight codes.
+// Eight fp32 values of a block -> eight codes, by x times the rounded 448 / a: a quotient
+// within 2^-23 of a border of two codes may fall to either.  (The values are rounded sums;
+// what they are off themselves is as much.)
 MOE_D uint2 codes8(const float* v, float inv) {
   return make_uint2(codes4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                     codes4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));

@@ -20,9 +20,12 @@
 // Every wait is bounded; one that gives up records MOE_ERR_TIMEOUT and every role
 // leaves its loop.
 //
-// FC1 of 16384 rows, 8 experts, 4096 -> 2 x 14336: 1515 us, 2.54 PFLOP/s (1005 us at
-// twice the measured bf16 rate).  What bounds it, by leaving parts of the work out when
-// it took 1552: the stages' copies alone 1100 us (48 KB a 512-cycle step, 75 bytes a clock
+// FC1 of 16384 rows, 8 experts, 4096 -> 2 x 14336: 1515 us in a burst, 2.54 PFLOP/s (1005
+// us at twice the measured bf16 rate), 1.69 to 1.73 ms in a long run (1400 W); 8-bit a
+// instead of bf16 the same, with the pre-activation 1.63 and 1.84 ms.  Evaluating and
+// storing a tile takes a time of its own whatever K is: FC2 of 16384 rows to 4096 columns
+// 70, 93, 138 and 236 us at K = 512, 1024, 2048 and 4096.  What bounds the FC1, by leaving
+// parts of the work out when a burst took 1552: the stages' copies alone 1100 us (48 KB a 512-cycle step, 75 bytes a clock
 // and SM), the MMAs and the hand-over 944, the joining alone 1190 (a packed FMA takes an
 // SM quarter 2.3 to 3 cycles, a TMEM load of 16 columns its latency), all but SiLU and
 // stores 1444.
@@ -427,10 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // (256 consecutive bytes a row for the DRAM; FC1's stages take gate and up in turn).
 // A block's products are then 128 x 16, which four warps join in a few cycles, and
 // eight accumulators stand ready, so that no MMA waits for one.  T = 13 of 64 experts,
-// 2048 -> 2 x 1024: 39 us (the kernel above 49; without evict-first weights 45), T = 1 of
-// 256, 2048 -> 7168: 28.7 (36.9; 32.8), both with 5 us of the event pair's own.  At 16
-// rows an expert on average it takes 0.78 to 1.08 times the other's time (8, 64 and 32
-// experts), at 32 rows 1.06 to 1.31 times.
+// 2048 -> 2 x 1024: 32 us among other calls, T = 1 of 256, 2048 -> 7168: 21.6.  By itself,
+// with 5 us of the event pair's own and without dependent launches, 39 (the kernel above
+// 49; without evict-first weights 45) and 28.7 (36.9; 32.8).  At 16 rows an expert on
+// average it takes 0.78 to 1.08 times the other's time (8, 64 and 32 experts), at 32 rows
+// 1.06 to 1.31 times.  The choice knows the average alone: rows that all go to a few of
+// many experts read those experts' weights again (from the L2) for every 16 of them, 4096
+// rows on 64 of 256 experts 508 us against the other kernel's 311, on one 506 against 107.
 //   warp 0     TMA producer, 6 stages
 //   warp 1     TMEM owner and MMA issuer
 //   warp 2     scales: the products sa sw of each token and block, to shared memory
