@@ -25,10 +25,10 @@
 // instead of bf16 the same, with the pre-activation 1.63 and 1.84 ms.  Evaluating and
 // storing a tile takes a time of its own whatever K is: FC2 of 16384 rows to 4096 columns
 // 70, 93, 138 and 236 us at K = 512, 1024, 2048 and 4096.  What bounds the FC1, by leaving
-// parts of the work out when a burst took 1552: the stages' copies alone 1100 us (48 KB a 512-cycle step, 75 bytes a clock
-// and SM), the MMAs and the hand-over 944, the joining alone 1190 (a packed FMA takes an
-// SM quarter 2.3 to 3 cycles, a TMEM load of 16 columns its latency), all but SiLU and
-// stores 1444.
+// parts of the work out when a burst took 1552: the stages' copies alone 1100 us (48 KB a
+// 512-cycle step, 75 bytes a clock and SM), the MMAs and the hand-over 944, the joining
+// alone 1190 (a packed FMA takes an SM quarter 2.3 to 3 cycles, a TMEM load of 16 columns
+// its latency), all but SiLU and stores 1444.
 // Steps: 4.0 ms with the joining's registers capped at 168 a thread (spills), 2.2 ms with
 // a register split, 1.78 with 16-column loads and intrinsics for the packed FMA (half the
 // moves), 1.65 with the scales in a warp of their own, 1.57 with 32-byte stores, 1.55 with

@@ -173,7 +173,12 @@ MOE_D void ranks_chunk(int c, int lane, uint32_t* my, const int32_t* __restrict_
     __syncwarp();
     if (e >= 0 && lane == __ffs(same) - 1) my[e] += __popc(same);
     __syncwarp();
-    if (in) place_pair(ti, k, e, pos, T, K, cap, prob, s_off, dst_row, src_token, perm_prob, status);
+    // (of a token's slots that share the row, the last one's probability stays)
+    const unsigned token = ((1u << K) - 1u) << (g * K);
+    const bool last = ((same & token) >> lane) == 1u;
+    if (in)
+      place_pair(ti, k, e, pos, T, K, cap, prob, s_off, dst_row, src_token, last ? perm_prob : nullptr,
+                 status);
   }
 }
 

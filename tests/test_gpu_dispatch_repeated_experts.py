@@ -30,10 +30,11 @@ class Maps:
         self.ws = torch.empty(M.moe_workspace_size(self.cfg), dtype=torch.uint8, device="cuda")
         self.counts, self.offsets, self.dst = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T, K, **i32)
         self.src = torch.full((T * K,), -7, **i32)
+        self.prob, self.perm_prob = torch.rand(T, K, device="cuda"), torch.full((T * K,), -1.0, device="cuda")
 
     def run(self):
-        self.M.moe_permute(self.cfg, None, self.idx, None, None, self.counts, self.offsets, self.dst, self.src, None,
-                           self.ws)
+        self.M.moe_permute(self.cfg, None, self.idx, self.prob, None, self.counts, self.offsets, self.dst, self.src,
+                           self.perm_prob, self.ws)
 
 
 @pytest.mark.parametrize("T,E,K,cap", [(5000, 256, 8, 0), (1000, 8, 4, 0), (40000, 64, 16, 0), (6000, 128, 6, 100),
@@ -58,6 +59,10 @@ def test_maps(T, E, K, cap):
     ok = dst >= 0
     src[dst[ok]] = np.repeat(np.arange(T), K).reshape(T, K)[ok]
     np.testing.assert_array_equal(m.src.cpu().numpy(), src)
+    pp, prob = np.full(T * K, -1.0, np.float32), m.prob.cpu().numpy()
+    for k in range(K):                                          # of a row's slots the last one's
+        pp[dst[ok[:, k], k]] = prob[ok[:, k], k]
+    np.testing.assert_array_equal(m.perm_prob.cpu().numpy(), pp)
 
 
 def test_time_beside_a_table_without_repeats():
